@@ -297,6 +297,152 @@ axon_status axon_ssd_scan(const axon_ssd_shape* shape, const axon_ssd_params* pa
                           const float* state_in, void* y, float* state_out, void* workspace,
                           size_t workspace_bytes, void* stream);
 
+/* ---- Packed sequences ------------------------------------------------------------------------
+ * Requests of unequal length are packed one behind the other in one buffer of total_tokens rows.
+ * axon_sequence_tables builds, on the GPU from the request lengths alone, where each sequence and
+ * each block of `block` tokens begins. One int32 array `tables` holds, in this order,
+ *   starts       (sequences + 1): starts[n] = min(total_tokens, sum of max(lengths, 0) before n)
+ *   block_starts (sequences + 1): blocks of the sequences before n; the last entry is their number
+ *   block_seq    (rows): the sequence of each block, -1 behind the last block
+ *   block_first  (rows): its first packed token, -1 behind the last block
+ * with rows = total_tokens / block + sequences, an upper bound of the number of blocks for any
+ * lengths, so that neither a host nor a captured graph has to know the lengths. A sequence's last
+ * block may be short; blocks never span two sequences. Lengths below zero count as zero; what goes
+ * past total_tokens is cut off there.
+ * Limits: sequences in [1, 65535], block >= 1, total_tokens in [0, 2^31), rows < 2^31 (else
+ * AXON_ERR_INVALID_ARGUMENT below and AXON_ERR_UNSUPPORTED above them). lengths and tables are
+ * device arrays, 4-byte aligned, that must not overlap. */
+
+/* Number of int32 elements of `tables` (0 for invalid arguments). */
+size_t axon_sequence_tables_count(int64_t sequences, int64_t total_tokens, int64_t block);
+
+axon_status axon_sequence_tables(int64_t sequences, int64_t total_tokens, int64_t block,
+                                 const int32_t* lengths, int32_t* tables, void* stream);
+
+/* ---- Gated delta rule ------------------------------------------------------------------------
+ * The scalar-decay recurrence of the SSD core with the delta rule's write: what the state already
+ * answers for a key is taken off before the value is written. For every sequence and value head h
+ * (key head h / (value_heads / key_heads)) with a state S[v, k] (V x K), per token:
+ *
+ *   dt    = min(max(softplus(dt_raw[h] + dt_bias[h]), dt_min), dt_max),  A = -exp(A_log[h])
+ *   beta  = sigmoid(beta_raw[h])
+ *   k^    = k / sqrt(sum k^2 + eps),   q^ = q / sqrt(sum q^2 + eps)
+ *   S    <- exp(dt A) S
+ *   S    <- S + beta (v - S k^) k^T
+ *   y     = scale S q^
+ *
+ * The step size and decay are those of axon_ssd_scan; the convolution, gate, norm and projections
+ * of the block are the caller's (axon_group_norm is the norm). axon_gated_delta_scan runs chunks of
+ * 64 tokens on the matrix cores: with g the inclusive sum of dt A inside the chunk and S0 the
+ * entering state, D = T (v - e^g S0 k^), T = (I + M)^-1 diag(beta), M[t,s] = beta_t e^(g_t - g_s)
+ * k^_t.k^_s for s < t, are the chunk's corrected writes. axon_gated_delta_step is the recurrence
+ * itself for one token a row. All sums, decays and states are fp32.
+ *
+ * Layouts: q, k (tokens, key_heads, K); v (tokens, value_heads, V); dt_raw, beta_raw
+ * (tokens, value_heads); y (tokens, value_heads, V); activation dtype. The rows of q, k and v may
+ * lie q_stride, k_stride, v_stride elements apart (parts of one projection's output; 0 = dense;
+ * else a multiple of 8 elements, at least the row's own length); everything else is contiguous.
+ *   A_log, dt_bias (value_heads) fp32;  pools of states (slots, value_heads, V, K) fp32.
+ * Supported: K 64 or 128; V a multiple of 16 up to 256; value_heads a multiple of key_heads (else
+ * AXON_ERR_UNSUPPORTED); sequences and heads in [1, 65535]; sequences * value_heads < 2^20;
+ * tokens < 2^29; tokens * heads * dim and slots * value_heads * V * K <= 2^40. Device pointers 16-byte aligned, integer arrays 4-byte.
+ *
+ * Slots: sequence (or row) n uses state slots[n] of the pool, or state n where slots is NULL (the
+ * pool then holds at least `sequences` states). A slot outside the pool means no state: a scan starts from
+ * zeros (in_slots) or does not store the final state (out_slots), a step leaves the row's y as it
+ * was and touches no state. The slots of one call that are written must be distinct, and no
+ * sequence may read a slot that another one writes; else those states and outputs are
+ * unspecified (no other memory is touched).
+ *
+ * A value that is not finite in a token makes the outputs of its head in the whole 64-token chunk
+ * and after it unspecified (a step: of its row and head); no other sequence or head sees it. */
+typedef struct {
+  int64_t sequences;    /* batch rows, or packed sequences */
+  int64_t tokens;       /* rows of q, k, v: sequences * seqlen, or the packed buffer's rows */
+  int64_t key_heads;
+  int64_t value_heads;
+  int64_t key_dim;      /* K */
+  int64_t value_dim;    /* V */
+  int64_t q_stride;     /* elements between the rows of q, k, v; 0 = dense */
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t state_slots;  /* states of the pool state_in (of the step's pool) */
+  int64_t out_slots;    /* states of the pool state_out; equal to state_slots in place; not read by
+                           the step */
+  int32_t act_dtype;    /* an axon_dtype value */
+} axon_gated_delta_shape;
+
+typedef struct {
+  const float* A_log;    /* (value_heads) */
+  const float* dt_bias;  /* (value_heads) */
+  float dt_min;          /* as for axon_ssd_scan */
+  float dt_max;
+  float scale;           /* of the readout, finite; K^-0.5 is usual */
+  float eps;             /* of the norms of q and k, finite and > 0 */
+} axon_gated_delta_params;
+
+/* Bytes of device workspace axon_gated_delta_scan needs (0 for an invalid shape or tokens == 0). */
+size_t axon_gated_delta_scan_workspace_bytes(const axon_gated_delta_shape* shape);
+
+/* Runs every sequence. tables: NULL for a uniform batch (tokens must be a multiple of sequences),
+ * else the packed sequences' tables of axon_sequence_tables for these sequences, these tokens as
+ * total_tokens and block 64 (other contents give unspecified results, but no access outside the
+ * arrays). Rows of y behind the last sequence are left as they were. state_in NULL: zeros.
+ * state_out NULL: the final states are not stored. state_out may equal state_in but must not
+ * overlap it otherwise; y and state_out overlap nothing else. A sequence without tokens copies its
+ * state. Running L1 tokens then L2 from the returned state equals running L1 + L2 up to rounding.
+ * workspace: device memory, 16-byte aligned, no initialisation needed; two calls that may overlap
+ * in time need one each. */
+axon_status axon_gated_delta_scan(const axon_gated_delta_shape* shape,
+                                  const axon_gated_delta_params* params, const void* q,
+                                  const void* k, const void* v, const void* dt_raw,
+                                  const void* beta_raw, const int32_t* tables,
+                                  const float* state_in, const int32_t* in_slots, void* y,
+                                  float* state_out, const int32_t* out_slots, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* One token for each of `sequences` rows (tokens == sequences), states updated in place. */
+axon_status axon_gated_delta_step(const axon_gated_delta_shape* shape,
+                                  const axon_gated_delta_params* params, const void* q,
+                                  const void* k, const void* v, const void* dt_raw,
+                                  const void* beta_raw, float* state, const int32_t* slots,
+                                  void* y, void* stream);
+
+/* ---- Group norm ------------------------------------------------------------------------------
+ * The normalisation behind a scan, channels last, with its activation and gate in one pass. Every
+ * row of x (rows, groups * width) is one token; every group of `width` channels has statistics of
+ * its own (over time as well they would see the future of a causal layer):
+ *
+ *   u = x, or x SiLU(z)                                      (gate AXON_GATE_BEFORE)
+ *   n = (u - mean(u)) / sqrt(var(u) + eps)    centered;  u / sqrt(mean(u^2) + eps)    otherwise
+ *   y = n weight + bias;   y = SiLU(y) (activation AXON_ACT_SILU);   y = y SiLU(z) (AXON_GATE_AFTER)
+ *
+ * x, z, y: activation dtype, rows x_stride / z_stride elements apart (0 = dense; else at least
+ * groups * width, any alignment of an element); y dense, fp32 statistics, rounded once. weight and
+ * bias: fp32, (groups * width), or (width) where shared_weights is set; either may be NULL (ones,
+ * zeros). y may equal x where x is dense; else y overlaps nothing. rows >= 0; groups, width >= 1;
+ * groups * width <= 2^30; rows * groups < 2^31; rows * groups * width <= 2^40. x, z, y and the
+ * parameters need the alignment of an element only. */
+enum { AXON_ACT_NONE = 0, AXON_ACT_SILU = 1 };
+enum { AXON_GATE_NONE = 0, AXON_GATE_BEFORE = 1, AXON_GATE_AFTER = 2 };
+
+typedef struct {
+  int64_t rows;
+  int64_t groups;
+  int64_t width;           /* channels of a group */
+  int64_t x_stride;        /* elements between rows; 0 = dense */
+  int64_t z_stride;
+  float eps;               /* finite, >= 0 */
+  int32_t act_dtype;       /* an axon_dtype value */
+  int32_t centered;        /* 0 or 1 */
+  int32_t activation;      /* AXON_ACT_* */
+  int32_t gate;            /* AXON_GATE_*; z is not read with AXON_GATE_NONE */
+  int32_t shared_weights;  /* 0 or 1 */
+} axon_group_norm_desc;
+
+axon_status axon_group_norm(const axon_group_norm_desc* desc, const void* x, const void* z,
+                            const float* weight, const float* bias, void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

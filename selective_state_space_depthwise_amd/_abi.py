@@ -67,6 +67,28 @@ class SsdParams(ctypes.Structure):
                 ("dt_min", ctypes.c_float), ("dt_max", ctypes.c_float)]
 
 
+class GatedDeltaShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "sequences", "tokens", "key_heads", "value_heads", "key_dim", "value_dim", "q_stride",
+        "k_stride", "v_stride", "state_slots", "out_slots")] + [("act_dtype", ctypes.c_int32)]
+
+
+class GatedDeltaParams(ctypes.Structure):
+    _fields_ = [("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+                ("dt_min", ctypes.c_float), ("dt_max", ctypes.c_float), ("scale", ctypes.c_float),
+                ("eps", ctypes.c_float)]
+
+
+class GroupNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("groups", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("act_dtype", ctypes.c_int32),
+                ("centered", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("shared_weights", ctypes.c_int32)]
+
+
+NORM_ACTIVATIONS = {"none": 0, "silu": 1}
+NORM_GATES = {"none": 0, "before": 1, "after": 2}
 CONV_ACTIVATIONS = {"none": 0, "silu": 1}
 DISCRETIZATIONS = {"first_order": 0, "zoh": 1}
 
@@ -122,6 +144,23 @@ def load():
         lib.axon_ssd_scan.restype = ctypes.c_int
         lib.axon_ssd_scan.argtypes = [ctypes.POINTER(SsdShape), ctypes.POINTER(SsdParams),
                                       P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        I = ctypes.c_int64  # noqa: E741
+        lib.axon_sequence_tables_count.restype = ctypes.c_size_t
+        lib.axon_sequence_tables_count.argtypes = [I, I, I]
+        lib.axon_sequence_tables.restype = ctypes.c_int
+        lib.axon_sequence_tables.argtypes = [I, I, I, P, P, P]
+        lib.axon_gated_delta_scan_workspace_bytes.restype = ctypes.c_size_t
+        lib.axon_gated_delta_scan_workspace_bytes.argtypes = [ctypes.POINTER(GatedDeltaShape)]
+        lib.axon_gated_delta_scan.restype = ctypes.c_int
+        lib.axon_gated_delta_scan.argtypes = [
+            ctypes.POINTER(GatedDeltaShape), ctypes.POINTER(GatedDeltaParams),
+            P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        lib.axon_gated_delta_step.restype = ctypes.c_int
+        lib.axon_gated_delta_step.argtypes = [
+            ctypes.POINTER(GatedDeltaShape), ctypes.POINTER(GatedDeltaParams),
+            P, P, P, P, P, P, P, P, P]
+        lib.axon_group_norm.restype = ctypes.c_int
+        lib.axon_group_norm.argtypes = [ctypes.POINTER(GroupNormDesc), P, P, P, P, P, P]
         _lib = lib
         return lib
 
@@ -229,6 +268,40 @@ def raw_ssd_scan(shape: SsdShape, params: SsdParams, x, dt_raw, B, C, state_in, 
     """axon_ssd_scan with integer pointers. Returns the status code."""
     return load().axon_ssd_scan(ctypes.byref(shape), ctypes.byref(params), x, dt_raw, B, C,
                                 state_in, y, state_out, workspace, int(workspace_bytes_), stream)
+
+
+def sequence_tables_count(sequences, total_tokens, block) -> int:
+    return int(load().axon_sequence_tables_count(sequences, total_tokens, block))
+
+
+def raw_sequence_tables(sequences, total_tokens, block, lengths, tables, stream) -> int:
+    """axon_sequence_tables with integer pointers. Returns the status code."""
+    return load().axon_sequence_tables(sequences, total_tokens, block, lengths, tables, stream)
+
+
+def gated_delta_workspace_bytes(shape: GatedDeltaShape) -> int:
+    return int(load().axon_gated_delta_scan_workspace_bytes(ctypes.byref(shape)))
+
+
+def raw_gated_delta_scan(shape: GatedDeltaShape, params: GatedDeltaParams, q, k, v, dt_raw,
+                         beta_raw, tables, state_in, in_slots, y, state_out, out_slots, workspace,
+                         workspace_bytes_, stream) -> int:
+    """axon_gated_delta_scan with integer pointers (None = NULL). Returns the status code."""
+    return load().axon_gated_delta_scan(ctypes.byref(shape), ctypes.byref(params), q, k, v, dt_raw,
+                                        beta_raw, tables, state_in, in_slots, y, state_out,
+                                        out_slots, workspace, workspace_bytes_, stream)
+
+
+def raw_gated_delta_step(shape: GatedDeltaShape, params: GatedDeltaParams, q, k, v, dt_raw,
+                         beta_raw, state, slots, y, stream) -> int:
+    """axon_gated_delta_step with integer pointers (None = NULL). Returns the status code."""
+    return load().axon_gated_delta_step(ctypes.byref(shape), ctypes.byref(params), q, k, v, dt_raw,
+                                        beta_raw, state, slots, y, stream)
+
+
+def raw_group_norm(desc: GroupNormDesc, x, z, weight, bias, y, stream) -> int:
+    """axon_group_norm with integer pointers (None = NULL). Returns the status code."""
+    return load().axon_group_norm(ctypes.byref(desc), x, z, weight, bias, y, stream)
 
 
 def declared_functions() -> list[str]:
