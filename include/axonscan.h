@@ -345,7 +345,8 @@ axon_status axon_sequence_tables(int64_t sequences, int64_t total_tokens, int64_
  *   A_log, dt_bias (value_heads) fp32;  pools of states (slots, value_heads, V, K) fp32.
  * Supported: K 64 or 128; V a multiple of 16 up to 256; value_heads a multiple of key_heads (else
  * AXON_ERR_UNSUPPORTED); sequences and heads in [1, 65535]; sequences * value_heads < 2^20;
- * tokens < 2^29; tokens * heads * dim and slots * value_heads * V * K <= 2^40. Device pointers 16-byte aligned, integer arrays 4-byte.
+ * tokens < 2^29; rows and their strides at most 2^22 elements; tokens * stride and slots *
+ * value_heads * V * K <= 2^40. Device pointers 16-byte aligned, integer arrays 4-byte.
  *
  * Slots: sequence (or row) n uses state slots[n] of the pool, or state n where slots is NULL (the
  * pool then holds at least `sequences` states). A slot outside the pool means no state: a scan starts from

@@ -3,11 +3,11 @@
 //
 // Inside a chunk, with g_t the inclusive sum of dt A from the chunk's start and S0 (V x K) the
 // entering state, the recurrence S_t = a_t S_{t-1} + D_t k^_t^T, D_t = beta_t (v_t - a_t S_{t-1} k^_t)
-// unrolls to
-//   D_t + beta_t sum_{s<t} e^{g_t-g_s} (k^_t.k^_s) D_s = beta_t (v_t - e^{g_t} S0 k^_t),
-// a unit lower triangular system (I + M) D = diag(beta) X. Its inverse does not depend on the
-// state, so it is computed for all chunks at once; the walk over the chunks is products only:
-//   X = v - e^g (S0 k^),  D = T X with T = (I + M)^-1 diag(beta),
+// unrolls, with D_t = beta_t E_t, to the unit lower triangular system
+//   E_t + sum_{s<t} e^{g_t-g_s} (k^_t.k^_s) beta_s E_s = X_t = v_t - e^{g_t} S0 k^_t.
+// The inverse T of its matrix I + M does not depend on the state, so it is computed for all chunks
+// at once; the walk over the chunks is products only:
+//   X = v - e^g (S0 k^),  D = diag(beta) T X,
 //   y = scale (e^g S0 q^ + A D),  A[t,s] = e^{g_t-g_s} q^_t.k^_s (s <= t),
 //   S <- e^{g_last} S0 + sum_t e^{g_last-g_t} D_t k^_t^T.
 // Every exponent is <= 0; the sums are compensated (head and tail) because steps near dt_max push
@@ -17,13 +17,21 @@
 //   prep_kernel  per chunk and key head: the Gram products, then per value head T (16 x 16 diagonal
 //                blocks by substitution, which stays accurate where keys are alike and powers of M
 //                would cancel; the blocks below by matrix products), A and the row factors.
-//   walk_kernel  per sequence, value head and 16 columns of V one wave walks the chunks with its
-//                slice of the state in registers. The state is held transposed (S^T, K x 16): the
-//                result layout of a 16 x 16 product (lane (g, i): rows 4 g + r, column i) is also
-//                the layout of the right operand of the next one when the contraction index is
-//                taken as 4 g + r, so state, X and D go from product to product without leaving
-//                their lanes.
-// Products run on v_mfma_f32_16x16x4f32 (layout in axon_ssd.hip's head comment).
+//   walk_kernel  per sequence, value head and slice of 16 or 32 columns of V one wave walks the
+//                chunks with its slice of the state in registers. The state is held transposed
+//                (S^T, K x 16): the result layout of a 16 x 16 product (lane (g, i), g = lane / 16,
+//                i = lane % 16: rows 4 g + r, column i) is also the layout of the next product's
+//                right operand when 32 contraction indices are dealt to (g, e) as 4 g + e for
+//                e < 4 and 16 + 4 g + e - 4 above, so state, X and D go from product to product
+//                without leaving their lanes.
+//
+// Precision. fp32 products would run at a sixteenth of the fp16 matrix rate, so the walk splits
+// each fp32 operand into fp16 pieces, x 2^s = hi + lo, with s per row of q and k and per column of
+// S, X and D such that the largest value lies in [2^13, 2^14): two pieces hold 22 bits, and what is
+// below 2^-27 of the largest is lost, so a product of pieces is as exact as an fp32 one. bf16 keys
+// and queries are exact in one piece. The states, every accumulator and every factor are fp32. For
+// bf16 activations the operands that only y sees (S, A and D of its two products) are one piece, 11
+// bits: 2^-12 against the 2^-9 of y's own rounding.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -41,14 +49,26 @@ constexpr int kMS = kQ + 4;  // LDS row stride of 64 x 64 matrices
 
 typedef float f4 __attribute__((ext_vector_type(4)));
 
-// What prep leaves for each (chunk, value head), in floats: T and A as ten 16 x 16 blocks on and
-// below the diagonal (block I (I + 1) / 2 + J), each as 64 lanes x 4 in left-operand order (lane
-// (g, i): row i, columns 4 g .. 4 g + 3), then the row factors e^g / |k|, e^{g_last-g} / |k|,
-// scale e^g / |q| of the 64 tokens and e^{g_last}.
+// fp16 pieces of an activation (bf16: exact in one) and of A (see above).
+template <typename Act>
+constexpr int kPieces = sizeof(Act) == 2 ? 1 : 2;
+
+// What prep leaves for each (chunk, value head): T in two pieces and A in one or two, each as ten
+// 16 x 16 blocks on and below the diagonal (block I (I + 1) / 2 + J), a block as 64 lanes x 4 fp16
+// in left-operand order (lane (g, i): row i, columns 4 g .. 4 g + 3), both times 2^12; then the row
+// factors of the 64 tokens, fp32, and e^{g_last}. What the walk keeps in LDS comes first.
 constexpr int kBlocks = 10;
-constexpr int kOffA = kBlocks * 256;
-constexpr int kOffRows = 2 * kBlocks * 256;
-constexpr int kRecord = kOffRows + 256;
+constexpr int kBlockBytes = 512;
+constexpr float kUp = 4096.0f;  // |T|, |A| <= 1: their pieces stay normal fp16 numbers
+enum Row { kRowX, kRowD, kRowS, kRowY, kRowK, kRowQ, kRows };
+//   kRowX  e^g / |k| / 2^s      of S0 k in X (s: the shift of k)
+//   kRowD  beta / 2^12          of T X in D
+//   kRowS  e^{g_last-g} / |k| / 2^s   of D in the state's sum
+//   kRowY  e^g / |q| / 2^s 2^12       of S0 q in y
+//   kRowK, kRowQ  the shifts of k and q: fp32 2^s, bf16 what is taken off both exponents of a pair
+constexpr int rows_at(int pieces) { return (2 + pieces) * kBlocks * kBlockBytes; }
+constexpr int lds_bytes(int pieces) { return rows_at(pieces) + kRowK * kQ * 4; }
+constexpr int record_bytes(int pieces) { return rows_at(pieces) + kRows * kQ * 4 + 64; }
 
 struct DeltaArgs {
   const void *q, *k, *v, *dt_raw, *beta_raw;
@@ -60,7 +80,7 @@ struct DeltaArgs {
   void* y;
   float* state_out;
   const int32_t* out_slots;
-  float* records;
+  char* records;
   int64_t tokens, seqlen, q_stride, k_stride, v_stride, in_count, out_count;
   int sequences, hk, hv, ratio, value_dim, col_groups;
   int rows;             // chunk rows of the workspace
@@ -112,16 +132,113 @@ __device__ __forceinline__ bool chunk_of(const DeltaArgs& a, int c, int64_t* fir
   return true;
 }
 
+// ---- fp16 pieces --------------------------------------------------------------------------------
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef uint16_t u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t w4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f4 mfma_h(h8 a, h8 b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// 2^s that takes m to [2^13, 2^14), and its inverse; the exponent is held to where both are normal.
+struct Scale {
+  float up, down;
+};
+__device__ __forceinline__ Scale scale_of(float m) {
+  int e = static_cast<int>(__float_as_uint(m) >> 23);
+  e = e < 30 ? 30 : e > 250 ? 250 : e;
+  return {__uint_as_float(static_cast<uint32_t>(267 - e) << 23),
+          __uint_as_float(static_cast<uint32_t>(e - 13) << 23)};
+}
+// bf16: what is taken off a pair's exponents so that the largest becomes fp16's 28 (2^13), and the
+// inverse of that shift. x 2^(112 - off) is exact in fp16 down to 2^-27 of the largest.
+__device__ __forceinline__ uint32_t pair_shift(float m) {
+  const uint32_t e = __float_as_uint(m) >> 23;
+  const uint32_t off = e > 28 ? e - 28 : 0;
+  return off << 7 | off << 23;
+}
+__device__ __forceinline__ float pair_unshift(uint32_t pair) {
+  return __uint_as_float((((pair >> 7) & 0xFF) + 15) << 23);
+}
+__device__ __forceinline__ uint32_t pair_to_fp16(uint32_t x, uint32_t pair) {
+  const u2 mag = __builtin_bit_cast(u2, x & 0x7FFF7FFFu);
+  u2 r = __builtin_elementwise_sub_sat(mag, __builtin_bit_cast(u2, pair));
+  r = r << static_cast<uint16_t>(3);
+  return (x & 0x80008000u) | __builtin_bit_cast(uint32_t, r);
+}
+
+// Four activations as loaded, and their fp16 pieces.
+template <typename Act>
+struct Four;
+template <>
+struct Four<bf16_bits> {
+  uint2 raw;
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t off) {
+    raw = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+  }
+  __device__ __forceinline__ void pieces(uint32_t shift, uint2* out) const {
+    out[0] = make_uint2(pair_to_fp16(raw.x, shift), pair_to_fp16(raw.y, shift));
+  }
+};
+template <>
+struct Four<float> {
+  f4 raw;
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t off) {
+    raw = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+  }
+  __device__ __forceinline__ void pieces(uint32_t shift, uint2* out) const {
+    const f4 x = raw * __uint_as_float(shift);
+    const h4 hi = __builtin_convertvector(x, h4);
+    const h4 lo = __builtin_convertvector(x - __builtin_convertvector(hi, f4), h4);
+    out[0] = __builtin_bit_cast(uint2, hi);
+    out[1] = __builtin_bit_cast(uint2, lo);
+  }
+};
+
+// Two pieces of eight values (two accumulators of one column) times a scale.
+__device__ __forceinline__ void split8(f4 a, f4 b, float up, h8* hi, h8* lo) {
+  a *= up, b *= up;
+  const h4 ha = __builtin_convertvector(a, h4), hb = __builtin_convertvector(b, h4);
+  const h4 la = __builtin_convertvector(a - __builtin_convertvector(ha, f4), h4);
+  const h4 lb = __builtin_convertvector(b - __builtin_convertvector(hb, f4), h4);
+  *hi = __builtin_shufflevector(ha, hb, 0, 1, 2, 3, 4, 5, 6, 7);
+  *lo = __builtin_shufflevector(la, lb, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// The value, computed anew where it is used: sums with it are not kept in registers across a loop.
+__device__ __forceinline__ uint32_t fresh(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// The largest over the four lanes (g = 0 .. 3) that share a column.
+__device__ __forceinline__ float column_max(float m) {
+  const uint32_t u = __float_as_uint(m);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const float x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const uint32_t v = __float_as_uint(x);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float max4(float m, f4 x) {
+  m = fmaxf(fmaxf(m, fabsf(x[0])), fabsf(x[1]));
+  return fmaxf(fmaxf(m, fabsf(x[2])), fabsf(x[3]));
+}
+
 // ---- T, A and the row factors of every chunk ----------------------------------------------------
 // Grid (chunk rows, key heads), 4 waves. Wave w owns rows 16 w .. 16 w + 15 of the Gram products
-// and column block w of the inverse.
+// and column block w of the inverse. The Gram products of bf16 inputs are exact bf16 products, those
+// of fp32 inputs and the inverse run on v_mfma_f32_16x16x4f32 (layout in axon_ssd.hip).
 template <typename Act, int K>
 __global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
-  constexpr int NB = K / 16;
+  constexpr int P = kPieces<Act>;
   __shared__ float Ms[kQ * kMS];
   __shared__ float As[kQ * kMS];
   __shared__ float Ds[4][16 * 20];
-  __shared__ float hi_s[kQ], lo_s[kQ], beta_s[kQ], rk_s[kQ], rq_s[kQ];
+  __shared__ float hi_s[kQ], lo_s[kQ], beta_s[kQ], rk_s[kQ], rq_s[kQ], mk_s[kQ], mq_s[kQ];
   int64_t first;
   int count;
   if (!chunk_of(a, blockIdx.x, &first, &count)) return;
@@ -130,57 +247,96 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
   const Act* kp = static_cast<const Act*>(a.k) + first * a.k_stride + int64_t(hk) * K;
   const Act* qp = static_cast<const Act*>(a.q) + first * a.q_stride + int64_t(hk) * K;
   f4 gk[4], gq[4];
+#pragma unroll
+  for (int st = 0; st < 4; ++st) gk[st] = gq[st] = f4{0.0f, 0.0f, 0.0f, 0.0f};
   {
-    float4 krow[NB], qrow[NB];
     const int t = 16 * w + i;
-    float sk = 0.0f, sq = 0.0f;
+    float sk = 0.0f, sq = 0.0f, mk = 0.0f, mq = 0.0f;
+    auto sums = [](f4 x, float& s, float& m) {
+      s += x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
+      m = max4(m, x);
+    };
+    if constexpr (P == 1) {
+      constexpr int NB = K / 32;
+      b8 krow[NB], qrow[NB], col[NB];
+      const b8 zero = {};
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      krow[b] = t < count ? load4(kp + t * a.k_stride + 16 * b + 4 * g) : float4{};
-      qrow[b] = t < count ? load4(qp + t * a.q_stride + 16 * b + 4 * g) : float4{};
-    }
+      for (int b = 0; b < NB; ++b) {
+        krow[b] = t < count ? *reinterpret_cast<const b8*>(kp + t * a.k_stride + 32 * b + 8 * g) : zero;
+        qrow[b] = t < count ? *reinterpret_cast<const b8*>(qp + t * a.q_stride + 32 * b + 8 * g) : zero;
+      }
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      sk += krow[b].x * krow[b].x + krow[b].y * krow[b].y + krow[b].z * krow[b].z +
-            krow[b].w * krow[b].w;
-      sq += qrow[b].x * qrow[b].x + qrow[b].y * qrow[b].y + qrow[b].z * qrow[b].z +
-            qrow[b].w * qrow[b].w;
+      for (int b = 0; b < NB; ++b) {
+        f4 x, y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = krow[b][e], y[e] = krow[b][e + 4];
+        sums(x, sk, mk);
+        sums(y, sk, mk);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = qrow[b][e], y[e] = qrow[b][e + 4];
+        sums(x, sq, mq);
+        sums(y, sq, mq);
+      }
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {
+        if (st > w) continue;
+        const int ts = 16 * st + i;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          col[b] = ts < count ? *reinterpret_cast<const b8*>(kp + ts * a.k_stride + 32 * b + 8 * g) : zero;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          gk[st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(krow[b], col[b], gk[st], 0, 0, 0);
+          gq[st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qrow[b], col[b], gq[st], 0, 0, 0);
+        }
+      }
+    } else {
+      constexpr int NB = K / 16;
+      f4 krow[NB], qrow[NB], col[NB];
+      const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        krow[b] = t < count ? *reinterpret_cast<const f4*>(kp + t * a.k_stride + 16 * b + 4 * g) : zero;
+        qrow[b] = t < count ? *reinterpret_cast<const f4*>(qp + t * a.q_stride + 16 * b + 4 * g) : zero;
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        sums(krow[b], sk, mk);
+        sums(qrow[b], sq, mq);
+      }
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {
+        if (st > w) continue;
+        const int ts = 16 * st + i;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          col[b] = ts < count ? *reinterpret_cast<const f4*>(kp + ts * a.k_stride + 16 * b + 4 * g) : zero;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            gk[st] = mfma4(krow[b][e], col[b][e], gk[st]);
+            gq[st] = mfma4(qrow[b][e], col[b][e], gq[st]);
+          }
+      }
     }
     sk += __shfl_xor(sk, 16, 64);
     sk += __shfl_xor(sk, 32, 64);
     sq += __shfl_xor(sq, 16, 64);
     sq += __shfl_xor(sq, 32, 64);
+    mk = column_max(mk);
+    mq = column_max(mq);
     if (g == 0) {
       rk_s[t] = 1.0f / sqrtf(sk + a.eps);
       rq_s[t] = 1.0f / sqrtf(sq + a.eps);
-    }
-#pragma unroll
-    for (int st = 0; st < 4; ++st) {
-      gk[st] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-      gq[st] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (st > w) continue;
-      const int ts = 16 * st + i;
-      float4 col[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        col[b] = ts < count ? load4(kp + ts * a.k_stride + 16 * b + 4 * g) : float4{};
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        gk[st] = mfma4(krow[b].x, col[b].x, gk[st]);
-        gq[st] = mfma4(qrow[b].x, col[b].x, gq[st]);
-        gk[st] = mfma4(krow[b].y, col[b].y, gk[st]);
-        gq[st] = mfma4(qrow[b].y, col[b].y, gq[st]);
-        gk[st] = mfma4(krow[b].z, col[b].z, gk[st]);
-        gq[st] = mfma4(qrow[b].z, col[b].z, gq[st]);
-        gk[st] = mfma4(krow[b].w, col[b].w, gk[st]);
-        gq[st] = mfma4(qrow[b].w, col[b].w, gq[st]);
-      }
+      mk_s[t] = mk;
+      mq_s[t] = mq;
     }
   }
   for (int vh = 0; vh < a.ratio; ++vh) {
     const int h = hk * a.ratio + vh;
-    float* rec = a.records + (int64_t(blockIdx.x) * a.hv + h) * kRecord;
-    __syncthreads();  // the previous head's matrices and factors have been read; rk_s, rq_s ready
+    char* rec = a.records + (int64_t(blockIdx.x) * a.hv + h) * record_bytes(P);
+    __syncthreads();  // the previous head's matrices and factors have been read; the norms are in
     if (w == 0) {
       float dt = 0.0f, beta = 0.0f;
       if (lane < count) {
@@ -205,23 +361,36 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
       hi_s[lane] = hi, lo_s[lane] = lo, beta_s[lane] = beta;
       const float last_hi = __shfl(hi, 63, 64), last_lo = __shfl(lo, 63, 64);
       const float e = __builtin_amdgcn_exp2f(hi + lo);
-      rec[kOffRows + lane] = e * rk_s[lane];
-      rec[kOffRows + 64 + lane] = exp2_diff(last_hi, last_lo, hi, lo) * rk_s[lane];
-      rec[kOffRows + 128 + lane] = a.scale * e * rq_s[lane];
-      if (lane == 63) rec[kOffRows + 192] = e;
+      float ku, kd, qu, qd;  // the shifts as the walk takes them, and their inverses
+      if constexpr (P == 1) {
+        const uint32_t k2 = pair_shift(mk_s[lane]), q2 = pair_shift(mq_s[lane]);
+        ku = __uint_as_float(k2), kd = pair_unshift(k2);
+        qu = __uint_as_float(q2), qd = pair_unshift(q2);
+      } else {
+        const Scale k2 = scale_of(mk_s[lane]), q2 = scale_of(mq_s[lane]);
+        ku = k2.up, kd = k2.down, qu = q2.up, qd = q2.down;
+      }
+      float* row = reinterpret_cast<float*>(rec + rows_at(P)) + lane;
+      row[kRowX * kQ] = e * (rk_s[lane] * kd);
+      row[kRowD * kQ] = beta * (1.0f / kUp);
+      row[kRowS * kQ] = exp2_diff(last_hi, last_lo, hi, lo) * (rk_s[lane] * kd);
+      row[kRowY * kQ] = e * (rq_s[lane] * qd) * kUp;
+      row[kRowK * kQ] = ku;
+      row[kRowQ * kQ] = qu;
+      if (lane == 63) row[kRows * kQ - 63] = e;
     }
     __syncthreads();
 #pragma unroll
     for (int st = 0; st < 4; ++st) {
       if (st > w) continue;
       const int s = 16 * st + i;
-      const float hs = hi_s[s], ls = lo_s[s], rks = rk_s[s];
+      const float hs = hi_s[s], ls = lo_s[s], rks = rk_s[s], bs = beta_s[s];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * w + 4 * g + r;
         const float e = exp2_diff(hi_s[t], lo_s[t], hs, ls) * rks;
-        Ms[t * kMS + s] = s < t ? beta_s[t] * rk_s[t] * e * gk[st][r] : 0.0f;
-        As[t * kMS + s] = s <= t ? a.scale * rq_s[t] * e * gq[st][r] : 0.0f;
+        Ms[t * kMS + s] = s < t ? bs * rk_s[t] * e * gk[st][r] : 0.0f;
+        As[t * kMS + s] = s <= t ? rq_s[t] * e * gq[st][r] : 0.0f;
       }
     }
     __syncthreads();
@@ -255,55 +424,70 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
 #pragma unroll
         for (int S = 0; S < I; ++S) {
           if (S < w) continue;
-          const float4 m = *reinterpret_cast<const float4*>(&Ms[(16 * I + i) * kMS + 16 * S + 4 * g]);
-          p = mfma4(m.x, X[S][0], p);
-          p = mfma4(m.y, X[S][1], p);
-          p = mfma4(m.z, X[S][2], p);
-          p = mfma4(m.w, X[S][3], p);
+          const f4 m = *reinterpret_cast<const f4*>(&Ms[(16 * I + i) * kMS + 16 * S + 4 * g]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) p = mfma4(m[r], X[S][r], p);
         }
-        const float4 d = *reinterpret_cast<const float4*>(&Ds[I][i * 20 + 4 * g]);
+        const f4 d = *reinterpret_cast<const f4*>(&Ds[I][i * 20 + 4 * g]);
         f4 x = f4{0.0f, 0.0f, 0.0f, 0.0f};
-        x = mfma4(d.x, p[0], x);
-        x = mfma4(d.y, p[1], x);
-        x = mfma4(d.z, p[2], x);
-        x = mfma4(d.w, p[3], x);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x = mfma4(d[r], p[r], x);
         X[I] = -x;
       }
     }
     __syncthreads();  // M has been read: T takes its place
-    const float beta = beta_s[16 * w + i];
 #pragma unroll
     for (int I = 0; I < 4; ++I) {
       if (I < w) continue;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) Ms[(16 * I + 4 * g + r) * kMS + 16 * w + i] = X[I][r] * beta;
+      for (int r = 0; r < 4; ++r) Ms[(16 * I + 4 * g + r) * kMS + 16 * w + i] = X[I][r];
     }
     __syncthreads();
     for (int b = w; b < 2 * kBlocks; b += 4) {
-      const int bb = b < kBlocks ? b : b - kBlocks;
+      const bool is_t = b < kBlocks;
+      const int bb = is_t ? b : b - kBlocks;
       const int I = bb < 1 ? 0 : bb < 3 ? 1 : bb < 6 ? 2 : 3;
       const int J = bb - I * (I + 1) / 2;
-      const float* src = (b < kBlocks ? Ms : As) + (16 * I + i) * kMS + 16 * J + 4 * g;
-      *reinterpret_cast<float4*>(rec + b * 256 + lane * 4) = *reinterpret_cast<const float4*>(src);
+      const float* src = (is_t ? Ms : As) + (16 * I + i) * kMS + 16 * J + 4 * g;
+      const f4 x = *reinterpret_cast<const f4*>(src) * kUp;
+      const h4 hi = __builtin_convertvector(x, h4);
+      char* dst = rec + ((is_t ? 0 : 2 * kBlocks) + bb) * kBlockBytes + lane * 8;
+      *reinterpret_cast<h4*>(dst) = hi;
+      if (is_t || P == 2)
+        *reinterpret_cast<h4*>(dst + kBlocks * kBlockBytes) =
+            __builtin_convertvector(x - __builtin_convertvector(hi, f4), h4);
     }
   }
 }
 
 // ---- the walk over the chunks -------------------------------------------------------------------
-// One wave per 16 columns of V, 4 waves a workgroup; the column groups of one head are spaced by
-// the 8 XCDs' round-robin so that they share that XCD's L2.
-template <typename Act, int K>
-__global__ __launch_bounds__(kThreads) void walk_kernel(DeltaArgs a) {
-  constexpr int NB = K / 16, KS = K + 4;
-  __shared__ float Ks[kQ * KS];
-  __shared__ float Qs[kQ * KS];
+// 4 waves a workgroup, each with NC tiles of 16 columns of V. Per chunk the workgroup brings k (as
+// left operand of S k^ and, transposed, of the state's sum), q and the chunk's record into LDS in
+// operand order, so that a wave reads whole 1 KiB operands without bank conflicts: operand (block
+// of 16 rows, 32 contraction indices) holds lane (g, i)'s eight fp16 at 16 (16 g + (i ^ g)); the
+// exclusive or spreads the writers, who own 4 tokens x 4 channels each, over the banks. The next
+// chunk's rows travel in registers meanwhile.
+template <typename Act, int K, int NC>
+__global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 2 : 1) void walk_kernel(DeltaArgs a) {
+  constexpr int P = kPieces<Act>;
+  constexpr int NB = K / 16, KB = K / 32;
+  constexpr int kOperand = 1024, kMat = 4 * KB * kOperand;  // one piece of k or q of a chunk
+  constexpr int kRec = record_bytes(P), kLds = lds_bytes(P);
+  static_assert(kLds % 1024 == 0, "whole wave loads");
+  constexpr int kUnits = K / 64;  // 4 x 4 blocks of k (and q) a thread brings
+  __shared__ __align__(16) char ks[P * kMat];
+  __shared__ __align__(16) char kt[P * kMat];
+  __shared__ __align__(16) char qs[P * kMat];
+  __shared__ __align__(16) char rs2[2][kLds];
+
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
   const int64_t nh = int64_t(slot / a.col_groups) * 8 + xcd;
   if (nh >= int64_t(a.sequences) * a.hv) return;
   const int n = static_cast<int>(nh / a.hv), h = static_cast<int>(nh - int64_t(n) * a.hv);
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, i = lane & 15;
-  const int col = ((slot % a.col_groups) * 4 + w) * 16 + i;  // of V
-  const bool mine = col < a.value_dim;                       // wave-uniform: V is a multiple of 16
+  const int col0 = ((slot % a.col_groups) * 4 + w) * 16 * NC;
+  const bool mine = col0 < a.value_dim;  // wave-uniform: V is a multiple of 16
+  const int hk = h / a.ratio;
   int64_t begin, len, row0;
   if (a.starts) {
     begin = a.starts[n];
@@ -317,120 +501,275 @@ __global__ __launch_bounds__(kThreads) void walk_kernel(DeltaArgs a) {
   int64_t chunks = len > 0 ? (len + kQ - 1) / kQ : 0;
   if (chunks > a.rows - row0) chunks = a.rows - row0;
 
-  f4 S[NB];
+  f4 S[NC][NB];
   {
     const int64_t slot_in = a.in_slots ? a.in_slots[n] : n;
-    const bool have = a.state_in && mine && slot_in >= 0 && slot_in < a.in_count;
+    const bool have = a.state_in && slot_in >= 0 && slot_in < a.in_count;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      S[b] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (have) {
-        const float4 v = load4(a.state_in + ((slot_in * a.hv + h) * a.value_dim + col) * K + 16 * b +
-                               4 * g);
-        S[b] = f4{v.x, v.y, v.z, v.w};
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int col = col0 + 16 * c + i;
+        S[c][b] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (have && col0 + 16 * c < a.value_dim)
+          S[c][b] = *reinterpret_cast<const f4*>(
+              a.state_in + ((slot_in * a.hv + h) * a.value_dim + col) * K + 16 * b + 4 * g);
       }
-    }
   }
-  const int hk = h / a.ratio;
-  for (int64_t c = 0; c < chunks; ++c) {
+
+  // What this thread brings: tokens 4 tau .. + 3, channels 4 kappa .. + 3.
+  const int tau = (w >> 1) * 8 + ((lane >> 3) & 3) + 4 * (lane >> 5);
+  const int kap0 = (lane & 7) + 8 * (K == 128 ? 2 * (w & 1) : (w & 1));
+  Four<Act> pk[kUnits][4], pq[kUnits][4];
+  w4 shk, shq;
+  float end = 0.0f, end_next = 0.0f;
+  const uint32_t es = sizeof(Act);
+  const uint32_t koff = static_cast<uint32_t>(a.k_stride) * es, qoff = static_cast<uint32_t>(a.q_stride) * es;
+  // Rows behind the sequence lie outside the resource's range and read as zeros.
+  auto load = [&](int64_t c) {
     const int64_t first = begin + c * kQ;
     const int count = len - c * kQ < kQ ? static_cast<int>(len - c * kQ) : kQ;
-    const float* rec = a.records + ((row0 + c) * a.hv + h) * kRecord;
-    {
-      const Act* kp = static_cast<const Act*>(a.k) + first * a.k_stride + int64_t(hk) * K;
-      const Act* qp = static_cast<const Act*>(a.q) + first * a.q_stride + int64_t(hk) * K;
-      for (int e = tid; e < kQ * K / 4; e += kThreads) {
-        const int t = e / (K / 4), kk = 4 * (e % (K / 4));
-        const float4 kv = t < count ? load4(kp + t * a.k_stride + kk) : float4{};
-        const float4 qv = t < count ? load4(qp + t * a.q_stride + kk) : float4{};
-        *reinterpret_cast<float4*>(&Ks[t * KS + kk]) = kv;
-        *reinterpret_cast<float4*>(&Qs[t * KS + kk]) = qv;
+    const rsrc_t kr = make_rsrc_bounded(
+        const_cast<Act*>(static_cast<const Act*>(a.k) + first * a.k_stride + int64_t(hk) * K),
+        (count - 1) * koff + K * es);
+    const rsrc_t qr = make_rsrc_bounded(
+        const_cast<Act*>(static_cast<const Act*>(a.q) + first * a.q_stride + int64_t(hk) * K),
+        (count - 1) * qoff + K * es);
+    const char* rec = a.records + ((row0 + c) * a.hv + h) * int64_t(kRec);
+    // The record goes to LDS without passing through registers, 1 KiB a wave and instruction.
+    for (int u = w; u < kLds / 1024; u += 4)
+      __builtin_amdgcn_global_load_lds(
+          reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(
+              reinterpret_cast<uintptr_t>(rec + u * 1024 + lane * 16)),
+          (__attribute__((address_space(3))) uint32_t*)(&rs2[c & 1][u * 1024]), 16, 0, 0);
+    const char* rows = rec + rows_at(P) + 16 * tau;
+    end_next = *reinterpret_cast<const float*>(rec + rows_at(P) + kRows * kQ * 4);
+    shk = *reinterpret_cast<const w4*>(rows + kRowK * kQ * 4);
+    shq = *reinterpret_cast<const w4*>(rows + kRowQ * kQ * 4);
+    const uint32_t k0 = fresh(4 * (tau * koff + kap0 * es)), q0 = fresh(4 * (tau * qoff + kap0 * es));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        pk[u][j].load(kr, k0 + j * koff + 32 * es * u);
+        pq[u][j].load(qr, q0 + j * qoff + 32 * es * u);
+      }
+  };
+  auto store = [&]() {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int kap = kap0 + 8 * u;
+      // as rows: operand (tau / 4, kappa / 8), lane group kappa % 4, half (kappa / 4) % 2
+      const int rbase = ((tau >> 2) * KB + (kap >> 3)) * kOperand + (kap & 3) * 256 + ((kap >> 2) & 1) * 8;
+      // transposed: operand (kappa / 4, tau / 8), lane group tau % 4, half (tau / 4) % 2
+      const int cbase = ((kap >> 2) * 2 + (tau >> 3)) * kOperand + (tau & 3) * 256 + ((tau >> 2) & 1) * 8;
+      uint2 pc[4][P];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        pq[u][j].pieces(shq[j], pc[j]);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          *reinterpret_cast<uint2*>(qs + p * kMat + rbase + ((4 * (tau & 3) + j) ^ (kap & 3)) * 16) = pc[j][p];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        pk[u][j].pieces(shk[j], pc[j]);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          *reinterpret_cast<uint2*>(ks + p * kMat + rbase + ((4 * (tau & 3) + j) ^ (kap & 3)) * 16) = pc[j][p];
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        uint2 c[4];
+        c[0] = make_uint2(__builtin_amdgcn_perm(pc[1][p].x, pc[0][p].x, 0x05040100),
+                          __builtin_amdgcn_perm(pc[3][p].x, pc[2][p].x, 0x05040100));
+        c[1] = make_uint2(__builtin_amdgcn_perm(pc[1][p].x, pc[0][p].x, 0x07060302),
+                          __builtin_amdgcn_perm(pc[3][p].x, pc[2][p].x, 0x07060302));
+        c[2] = make_uint2(__builtin_amdgcn_perm(pc[1][p].y, pc[0][p].y, 0x05040100),
+                          __builtin_amdgcn_perm(pc[3][p].y, pc[2][p].y, 0x05040100));
+        c[3] = make_uint2(__builtin_amdgcn_perm(pc[1][p].y, pc[0][p].y, 0x07060302),
+                          __builtin_amdgcn_perm(pc[3][p].y, pc[2][p].y, 0x07060302));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint2*>(kt + p * kMat + cbase + ((4 * (kap & 3) + j) ^ (tau & 3)) * 16) = c[j];
       }
     }
+  };
+  const int at16 = (16 * g + (i ^ g)) * 16;
+  auto operand = [&](const char* m, int p, int index) {
+    return *reinterpret_cast<const h8*>(m + p * kMat + index * kOperand + at16);
+  };
+  const char* rs = rs2[0];
+  // Row block tt, contraction blocks 2 ss and 2 ss + 1 of a lower triangular matrix.
+  auto lower = [&](int mat, int tt, int ss) {
+    const char* p = rs + (mat * kBlocks + tt * (tt + 1) / 2 + 2 * ss) * kBlockBytes + lane * 8;
+    const h4 x = *reinterpret_cast<const h4*>(p);
+    h4 y = {};
+    if (2 * ss + 1 <= tt) y = *reinterpret_cast<const h4*>(p + kBlockBytes);
+    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto row4 = [&](int row, int tt) {
+    return *reinterpret_cast<const f4*>(rs + rows_at(P) + (row * kQ + 16 * tt + 4 * g) * 4);
+  };
+
+  if (chunks > 0) load(0);
+  for (int64_t c = 0; c < chunks; ++c) {
+    store();
+    rs = rs2[c & 1];
+    end = end_next;
+    // This wave's part of the record is in LDS.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
+    if (c + 1 < chunks) load(c + 1);
     if (mine) {
-      const Act* vp = static_cast<const Act*>(a.v) + first * a.v_stride + int64_t(h) * a.value_dim + col;
-      f4 X[4], O[4];
+      const int64_t first = begin + c * kQ;
+      const int count = len - c * kQ < kQ ? static_cast<int>(len - c * kQ) : kQ;
+      const uint32_t voff = static_cast<uint32_t>(a.v_stride) * es;
+      const uint32_t yoff = static_cast<uint32_t>(a.hv) * a.value_dim * es;
+      const rsrc_t vr = make_rsrc_bounded(
+          const_cast<Act*>(static_cast<const Act*>(a.v) + first * a.v_stride + int64_t(h) * a.value_dim),
+          (count - 1) * voff + a.value_dim * es);
+      const rsrc_t yr = make_rsrc_bounded(
+          static_cast<Act*>(a.y) + (first * a.hv + h) * a.value_dim, (count - 1) * yoff + a.value_dim * es);
+      typename RawOf<Act>::type V[NC][16];
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        f4 p = f4{0.0f, 0.0f, 0.0f, 0.0f}, o = p;
+      for (int z = 0; z < NC; ++z) {
+        // A tile behind the columns reads zeros (never another row's) and stores nothing.
+        const uint32_t v0 = fresh(
+            (col0 + 16 * z < a.value_dim ? (col0 + 16 * z + i) * es : kNoStore) + 4 * g * voff);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          V[z][e] = load_raw_t<Act>(vr, v0 + (16 * (e >> 2) + (e & 3)) * voff);
+      }
+      f4 X[NC][4], O[NC][4];
+      Scale sS[NC];
+      float mS[NC];
+#pragma unroll
+      for (int z = 0; z < NC; ++z) {
+        float m = 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) m = max4(m, S[z][b]);
+        mS[z] = column_max(m);
+        sS[z] = scale_of(mS[z]);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) X[z][tt] = O[z][tt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        h8 hi[NC], lo[NC];
+#pragma unroll
+        for (int z = 0; z < NC; ++z) split8(S[z][2 * kb], S[z][2 * kb + 1], sS[z].up, &hi[z], &lo[z]);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          const h8 k0 = operand(ks, 0, tt * KB + kb), q0 = operand(qs, 0, tt * KB + kb);
+#pragma unroll
+          for (int z = 0; z < NC; ++z) {
+            X[z][tt] = mfma_h(k0, hi[z], X[z][tt]);
+            O[z][tt] = mfma_h(q0, hi[z], O[z][tt]);
+            X[z][tt] = mfma_h(k0, lo[z], X[z][tt]);
+          }
+          if constexpr (P == 2) {
+            const h8 k1 = operand(ks, 1, tt * KB + kb), q1 = operand(qs, 1, tt * KB + kb);
+#pragma unroll
+            for (int z = 0; z < NC; ++z) {
+              X[z][tt] = mfma_h(k1, hi[z], X[z][tt]);
+              O[z][tt] = mfma_h(q1, hi[z], O[z][tt]);
+              O[z][tt] = mfma_h(q0, lo[z], O[z][tt]);
+            }
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // both phases at once would not fit the registers
+      // X, D and the products with them.
+      f4 D[NC][4];
+#pragma unroll
+      for (int z = 0; z < NC; ++z) {
+        float m = 0.0f;
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          const f4 f = row4(kRowX, tt) * sS[z].down;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            X[z][tt][r] = fmaf(-f[r], X[z][tt][r], widen(V[z][4 * tt + r]));
+          m = max4(m, X[z][tt]);
+        }
+        const Scale sX = scale_of(column_max(m));
+        h8 xh[2], xl[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) split8(X[z][2 * s], X[z][2 * s + 1], sX.up, &xh[s], &xl[s]);
+        float md = 0.0f, ms = 0.0f;
+        f4 U[4];
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          f4 e = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int s = 0; s <= tt / 2; ++s) {
+            const h8 t0 = lower(0, tt, s), t1 = lower(1, tt, s);
+            e = mfma_h(t0, xh[s], e);
+            e = mfma_h(t0, xl[s], e);
+            e = mfma_h(t1, xh[s], e);
+          }
+          D[z][tt] = e * (row4(kRowD, tt) * sX.down);
+          U[tt] = D[z][tt] * row4(kRowS, tt);
+          md = max4(md, D[z][tt]);
+          ms = max4(ms, U[tt]);
+        }
+        // Where D is nothing beside S its scale stays within reach of S's.
+        const float least = mS[z] * 0x1p-40f;
+        const Scale sD = scale_of(fmaxf(column_max(md), least));
+        const Scale sU = scale_of(fmaxf(column_max(ms), least));
+        h8 dh[2], dl[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) split8(D[z][2 * s], D[z][2 * s + 1], sD.up, &dh[s], &dl[s]);
+        const float fy = sS[z].down * sD.up, out = a.scale * sD.down * (1.0f / kUp);
+        const uint32_t y0 = fresh(
+            (col0 + 16 * z < a.value_dim ? (col0 + 16 * z + i) * es : kNoStore) + 4 * g * yoff);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          f4 o = O[z][tt] * (row4(kRowY, tt) * fy);
+#pragma unroll
+          for (int s = 0; s <= tt / 2; ++s) {
+            const h8 a0 = lower(2, tt, s);
+            o = mfma_h(a0, dh[s], o);
+            if constexpr (P == 2) {
+              o = mfma_h(a0, dl[s], o);
+              o = mfma_h(lower(3, tt, s), dh[s], o);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            store_buf<Act>(yr, y0 + (16 * tt + r) * yoff, o[r] * out);
+        }
+        h8 uh[2], ul[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) split8(U[2 * s], U[2 * s + 1], sU.up, &uh[s], &ul[s]);
+        const float keep = end * sU.up;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const float4 kf = *reinterpret_cast<const float4*>(&Ks[(16 * tt + i) * KS + 16 * b + 4 * g]);
-          const float4 qf = *reinterpret_cast<const float4*>(&Qs[(16 * tt + i) * KS + 16 * b + 4 * g]);
-          p = mfma4(kf.x, S[b][0], p);
-          o = mfma4(qf.x, S[b][0], o);
-          p = mfma4(kf.y, S[b][1], p);
-          o = mfma4(qf.y, S[b][1], o);
-          p = mfma4(kf.z, S[b][2], p);
-          o = mfma4(qf.z, S[b][2], o);
-          p = mfma4(kf.w, S[b][3], p);
-          o = mfma4(qf.w, S[b][3], o);
-        }
-        const float4 s1 = load4(rec + kOffRows + 16 * tt + 4 * g);
-        const float4 s3 = load4(rec + kOffRows + 128 + 16 * tt + 4 * g);
-        const float f1[4] = {s1.x, s1.y, s1.z, s1.w}, f3[4] = {s3.x, s3.y, s3.z, s3.w};
+          f4 x = S[z][b] * keep;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = 16 * tt + 4 * g + r;
-          const float v = t < count ? load_act(vp, t * a.v_stride) : 0.0f;
-          X[tt][r] = fmaf(-f1[r], p[r], v);
-          O[tt][r] = f3[r] * o[r];
-        }
-      }
-      f4 D[4];
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        D[tt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int st = 0; st <= tt; ++st) {
-          const float4 m = load4(rec + (tt * (tt + 1) / 2 + st) * 256 + lane * 4);
-          D[tt] = mfma4(m.x, X[st][0], D[tt]);
-          D[tt] = mfma4(m.y, X[st][1], D[tt]);
-          D[tt] = mfma4(m.z, X[st][2], D[tt]);
-          D[tt] = mfma4(m.w, X[st][3], D[tt]);
-        }
-      }
-      Act* yp = static_cast<Act*>(a.y) + (first * a.hv + h) * a.value_dim + col;
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-        for (int st = 0; st <= tt; ++st) {
-          const float4 m = load4(rec + kOffA + (tt * (tt + 1) / 2 + st) * 256 + lane * 4);
-          O[tt] = mfma4(m.x, D[st][0], O[tt]);
-          O[tt] = mfma4(m.y, D[st][1], O[tt]);
-          O[tt] = mfma4(m.z, D[st][2], O[tt]);
-          O[tt] = mfma4(m.w, D[st][3], O[tt]);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = 16 * tt + 4 * g + r;
-          if (t < count) store_act(yp, int64_t(t) * a.hv * a.value_dim, O[tt][r]);
-        }
-      }
-      const float end = rec[kOffRows + 192];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) S[b] *= end;
-#pragma unroll
-      for (int ts = 0; ts < 4; ++ts) {
-        const float4 s2 = load4(rec + kOffRows + 64 + 16 * ts + 4 * g);
-        const float d[4] = {D[ts][0] * s2.x, D[ts][1] * s2.y, D[ts][2] * s2.z, D[ts][3] * s2.w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            S[b] = mfma4(Ks[(16 * ts + 4 * g + r) * KS + 16 * b + i], d[r], S[b]);
+          for (int s = 0; s < 2; ++s) {
+            const h8 k0 = operand(kt, 0, 2 * b + s);
+            x = mfma_h(k0, uh[s], x);
+            x = mfma_h(k0, ul[s], x);
+            if constexpr (P == 2) x = mfma_h(operand(kt, 1, 2 * b + s), uh[s], x);
+          }
+          S[z][b] = x * sU.down;
         }
       }
     }
     __syncthreads();
   }
   const int64_t slot_out = a.out_slots ? a.out_slots[n] : n;
-  if (a.state_out && mine && slot_out >= 0 && slot_out < a.out_count) {
+  if (a.state_out && slot_out >= 0 && slot_out < a.out_count) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-      *reinterpret_cast<float4*>(a.state_out + ((slot_out * a.hv + h) * a.value_dim + col) * K +
-                                 16 * b + 4 * g) = make_float4(S[b][0], S[b][1], S[b][2], S[b][3]);
+    for (int z = 0; z < NC; ++z)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        if (col0 + 16 * z < a.value_dim)
+          *reinterpret_cast<f4*>(a.state_out + ((slot_out * a.hv + h) * a.value_dim + col0 + 16 * z + i) * K +
+                                 16 * b + 4 * g) = S[z][b];
   }
 }
 
@@ -535,6 +874,8 @@ __global__ __launch_bounds__(kThreads) void step_kernel(StepArgs a) {
 constexpr int64_t kMaxGrid = 65535;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 
+constexpr int64_t kMaxRow = int64_t(1) << 22;  // elements between two rows
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool product_ok(int64_t a, int64_t b, int64_t* out) {
@@ -556,7 +897,10 @@ axon_status check_shape(const axon_gated_delta_shape* s) {
   const int64_t strides[] = {s->q_stride, s->k_stride, s->v_stride};
   const int64_t own[] = {s->key_heads * s->key_dim, s->key_heads * s->key_dim,
                          s->value_heads * s->value_dim};
+  // The kernels address a chunk's 64 rows with 32-bit byte offsets below 2^31.
+  if (own[0] > kMaxRow || own[2] > kMaxRow) return AXON_ERR_UNSUPPORTED;
   for (int j = 0; j < 3; ++j) {
+    if (strides[j] > kMaxRow) return AXON_ERR_UNSUPPORTED;
     if (strides[j] && (strides[j] < own[j] || strides[j] % 8)) return AXON_ERR_INVALID_ARGUMENT;
     int64_t t;
     if (!product_ok(s->tokens, strides[j] ? strides[j] : own[j], &t)) return AXON_ERR_UNSUPPORTED;
@@ -583,7 +927,8 @@ axon_status check_params(const axon_gated_delta_params* p) {
 int64_t rows_of(const axon_gated_delta_shape* s) { return s->tokens / kQ + s->sequences; }
 
 size_t workspace_of(const axon_gated_delta_shape* s) {
-  return s->tokens ? sizeof(float) * kRecord * size_t(rows_of(s)) * size_t(s->value_heads) : 0;
+  const size_t record = record_bytes(s->act_dtype == AXON_BF16 ? 1 : 2);
+  return s->tokens ? record * size_t(rows_of(s)) * size_t(s->value_heads) : 0;
 }
 
 struct Strides {
@@ -612,14 +957,22 @@ void input_spans(const axon_gated_delta_shape* s, const axon_gated_delta_params*
 }
 
 template <typename Act, int K>
-void launch_scan(const DeltaArgs& a, bool any, hipStream_t st) {
+void launch_scan(DeltaArgs a, bool any, hipStream_t st) {
   if (any) {
     hipLaunchKernelGGL((prep_kernel<Act, K>), dim3(unsigned(a.rows), unsigned(a.hk)), dim3(kThreads),
                        0, st, a);
   }
-  const int64_t heads8 = (int64_t(a.sequences) * a.hv + 7) / 8 * 8;
-  hipLaunchKernelGGL((walk_kernel<Act, K>), dim3(unsigned(heads8 * a.col_groups)), dim3(kThreads), 0,
-                     st, a);
+  // Two column tiles a wave halve what is read from LDS for each product; one tile spreads the
+  // columns over twice the workgroups.
+  const int64_t heads = int64_t(a.sequences) * a.hv;
+  const int64_t heads8 = (heads + 7) / 8 * 8;
+  const bool two = a.value_dim > 64 && heads >= 256;
+  a.col_groups = two ? (a.value_dim + 127) / 128 : (a.value_dim + 63) / 64;
+  const dim3 grid(unsigned(heads8 * a.col_groups));
+  if (two)
+    hipLaunchKernelGGL((walk_kernel<Act, K, 2>), grid, dim3(kThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((walk_kernel<Act, K, 1>), grid, dim3(kThreads), 0, st, a);
 }
 
 template <typename Act, int K>
@@ -714,13 +1067,12 @@ axon_status axon_gated_delta_scan(const axon_gated_delta_shape* shape,
     a.block_first = a.block_seq + rows;
   }
   a.state_in = state_in, a.in_slots = in_slots, a.y = y, a.state_out = state_out;
-  a.out_slots = out_slots, a.records = static_cast<float*>(workspace);
+  a.out_slots = out_slots, a.records = static_cast<char*>(workspace);
   const Strides st = strides_of(shape);
   a.tokens = s.tokens, a.q_stride = st.q, a.k_stride = st.k, a.v_stride = st.v;
   a.in_count = s.state_slots, a.out_count = s.out_slots;
   a.sequences = int(s.sequences), a.hk = int(s.key_heads), a.hv = int(s.value_heads);
   a.ratio = int(s.value_heads / s.key_heads), a.value_dim = int(s.value_dim);
-  a.col_groups = int((s.value_dim + 63) / 64);
   a.seqlen = s.tokens / s.sequences;
   a.chunks_per_seq = int((a.seqlen + kQ - 1) / kQ);
   a.rows = int(tables ? rows : s.sequences * a.chunks_per_seq);
