@@ -7,9 +7,9 @@
 //   E_t + sum_{s<t} e^{g_t-g_s} (k^_t.k^_s) beta_s E_s = X_t = v_t - e^{g_t} S0 k^_t.
 // The inverse T of its matrix I + M does not depend on the state, so it is computed for all chunks
 // at once; the walk over the chunks is products only:
-//   X = v - e^g (S0 k^),  D = diag(beta) T X,
-//   y = scale (e^g S0 q^ + A D),  A[t,s] = e^{g_t-g_s} q^_t.k^_s (s <= t),
-//   S <- e^{g_last} S0 + sum_t e^{g_last-g_t} D_t k^_t^T.
+//   X = v - e^g (S0 k^),  E = T X,
+//   y = scale (e^g S0 q^ + A E),  A[t,s] = e^{g_t-g_s} (q^_t.k^_s) beta_s (s <= t),
+//   S <- e^{g_last} S0 + sum_t e^{g_last-g_t} beta_t E_t k^_t^T.
 // Every exponent is <= 0; the sums are compensated (head and tail) because steps near dt_max push
 // g to thousands, where the plain fp32 sum's ulp would be the error of later differences. The
 // norms of q and k multiply rows of the products instead of the operands.
@@ -22,15 +22,19 @@
 //                (S^T, K x 16): the result layout of a 16 x 16 product (lane (g, i), g = lane / 16,
 //                i = lane % 16: rows 4 g + r, column i) is also the layout of the next product's
 //                right operand when 32 contraction indices are dealt to (g, e) as 4 g + e for
-//                e < 4 and 16 + 4 g + e - 4 above, so state, X and D go from product to product
+//                e < 4 and 16 + 4 g + e - 4 above, so state, X and E go from product to product
 //                without leaving their lanes.
 //
 // Precision. fp32 products would run at a sixteenth of the fp16 matrix rate, so the walk splits
-// each fp32 operand into fp16 pieces, x 2^s = hi + lo, with s per row of q and k and per column of
-// S, X and D such that the largest value lies in [2^13, 2^14): two pieces hold 22 bits, and what is
-// below 2^-27 of the largest is lost, so a product of pieces is as exact as an fp32 one. bf16 keys
-// and queries are exact in one piece. The states, every accumulator and every factor are fp32. For
-// bf16 activations the operands that only y sees (S, A and D of its two products) are one piece, 11
+// each fp32 operand into two fp16 pieces, x = hi + lo: 22 bits of x, and 2^-25 of one at least. A
+// product of pieces (hi hi + hi lo + lo hi) is then as exact as an fp32 one if the operands lie near
+// one: T and A are at most 1; rows of k and q are scaled by a power of two that takes their largest
+// entry to [1, 2) (bf16 entries are then exact in one piece); each column of S, with what the chunk
+// makes of its v (X, E and the writes), is kept in a unit of its own, a power of two that takes the
+// larger of S and v to about 2^5. By the contraction of the delta rule (0 <= beta <= 1) no entry of
+// S, X or E exceeds 2^8 sqrt(K) + 64 2^8 < 2^15 before the next chunk looks at the unit again, so
+// nothing leaves the range of fp16. The states, every accumulator and every factor are fp32. For
+// bf16 activations the operands that only y sees (S, A and E of its two products) are one piece, 11
 // bits: 2^-12 against the 2^-9 of y's own rounding.
 #include <hip/hip_runtime.h>
 
@@ -45,6 +49,7 @@ namespace {
 
 constexpr int kQ = 64;  // tokens of a chunk
 constexpr int kThreads = 256;
+constexpr int kWalkThreads = 512;
 constexpr int kMS = kQ + 4;  // LDS row stride of 64 x 64 matrices
 
 typedef float f4 __attribute__((ext_vector_type(4)));
@@ -55,19 +60,17 @@ constexpr int kPieces = sizeof(Act) == 2 ? 1 : 2;
 
 // What prep leaves for each (chunk, value head): T in two pieces and A in one or two, each as ten
 // 16 x 16 blocks on and below the diagonal (block I (I + 1) / 2 + J), a block as 64 lanes x 4 fp16
-// in left-operand order (lane (g, i): row i, columns 4 g .. 4 g + 3), both times 2^12; then the row
+// in left-operand order (lane (g, i): row i, columns 4 g .. 4 g + 3); then the row
 // factors of the 64 tokens, fp32, and e^{g_last}. What the walk keeps in LDS comes first.
 constexpr int kBlocks = 10;
 constexpr int kBlockBytes = 512;
-constexpr float kUp = 4096.0f;  // |T|, |A| <= 1: their pieces stay normal fp16 numbers
-enum Row { kRowX, kRowD, kRowS, kRowY, kRowK, kRowQ, kRows };
-//   kRowX  e^g / |k| / 2^s      of S0 k in X (s: the shift of k)
-//   kRowD  beta / 2^12          of T X in D
-//   kRowS  e^{g_last-g} / |k| / 2^s   of D in the state's sum
-//   kRowY  e^g / |q| / 2^s 2^12       of S0 q in y
-//   kRowK, kRowQ  the shifts of k and q: fp32 2^s, bf16 what is taken off both exponents of a pair
+enum Row { kRowX, kRowS, kRowY, kRowKQ, kRows = kRowKQ + 2 };
+//   kRowX  e^g / |k| / 2^s                 of S0 k in X (2^s: the scale of k's row)
+//   kRowS  beta e^{g_last-g} / |k| / 2^s   of E in the state's sum
+//   kRowY  e^g / |q| / 2^s                 of S0 q in y
+//   kRowKQ 2^s of k and of q, in pairs
 constexpr int rows_at(int pieces) { return (2 + pieces) * kBlocks * kBlockBytes; }
-constexpr int lds_bytes(int pieces) { return rows_at(pieces) + kRowK * kQ * 4; }
+constexpr int lds_bytes(int pieces) { return rows_at(pieces) + 4 * kQ * 4; }
 constexpr int record_bytes(int pieces) { return rows_at(pieces) + kRows * kQ * 4 + 64; }
 
 struct DeltaArgs {
@@ -137,70 +140,71 @@ typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef uint16_t u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t w2 __attribute__((ext_vector_type(2)));
 typedef uint32_t w4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f4 mfma_h(h8 a, h8 b, f4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// 2^s that takes m to [2^13, 2^14), and its inverse; the exponent is held to where both are normal.
+// 2^s that takes m to [1, 2), and its inverse; m is held to [2^-97, 2^123], where both are normal
+// numbers.
 struct Scale {
   float up, down;
 };
 __device__ __forceinline__ Scale scale_of(float m) {
   int e = static_cast<int>(__float_as_uint(m) >> 23);
   e = e < 30 ? 30 : e > 250 ? 250 : e;
-  return {__uint_as_float(static_cast<uint32_t>(267 - e) << 23),
-          __uint_as_float(static_cast<uint32_t>(e - 13) << 23)};
-}
-// bf16: what is taken off a pair's exponents so that the largest becomes fp16's 28 (2^13), and the
-// inverse of that shift. x 2^(112 - off) is exact in fp16 down to 2^-27 of the largest.
-__device__ __forceinline__ uint32_t pair_shift(float m) {
-  const uint32_t e = __float_as_uint(m) >> 23;
-  const uint32_t off = e > 28 ? e - 28 : 0;
-  return off << 7 | off << 23;
-}
-__device__ __forceinline__ float pair_unshift(uint32_t pair) {
-  return __uint_as_float((((pair >> 7) & 0xFF) + 15) << 23);
-}
-__device__ __forceinline__ uint32_t pair_to_fp16(uint32_t x, uint32_t pair) {
-  const u2 mag = __builtin_bit_cast(u2, x & 0x7FFF7FFFu);
-  u2 r = __builtin_elementwise_sub_sat(mag, __builtin_bit_cast(u2, pair));
-  r = r << static_cast<uint16_t>(3);
-  return (x & 0x80008000u) | __builtin_bit_cast(uint32_t, r);
+  return {__uint_as_float(static_cast<uint32_t>(254 - e) << 23),
+          __uint_as_float(static_cast<uint32_t>(e) << 23)};
 }
 
-// Four activations as loaded, and their fp16 pieces.
+// Eight activations as loaded, and their fp16 pieces.
 template <typename Act>
-struct Four;
+struct Eight;
 template <>
-struct Four<bf16_bits> {
-  uint2 raw;
+struct Eight<bf16_bits> {
+  w4 raw;
   __device__ __forceinline__ void load(rsrc_t r, uint32_t off) {
-    raw = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+    raw = __builtin_bit_cast(w4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
   }
-  __device__ __forceinline__ void pieces(uint32_t shift, uint2* out) const {
-    out[0] = make_uint2(pair_to_fp16(raw.x, shift), pair_to_fp16(raw.y, shift));
+  __device__ __forceinline__ void pieces(float up, w4* out) const {
+    f4 a, b;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      a[2 * e] = __uint_as_float(raw[e] << 16) * up;
+      a[2 * e + 1] = __uint_as_float(raw[e] & 0xFFFF0000u) * up;
+      b[2 * e] = __uint_as_float(raw[e + 2] << 16) * up;
+      b[2 * e + 1] = __uint_as_float(raw[e + 2] & 0xFFFF0000u) * up;
+    }
+    out[0] = __builtin_bit_cast(
+        w4, __builtin_shufflevector(__builtin_convertvector(a, h4), __builtin_convertvector(b, h4), 0,
+                                    1, 2, 3, 4, 5, 6, 7));
   }
 };
 template <>
-struct Four<float> {
-  f4 raw;
+struct Eight<float> {
+  f4 lo, hi;
   __device__ __forceinline__ void load(rsrc_t r, uint32_t off) {
-    raw = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    lo = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    hi = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 16, 0, 0));
   }
-  __device__ __forceinline__ void pieces(uint32_t shift, uint2* out) const {
-    const f4 x = raw * __uint_as_float(shift);
-    const h4 hi = __builtin_convertvector(x, h4);
-    const h4 lo = __builtin_convertvector(x - __builtin_convertvector(hi, f4), h4);
-    out[0] = __builtin_bit_cast(uint2, hi);
-    out[1] = __builtin_bit_cast(uint2, lo);
+  __device__ __forceinline__ void pieces(float up, w4* out) const {
+    const f4 a = lo * up, b = hi * up;
+    const h4 ha = __builtin_convertvector(a, h4), hb = __builtin_convertvector(b, h4);
+    const h4 la = __builtin_convertvector(a - __builtin_convertvector(ha, f4), h4);
+    const h4 lb = __builtin_convertvector(b - __builtin_convertvector(hb, f4), h4);
+    out[0] = __builtin_bit_cast(w4, __builtin_shufflevector(ha, hb, 0, 1, 2, 3, 4, 5, 6, 7));
+    out[1] = __builtin_bit_cast(w4, __builtin_shufflevector(la, lb, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 };
 
-// Two pieces of eight values (two accumulators of one column) times a scale.
-__device__ __forceinline__ void split8(f4 a, f4 b, float up, h8* hi, h8* lo) {
-  a *= up, b *= up;
+// Two pieces of eight values (two accumulators of one column).
+__device__ __forceinline__ h8 first_piece(f4 a, f4 b) {
+  return __builtin_shufflevector(__builtin_convertvector(a, h4), __builtin_convertvector(b, h4), 0, 1,
+                                 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ void split8(f4 a, f4 b, h8* hi, h8* lo) {
   const h4 ha = __builtin_convertvector(a, h4), hb = __builtin_convertvector(b, h4);
   const h4 la = __builtin_convertvector(a - __builtin_convertvector(ha, f4), h4);
   const h4 lb = __builtin_convertvector(b - __builtin_convertvector(hb, f4), h4);
@@ -208,10 +212,29 @@ __device__ __forceinline__ void split8(f4 a, f4 b, float up, h8* hi, h8* lo) {
   *lo = __builtin_shufflevector(la, lb, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// 16 lanes read 4 rows x 16 fp16 (lane j: row j / 4, columns 4 (j % 4) ..) and lane j gets column j.
+__device__ __forceinline__ h4 read_transposed(const char* p) {
+  typedef short s4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(
+      h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p));
+}
+
 // The value, computed anew where it is used: sums with it are not kept in registers across a loop.
 __device__ __forceinline__ uint32_t fresh(uint32_t v) {
   asm volatile("" : "+v"(v));
   return v;
+}
+
+// 16 bytes a lane from `base + off` to the wave's consecutive 1024 bytes at `to` in LDS. Written out
+// because the compiler would wait for the copy before any read of LDS, also of another buffer; the
+// caller waits for it (no register is written).
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, char* to) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)to)));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(m0), "v"(off), "s"(base)
+               : "m0", "memory");
 }
 
 // The largest over the four lanes (g = 0 .. 3) that share a column.
@@ -361,22 +384,12 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
       hi_s[lane] = hi, lo_s[lane] = lo, beta_s[lane] = beta;
       const float last_hi = __shfl(hi, 63, 64), last_lo = __shfl(lo, 63, 64);
       const float e = __builtin_amdgcn_exp2f(hi + lo);
-      float ku, kd, qu, qd;  // the shifts as the walk takes them, and their inverses
-      if constexpr (P == 1) {
-        const uint32_t k2 = pair_shift(mk_s[lane]), q2 = pair_shift(mq_s[lane]);
-        ku = __uint_as_float(k2), kd = pair_unshift(k2);
-        qu = __uint_as_float(q2), qd = pair_unshift(q2);
-      } else {
-        const Scale k2 = scale_of(mk_s[lane]), q2 = scale_of(mq_s[lane]);
-        ku = k2.up, kd = k2.down, qu = q2.up, qd = q2.down;
-      }
+      const Scale k2 = scale_of(mk_s[lane]), q2 = scale_of(mq_s[lane]);
       float* row = reinterpret_cast<float*>(rec + rows_at(P)) + lane;
-      row[kRowX * kQ] = e * (rk_s[lane] * kd);
-      row[kRowD * kQ] = beta * (1.0f / kUp);
-      row[kRowS * kQ] = exp2_diff(last_hi, last_lo, hi, lo) * (rk_s[lane] * kd);
-      row[kRowY * kQ] = e * (rq_s[lane] * qd) * kUp;
-      row[kRowK * kQ] = ku;
-      row[kRowQ * kQ] = qu;
+      row[kRowX * kQ] = e * (rk_s[lane] * k2.down);
+      row[kRowS * kQ] = beta * exp2_diff(last_hi, last_lo, hi, lo) * (rk_s[lane] * k2.down);
+      row[kRowY * kQ] = e * (rq_s[lane] * q2.down);
+      *reinterpret_cast<float2*>(row + kRowKQ * kQ + lane) = make_float2(k2.up, q2.up);
       if (lane == 63) row[kRows * kQ - 63] = e;
     }
     __syncthreads();
@@ -384,12 +397,12 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
     for (int st = 0; st < 4; ++st) {
       if (st > w) continue;
       const int s = 16 * st + i;
-      const float hs = hi_s[s], ls = lo_s[s], rks = rk_s[s], bs = beta_s[s];
+      const float hs = hi_s[s], ls = lo_s[s], rks = rk_s[s] * beta_s[s];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * w + 4 * g + r;
         const float e = exp2_diff(hi_s[t], lo_s[t], hs, ls) * rks;
-        Ms[t * kMS + s] = s < t ? bs * rk_s[t] * e * gk[st][r] : 0.0f;
+        Ms[t * kMS + s] = s < t ? rk_s[t] * e * gk[st][r] : 0.0f;
         As[t * kMS + s] = s <= t ? rq_s[t] * e * gq[st][r] : 0.0f;
       }
     }
@@ -449,7 +462,7 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
       const int I = bb < 1 ? 0 : bb < 3 ? 1 : bb < 6 ? 2 : 3;
       const int J = bb - I * (I + 1) / 2;
       const float* src = (is_t ? Ms : As) + (16 * I + i) * kMS + 16 * J + 4 * g;
-      const f4 x = *reinterpret_cast<const f4*>(src) * kUp;
+      const f4 x = *reinterpret_cast<const f4*>(src);
       const h4 hi = __builtin_convertvector(x, h4);
       char* dst = rec + ((is_t ? 0 : 2 * kBlocks) + bb) * kBlockBytes + lane * 8;
       *reinterpret_cast<h4*>(dst) = hi;
@@ -461,33 +474,47 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
 }
 
 // ---- the walk over the chunks -------------------------------------------------------------------
-// 4 waves a workgroup, each with NC tiles of 16 columns of V. Per chunk the workgroup brings k (as
-// left operand of S k^ and, transposed, of the state's sum), q and the chunk's record into LDS in
-// operand order, so that a wave reads whole 1 KiB operands without bank conflicts: operand (block
-// of 16 rows, 32 contraction indices) holds lane (g, i)'s eight fp16 at 16 (16 g + (i ^ g)); the
-// exclusive or spreads the writers, who own 4 tokens x 4 channels each, over the banks. The next
-// chunk's rows travel in registers meanwhile.
-template <typename Act, int K, int NC>
-__global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 2 : 1) void walk_kernel(DeltaArgs a) {
+// 8 waves a workgroup, each with NC tiles of 16 columns of V; HV value heads of one key head share
+// what is brought of k and q. Per chunk the workgroup brings k and q, converted to fp16 pieces on
+// the way, as rows of K fp16 (read as left operand of S k^ and S q^, and k by transposing reads as
+// left operand of the state's sum) and each head's record. Both have two buffers (fp32: k and q
+// one), and the next chunk's rows travel in registers while this one's are used.
+//
+// Row i of tile b of the transposed state is channel 32 (b / 2) + 8 (i / 4) + 4 (b % 2) + i % 4, so
+// that a lane's eight values of two tiles are eight channels in a row: 16 bytes of a k or q row.
+// Those rows would all begin in the same bank: the 16-byte piece c of token t lies at c ^ swizzle(t),
+// which spreads both the 16 rows of an operand and the 4 rows x 4 pieces of a transposing read.
+template <int K>
+__device__ __forceinline__ int swizzle(int t) {
+  return K == 128 ? (t & 3) << 2 | ((t >> 2) & 3) : (t & 2) << 1 | ((t >> 2) & 3);
+}
+
+template <typename Act, int K, int HV, int NC>
+__global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(DeltaArgs a) {
   constexpr int P = kPieces<Act>;
   constexpr int NB = K / 16, KB = K / 32;
-  constexpr int kOperand = 1024, kMat = 4 * KB * kOperand;  // one piece of k or q of a chunk
-  constexpr int kRec = record_bytes(P), kLds = lds_bytes(P);
+  constexpr int kRow = 2 * K, kMat = kQ * kRow;  // bytes of a row, of one piece of k or q of a chunk
+  constexpr int kRec = record_bytes(P), kLds = lds_bytes(P), kLoads = kLds / 1024;
+  constexpr int kWaves = kWalkThreads / 64, kPerHead = kWaves / HV;
+  constexpr int kBufs = P == 1 ? 2 : 1;                    // of k and q
+  constexpr int kUnits = kQ * K / 8 / kWalkThreads;        // 16-byte pieces of k (and q) a thread brings
   static_assert(kLds % 1024 == 0, "whole wave loads");
-  constexpr int kUnits = K / 64;  // 4 x 4 blocks of k (and q) a thread brings
-  __shared__ __align__(16) char ks[P * kMat];
-  __shared__ __align__(16) char kt[P * kMat];
-  __shared__ __align__(16) char qs[P * kMat];
-  __shared__ __align__(16) char rs2[2][kLds];
+  __shared__ __align__(16) char ks[kBufs][P * kMat];
+  __shared__ __align__(16) char qs[kBufs][P * kMat];
+  __shared__ __align__(16) char rs2[2][HV][kLds];
+  __shared__ __align__(16) char vs[kWaves][kQ * 16 * NC * sizeof(Act)];
 
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-  const int64_t nh = int64_t(slot / a.col_groups) * 8 + xcd;
-  if (nh >= int64_t(a.sequences) * a.hv) return;
-  const int n = static_cast<int>(nh / a.hv), h = static_cast<int>(nh - int64_t(n) * a.hv);
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, i = lane & 15;
-  const int col0 = ((slot % a.col_groups) * 4 + w) * 16 * NC;
-  const bool mine = col0 < a.value_dim;  // wave-uniform: V is a multiple of 16
+  const int groups = a.hv / HV;
+  const int64_t ng = int64_t(slot / a.col_groups) * 8 + xcd;
+  if (ng >= int64_t(a.sequences) * groups) return;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, i = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = static_cast<int>(ng / groups);
+  const int hl = w / kPerHead;  // this wave's head of the workgroup
+  const int h = static_cast<int>(ng - int64_t(n) * groups) * HV + hl;
   const int hk = h / a.ratio;
+  const int col0 = ((slot % a.col_groups) * kPerHead + w % kPerHead) * 16 * NC;
   int64_t begin, len, row0;
   if (a.starts) {
     begin = a.starts[n];
@@ -501,34 +528,37 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 2 : 1) void walk_kerne
   int64_t chunks = len > 0 ? (len + kQ - 1) / kQ : 0;
   if (chunks > a.rows - row0) chunks = a.rows - row0;
 
+  // The state in units of its columns: S / unit.
   f4 S[NC][NB];
-  {
-    const int64_t slot_in = a.in_slots ? a.in_slots[n] : n;
-    const bool have = a.state_in && slot_in >= 0 && slot_in < a.in_count;
+  float unit[NC], inverse[NC];
+  f4 out4[NC];  // scale * unit of the columns 4 g + r, for y
+  // Element (z, b, r) is row 32 (b / 2) + 8 g + 4 (b % 2) + r of column col0 + 16 z + i.
+  const int64_t slot_in = a.in_slots ? a.in_slots[n] : n;
+  const bool have = a.state_in && slot_in >= 0 && slot_in < a.in_count;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+  for (int z = 0; z < NC; ++z) {
+    unit[z] = inverse[z] = 1.0f;
+    out4[z] = f4{a.scale, a.scale, a.scale, a.scale};
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int col = col0 + 16 * c + i;
-        S[c][b] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (have && col0 + 16 * c < a.value_dim)
-          S[c][b] = *reinterpret_cast<const f4*>(
-              a.state_in + ((slot_in * a.hv + h) * a.value_dim + col) * K + 16 * b + 4 * g);
-      }
+    for (int b = 0; b < NB; ++b) {
+      S[z][b] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (have && col0 + 16 * z < a.value_dim)
+        S[z][b] = *reinterpret_cast<const f4*>(
+            a.state_in + ((slot_in * a.hv + h) * a.value_dim + col0 + 16 * z + i) * K + 32 * (b >> 1) +
+            8 * g + 4 * (b & 1));
+    }
   }
 
-  // What this thread brings: tokens 4 tau .. + 3, channels 4 kappa .. + 3.
-  const int tau = (w >> 1) * 8 + ((lane >> 3) & 3) + 4 * (lane >> 5);
-  const int kap0 = (lane & 7) + 8 * (K == 128 ? 2 * (w & 1) : (w & 1));
-  Four<Act> pk[kUnits][4], pq[kUnits][4];
-  w4 shk, shq;
+  constexpr uint32_t es = sizeof(Act);
+  // This thread brings pieces tid, tid + 512, ... of the chunk's rows (K / 8 pieces a row).
+  Eight<Act> pk[kUnits], pq[kUnits];
+  float2 sh[kUnits];
   float end = 0.0f, end_next = 0.0f;
-  const uint32_t es = sizeof(Act);
-  const uint32_t koff = static_cast<uint32_t>(a.k_stride) * es, qoff = static_cast<uint32_t>(a.q_stride) * es;
   // Rows behind the sequence lie outside the resource's range and read as zeros.
-  auto load = [&](int64_t c) {
+  auto load = [&](int64_t c, int buf) {
     const int64_t first = begin + c * kQ;
     const int count = len - c * kQ < kQ ? static_cast<int>(len - c * kQ) : kQ;
+    const uint32_t koff = static_cast<uint32_t>(a.k_stride) * es, qoff = static_cast<uint32_t>(a.q_stride) * es;
     const rsrc_t kr = make_rsrc_bounded(
         const_cast<Act*>(static_cast<const Act*>(a.k) + first * a.k_stride + int64_t(hk) * K),
         (count - 1) * koff + K * es);
@@ -537,69 +567,107 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 2 : 1) void walk_kerne
         (count - 1) * qoff + K * es);
     const char* rec = a.records + ((row0 + c) * a.hv + h) * int64_t(kRec);
     // The record goes to LDS without passing through registers, 1 KiB a wave and instruction.
-    for (int u = w; u < kLds / 1024; u += 4)
-      __builtin_amdgcn_global_load_lds(
-          reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(
-              reinterpret_cast<uintptr_t>(rec + u * 1024 + lane * 16)),
-          (__attribute__((address_space(3))) uint32_t*)(&rs2[c & 1][u * 1024]), 16, 0, 0);
-    const char* rows = rec + rows_at(P) + 16 * tau;
+    // (Where the pieces are no multiple of the waves, the last one is brought more than once.)
+#pragma unroll
+    for (int u0 = 0; u0 < kLoads; u0 += kPerHead) {
+      const int u = min(u0 + w % kPerHead, kLoads - 1);
+      load_to_lds(rec + u * 1024, lane * 16, &rs2[buf][hl][u * 1024]);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // before the loads below: see the wait in the loop
     end_next = *reinterpret_cast<const float*>(rec + rows_at(P) + kRows * kQ * 4);
-    shk = *reinterpret_cast<const w4*>(rows + kRowK * kQ * 4);
-    shq = *reinterpret_cast<const w4*>(rows + kRowQ * kQ * 4);
-    const uint32_t k0 = fresh(4 * (tau * koff + kap0 * es)), q0 = fresh(4 * (tau * qoff + kap0 * es));
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        pk[u][j].load(kr, k0 + j * koff + 32 * es * u);
-        pq[u][j].load(qr, q0 + j * qoff + 32 * es * u);
-      }
-  };
-  auto store = [&]() {
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-      const int kap = kap0 + 8 * u;
-      // as rows: operand (tau / 4, kappa / 8), lane group kappa % 4, half (kappa / 4) % 2
-      const int rbase = ((tau >> 2) * KB + (kap >> 3)) * kOperand + (kap & 3) * 256 + ((kap >> 2) & 1) * 8;
-      // transposed: operand (kappa / 4, tau / 8), lane group tau % 4, half (tau / 4) % 2
-      const int cbase = ((kap >> 2) * 2 + (tau >> 3)) * kOperand + (tau & 3) * 256 + ((tau >> 2) & 1) * 8;
-      uint2 pc[4][P];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        pq[u][j].pieces(shq[j], pc[j]);
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-          *reinterpret_cast<uint2*>(qs + p * kMat + rbase + ((4 * (tau & 3) + j) ^ (kap & 3)) * 16) = pc[j][p];
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        pk[u][j].pieces(shk[j], pc[j]);
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-          *reinterpret_cast<uint2*>(ks + p * kMat + rbase + ((4 * (tau & 3) + j) ^ (kap & 3)) * 16) = pc[j][p];
-      }
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        uint2 c[4];
-        c[0] = make_uint2(__builtin_amdgcn_perm(pc[1][p].x, pc[0][p].x, 0x05040100),
-                          __builtin_amdgcn_perm(pc[3][p].x, pc[2][p].x, 0x05040100));
-        c[1] = make_uint2(__builtin_amdgcn_perm(pc[1][p].x, pc[0][p].x, 0x07060302),
-                          __builtin_amdgcn_perm(pc[3][p].x, pc[2][p].x, 0x07060302));
-        c[2] = make_uint2(__builtin_amdgcn_perm(pc[1][p].y, pc[0][p].y, 0x05040100),
-                          __builtin_amdgcn_perm(pc[3][p].y, pc[2][p].y, 0x05040100));
-        c[3] = make_uint2(__builtin_amdgcn_perm(pc[1][p].y, pc[0][p].y, 0x07060302),
-                          __builtin_amdgcn_perm(pc[3][p].y, pc[2][p].y, 0x07060302));
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint2*>(kt + p * kMat + cbase + ((4 * (kap & 3) + j) ^ (tau & 3)) * 16) = c[j];
-      }
+      const int at = tid + u * kWalkThreads, t = at / (K / 8), piece = at % (K / 8);
+      const uint32_t ko = fresh(t * koff + piece * 8 * es), qo = fresh(t * qoff + piece * 8 * es);
+      sh[u] = *reinterpret_cast<const float2*>(rec + rows_at(P) + kRowKQ * kQ * 4 + t * 8);
+      pk[u].load(kr, ko);
+      pq[u].load(qr, qo);
     }
   };
-  const int at16 = (16 * g + (i ^ g)) * 16;
-  auto operand = [&](const char* m, int p, int index) {
-    return *reinterpret_cast<const h8*>(m + p * kMat + index * kOperand + at16);
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int at = tid + u * kWalkThreads, t = at / (K / 8), piece = at % (K / 8);
+      const int to = t * kRow + (piece ^ swizzle<K>(t)) * 16;
+      w4 out[P];
+      pk[u].pieces(sh[u].x, out);
+#pragma unroll
+      for (int p = 0; p < P; ++p) *reinterpret_cast<w4*>(&ks[buf][p * kMat + to]) = out[p];
+      pq[u].pieces(sh[u].y, out);
+#pragma unroll
+      for (int p = 0; p < P; ++p) *reinterpret_cast<w4*>(&qs[buf][p * kMat + to]) = out[p];
+    }
   };
-  const char* rs = rs2[0];
+  // This wave's columns of a chunk's v go to LDS as rows of 16 NC values (only this wave reads them):
+  // 16-byte pieces, those of rows behind the sequence from its last row (their factors are zeros).
+  // fp32 rows lie in the order that puts rows 4 g + r of one r in different banks.
+  char* const vw = vs[w];
+  auto load_v = [&](int64_t c) {
+    const int64_t first = begin + c * kQ;
+    const int count = len - c * kQ < kQ ? static_cast<int>(len - c * kQ) : kQ;
+    const char* from = static_cast<const char*>(a.v) +
+                       (first * a.v_stride + int64_t(h) * a.value_dim) * int64_t(es);
+    constexpr int kPieces16 = NC * static_cast<int>(sizeof(Act));  // 16-byte pieces of a row
+    constexpr int kRowsPer = 64 / kPieces16;
+#pragma unroll
+    for (int j = 0; j < kQ / kRowsPer; ++j) {
+      const int at = lane / kPieces16;
+      const int t = es == 2 ? j * kRowsPer + at : j * kRowsPer + 4 * (at & 3) + (at >> 2);
+      const int colb = min((col0 * static_cast<int>(es)) + (lane % kPieces16) * 16, a.value_dim * static_cast<int>(es) - 16);
+      load_to_lds(from, fresh(min(t, count - 1) * static_cast<uint32_t>(a.v_stride) * es + colb),
+                  vw + j * 1024);
+    }
+  };
+  // Rows 16 tt + 4 g .. + 3 of column 16 z + i.
+  auto v4 = [&](int z, int tt) {
+    f4 v;
+    if constexpr (P == 1) {
+      const w2 x = __builtin_bit_cast(
+          w2, read_transposed(vw + (16 * tt + 4 * g + (i >> 2)) * 32 * NC + 32 * z + (i & 3) * 8));
+      v[0] = __uint_as_float(x[0] << 16);
+      v[1] = __uint_as_float(x[0] & 0xFFFF0000u);
+      v[2] = __uint_as_float(x[1] << 16);
+      v[3] = __uint_as_float(x[1] & 0xFFFF0000u);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        v[r] = *reinterpret_cast<const float*>(vw + (16 * tt + 4 * r + g) * 64 * NC + 64 * z + 4 * i);
+    }
+    return v;
+  };
+  // y is computed transposed (rows: 4 columns 4 g + r, column: token i), so that a lane stores four
+  // values in a row. Rows behind the sequence and columns behind V lie outside the range.
+  const int64_t y_stride = int64_t(a.hv) * a.value_dim;
+  const uint32_t yoff = (i * static_cast<uint32_t>(y_stride) + col0 + 4 * g) * es;
+  auto store_y = [&](int64_t c, int z, int tt, f4 o) {
+    const int64_t first = begin + c * kQ;
+    const int left = (len - c * kQ < kQ ? static_cast<int>(len - c * kQ) : kQ) - 16 * tt;
+    const rsrc_t yr = make_rsrc_bounded(
+        static_cast<char*>(a.y) + ((first + 16 * tt) * y_stride + int64_t(h) * a.value_dim) * int64_t(es),
+        left > 0 ? ((left - 1) * static_cast<uint32_t>(y_stride) + a.value_dim) * es : 0);
+    const uint32_t off = col0 + 16 * z < a.value_dim ? yoff + 16 * z * es : kNoStore;
+    if constexpr (P == 1) {
+      const w2 v = {f32_to_bf16(o[0]) | static_cast<uint32_t>(f32_to_bf16(o[1])) << 16,
+                    f32_to_bf16(o[2]) | static_cast<uint32_t>(f32_to_bf16(o[3])) << 16};
+      __builtin_amdgcn_raw_buffer_store_b64(v, yr, off, 0, 0);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(w4, o), yr, off, 0, 0);
+    }
+  };
+  // Left operand: rows 16 tt + i, channels 32 kb + 8 g .. + 7.
+  const int srow = i * kRow, sw = swizzle<K>(i);
+  auto operand = [&](const char* m, int p, int tt, int kb) {
+    return *reinterpret_cast<const h8*>(m + p * kMat + tt * 16 * kRow + srow + ((4 * kb + g) ^ sw) * 16);
+  };
+  // Left operand: rows of state tile b, tokens 32 s + 4 g + e and 32 s + 16 + 4 g + e. The 16 lanes
+  // of group g read 4 tokens x 16 channels, and each gets its own channel's 4 tokens.
+  const int trow = (4 * g + (i >> 2)) * kRow, tsw = swizzle<K>(4 * g + (i >> 2));
+  auto transposed = [&](const char* m, int p, int b, int s) {
+    const char* at = m + p * kMat + s * 32 * kRow + trow + ((4 * (b >> 1) + (i & 3)) ^ tsw) * 16 + (b & 1) * 8;
+    const h4 x = read_transposed(at), y = read_transposed(at + 16 * kRow);
+    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  const char* rs = rs2[0][0];
   // Row block tt, contraction blocks 2 ss and 2 ss + 1 of a lower triangular matrix.
   auto lower = [&](int mat, int tt, int ss) {
     const char* p = rs + (mat * kBlocks + tt * (tt + 1) / 2 + 2 * ss) * kBlockBytes + lane * 8;
@@ -612,154 +680,152 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 2 : 1) void walk_kerne
     return *reinterpret_cast<const f4*>(rs + rows_at(P) + (row * kQ + 16 * tt + 4 * g) * 4);
   };
 
-  if (chunks > 0) load(0);
+  // No branch inside the loop but the loop itself, so that the waits for loads count exactly and
+  // the next chunk's stay in flight: behind the last chunk it is loaded once more (and not used),
+  // and waves without columns run on zeros.
+  if (chunks > 0) {
+    load_v(0);
+    load(0, 0);
+  }
   for (int64_t c = 0; c < chunks; ++c) {
-    store();
-    rs = rs2[c & 1];
+    const int kb2 = kBufs == 2 ? c & 1 : 0;
+    store(kb2);
+    const char *kc = ks[kb2], *qc = qs[kb2];
+    rs = rs2[c & 1][hl];
     end = end_next;
-    // This wave's part of the record is in LDS.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // This wave's parts of the record and v are in LDS: vector memory operations of a wave complete
+    // in the order of their issue, and behind the last of them, v, only y's 4 NC stores were issued.
+    if (NC == 1)
+      asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    // Behind this barrier chunk c is complete in LDS and every wave is done with chunk c - 1, whose
+    // buffers the next chunk takes.
     __syncthreads();
-    if (c + 1 < chunks) load(c + 1);
-    if (mine) {
-      const int64_t first = begin + c * kQ;
-      const int count = len - c * kQ < kQ ? static_cast<int>(len - c * kQ) : kQ;
-      const uint32_t voff = static_cast<uint32_t>(a.v_stride) * es;
-      const uint32_t yoff = static_cast<uint32_t>(a.hv) * a.value_dim * es;
-      const rsrc_t vr = make_rsrc_bounded(
-          const_cast<Act*>(static_cast<const Act*>(a.v) + first * a.v_stride + int64_t(h) * a.value_dim),
-          (count - 1) * voff + a.value_dim * es);
-      const rsrc_t yr = make_rsrc_bounded(
-          static_cast<Act*>(a.y) + (first * a.hv + h) * a.value_dim, (count - 1) * yoff + a.value_dim * es);
-      typename RawOf<Act>::type V[NC][16];
+    const int64_t next = c + 1 < chunks ? c + 1 : c;
+    load(next, (c + 1) & 1);
+    f4 X[NC][4], O[NC][4], v[NC][4];
 #pragma unroll
-      for (int z = 0; z < NC; ++z) {
-        // A tile behind the columns reads zeros (never another row's) and stores nothing.
-        const uint32_t v0 = fresh(
-            (col0 + 16 * z < a.value_dim ? (col0 + 16 * z + i) * es : kNoStore) + 4 * g * voff);
+    for (int z = 0; z < NC; ++z) {
+      float m = 0.0f, ms = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          V[z][e] = load_raw_t<Act>(vr, v0 + (16 * (e >> 2) + (e & 3)) * voff);
-      }
-      f4 X[NC][4], O[NC][4];
-      Scale sS[NC];
-      float mS[NC];
-#pragma unroll
-      for (int z = 0; z < NC; ++z) {
-        float m = 0.0f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) m = max4(m, S[z][b]);
-        mS[z] = column_max(m);
-        sS[z] = scale_of(mS[z]);
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) X[z][tt] = O[z][tt] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int tt = 0; tt < 4; ++tt) {
+        v[z][tt] = v4(z, tt);
+        m = max4(m, v[z][tt]);
       }
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        h8 hi[NC], lo[NC];
+      for (int b = 0; b < NB; ++b) ms = max4(ms, S[z][b]);
+      m = column_max(fmaxf(m, ms * unit[z]));
+      // The unit stays while the column's largest is between 2^2 and 2^8 of it.
+      const float at = m * inverse[z];
+      if (__any(m > 0.0f && !(at >= 0x1p2f && at <= 0x1p8f))) {
+        const Scale to = scale_of(m);
+        const float by = unit[z] * (to.up * 0x1p5f);
+        inverse[z] = to.up * 0x1p5f;
+        unit[z] = to.down * 0x1p-5f;
 #pragma unroll
-        for (int z = 0; z < NC; ++z) split8(S[z][2 * kb], S[z][2 * kb + 1], sS[z].up, &hi[z], &lo[z]);
+        for (int b = 0; b < NB; ++b) S[z][b] *= by;
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          const h8 k0 = operand(ks, 0, tt * KB + kb), q0 = operand(qs, 0, tt * KB + kb);
-#pragma unroll
-          for (int z = 0; z < NC; ++z) {
-            X[z][tt] = mfma_h(k0, hi[z], X[z][tt]);
-            O[z][tt] = mfma_h(q0, hi[z], O[z][tt]);
-            X[z][tt] = mfma_h(k0, lo[z], X[z][tt]);
-          }
-          if constexpr (P == 2) {
-            const h8 k1 = operand(ks, 1, tt * KB + kb), q1 = operand(qs, 1, tt * KB + kb);
-#pragma unroll
-            for (int z = 0; z < NC; ++z) {
-              X[z][tt] = mfma_h(k1, hi[z], X[z][tt]);
-              O[z][tt] = mfma_h(q1, hi[z], O[z][tt]);
-              O[z][tt] = mfma_h(q0, lo[z], O[z][tt]);
-            }
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      __builtin_amdgcn_sched_barrier(0);  // both phases at once would not fit the registers
-      // X, D and the products with them.
-      f4 D[NC][4];
-#pragma unroll
-      for (int z = 0; z < NC; ++z) {
-        float m = 0.0f;
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          const f4 f = row4(kRowX, tt) * sS[z].down;
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            X[z][tt][r] = fmaf(-f[r], X[z][tt][r], widen(V[z][4 * tt + r]));
-          m = max4(m, X[z][tt]);
-        }
-        const Scale sX = scale_of(column_max(m));
-        h8 xh[2], xl[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) split8(X[z][2 * s], X[z][2 * s + 1], sX.up, &xh[s], &xl[s]);
-        float md = 0.0f, ms = 0.0f;
-        f4 U[4];
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          f4 e = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int s = 0; s <= tt / 2; ++s) {
-            const h8 t0 = lower(0, tt, s), t1 = lower(1, tt, s);
-            e = mfma_h(t0, xh[s], e);
-            e = mfma_h(t0, xl[s], e);
-            e = mfma_h(t1, xh[s], e);
-          }
-          D[z][tt] = e * (row4(kRowD, tt) * sX.down);
-          U[tt] = D[z][tt] * row4(kRowS, tt);
-          md = max4(md, D[z][tt]);
-          ms = max4(ms, U[tt]);
-        }
-        // Where D is nothing beside S its scale stays within reach of S's.
-        const float least = mS[z] * 0x1p-40f;
-        const Scale sD = scale_of(fmaxf(column_max(md), least));
-        const Scale sU = scale_of(fmaxf(column_max(ms), least));
-        h8 dh[2], dl[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) split8(D[z][2 * s], D[z][2 * s + 1], sD.up, &dh[s], &dl[s]);
-        const float fy = sS[z].down * sD.up, out = a.scale * sD.down * (1.0f / kUp);
-        const uint32_t y0 = fresh(
-            (col0 + 16 * z < a.value_dim ? (col0 + 16 * z + i) * es : kNoStore) + 4 * g * yoff);
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          f4 o = O[z][tt] * (row4(kRowY, tt) * fy);
-#pragma unroll
-          for (int s = 0; s <= tt / 2; ++s) {
-            const h8 a0 = lower(2, tt, s);
-            o = mfma_h(a0, dh[s], o);
-            if constexpr (P == 2) {
-              o = mfma_h(a0, dl[s], o);
-              o = mfma_h(lower(3, tt, s), dh[s], o);
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            store_buf<Act>(yr, y0 + (16 * tt + r) * yoff, o[r] * out);
-        }
-        h8 uh[2], ul[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) split8(U[2 * s], U[2 * s + 1], sU.up, &uh[s], &ul[s]);
-        const float keep = end * sU.up;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          f4 x = S[z][b] * keep;
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const h8 k0 = operand(kt, 0, 2 * b + s);
-            x = mfma_h(k0, uh[s], x);
-            x = mfma_h(k0, ul[s], x);
-            if constexpr (P == 2) x = mfma_h(operand(kt, 1, 2 * b + s), uh[s], x);
-          }
-          S[z][b] = x * sU.down;
-        }
+        for (int r = 0; r < 4; ++r) out4[z][r] = a.scale * __shfl(unit[z], 4 * g + r, 16);
       }
     }
-    __syncthreads();
+    // This wave has read its columns of v: the next chunk's may take their place.
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    load_v(next);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      h8 hi[NC], lo[NC];
+#pragma unroll
+      for (int z = 0; z < NC; ++z) split8(S[z][2 * kb], S[z][2 * kb + 1], &hi[z], &lo[z]);
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const h8 k0 = operand(kc, 0, tt, kb), q0 = operand(qc, 0, tt, kb);
+#pragma unroll
+        for (int z = 0; z < NC; ++z) {
+          const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+          X[z][tt] = mfma_h(k0, hi[z], kb ? X[z][tt] : zero);
+          O[z][tt] = mfma_h(hi[z], q0, kb ? O[z][tt] : zero);
+          X[z][tt] = mfma_h(k0, lo[z], X[z][tt]);
+        }
+        if constexpr (P == 2) {
+          const h8 k1 = operand(kc, 1, tt, kb), q1 = operand(qc, 1, tt, kb);
+#pragma unroll
+          for (int z = 0; z < NC; ++z) {
+            X[z][tt] = mfma_h(k1, hi[z], X[z][tt]);
+            O[z][tt] = mfma_h(hi[z], q1, O[z][tt]);
+            O[z][tt] = mfma_h(lo[z], q0, O[z][tt]);
+          }
+        }
+      }
+      if (NC > 1) __builtin_amdgcn_sched_barrier(0);  // more pieces at once would not fit the registers
+    }
+    if (NC > 1) __builtin_amdgcn_sched_barrier(0);
+    // X, E and the products with them.
+#pragma unroll
+    for (int z = 0; z < NC; ++z) {
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const f4 f = row4(kRowX, tt);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) X[z][tt][r] = fmaf(-f[r], X[z][tt][r], v[z][tt][r] * inverse[z]);
+      }
+      h8 xh[2], xl[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) split8(X[z][2 * s], X[z][2 * s + 1], &xh[s], &xl[s]);
+      f4 E[4], U[4];
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        f4 e = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s <= tt / 2; ++s) {
+          const h8 t0 = lower(0, tt, s), t1 = lower(1, tt, s);
+          e = mfma_h(t0, xh[s], e);
+          e = mfma_h(t0, xl[s], e);
+          e = mfma_h(t1, xh[s], e);
+        }
+        E[tt] = e;
+        U[tt] = e * row4(kRowS, tt);
+      }
+      h8 eh[2], el[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if constexpr (P == 1)
+          eh[s] = first_piece(E[2 * s], E[2 * s + 1]);
+        else
+          split8(E[2 * s], E[2 * s + 1], &eh[s], &el[s]);
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        f4 o = O[z][tt] * *reinterpret_cast<const float*>(rs + rows_at(P) + (kRowY * kQ + 16 * tt + i) * 4);
+#pragma unroll
+        for (int s = 0; s <= tt / 2; ++s) {
+          const h8 a0 = lower(2, tt, s);
+          o = mfma_h(eh[s], a0, o);
+          if constexpr (P == 2) {
+            o = mfma_h(el[s], a0, o);
+            o = mfma_h(eh[s], lower(3, tt, s), o);
+          }
+        }
+        store_y(c, z, tt, o * out4[z]);
+      }
+      h8 uh[2], ul[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) split8(U[2 * s], U[2 * s + 1], &uh[s], &ul[s]);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        f4 x = S[z][b] * end;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const h8 k0 = transposed(kc, 0, b, s);
+          x = mfma_h(k0, uh[s], x);
+          x = mfma_h(k0, ul[s], x);
+          if constexpr (P == 2) x = mfma_h(transposed(kc, 1, b, s), uh[s], x);
+        }
+        S[z][b] = x;
+      }
+      if (NC > 1) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (kBufs == 1) __syncthreads();
   }
   const int64_t slot_out = a.out_slots ? a.out_slots[n] : n;
   if (a.state_out && slot_out >= 0 && slot_out < a.out_count) {
@@ -769,7 +835,7 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 2 : 1) void walk_kerne
       for (int b = 0; b < NB; ++b)
         if (col0 + 16 * z < a.value_dim)
           *reinterpret_cast<f4*>(a.state_out + ((slot_out * a.hv + h) * a.value_dim + col0 + 16 * z + i) * K +
-                                 16 * b + 4 * g) = S[z][b];
+                                 32 * (b >> 1) + 8 * g + 4 * (b & 1)) = S[z][b] * unit[z];
   }
 }
 
@@ -962,17 +1028,10 @@ void launch_scan(DeltaArgs a, bool any, hipStream_t st) {
     hipLaunchKernelGGL((prep_kernel<Act, K>), dim3(unsigned(a.rows), unsigned(a.hk)), dim3(kThreads),
                        0, st, a);
   }
-  // Two column tiles a wave halve what is read from LDS for each product; one tile spreads the
-  // columns over twice the workgroups.
-  const int64_t heads = int64_t(a.sequences) * a.hv;
-  const int64_t heads8 = (heads + 7) / 8 * 8;
-  const bool two = a.value_dim > 64 && heads >= 256;
-  a.col_groups = two ? (a.value_dim + 127) / 128 : (a.value_dim + 63) / 64;
-  const dim3 grid(unsigned(heads8 * a.col_groups));
-  if (two)
-    hipLaunchKernelGGL((walk_kernel<Act, K, 2>), grid, dim3(kThreads), 0, st, a);
-  else
-    hipLaunchKernelGGL((walk_kernel<Act, K, 1>), grid, dim3(kThreads), 0, st, a);
+  a.col_groups = (a.value_dim + 127) / 128;
+  const int64_t units = (int64_t(a.sequences) * a.hv + 7) / 8 * 8;
+  hipLaunchKernelGGL((walk_kernel<Act, K, 1, 1>), dim3(unsigned(units * a.col_groups)),
+                     dim3(kWalkThreads), 0, st, a);
 }
 
 template <typename Act, int K>
