@@ -17,7 +17,7 @@
 //   prep_kernel  per chunk and key head: the Gram products, then per value head T (16 x 16 diagonal
 //                blocks by substitution, which stays accurate where keys are alike and powers of M
 //                would cancel; the blocks below by matrix products), A and the row factors.
-//   walk_kernel  per sequence, value head and slice of 16 or 32 columns of V one wave walks the
+//   walk_kernel  per sequence, value head and slice of 16 columns of V one wave walks the
 //                chunks with its slice of the state in registers. The state is held transposed
 //                (S^T, K x 16): the result layout of a 16 x 16 product (lane (g, i), g = lane / 16,
 //                i = lane % 16: rows 4 g + r, column i) is also the layout of the next product's
@@ -49,7 +49,6 @@ namespace {
 
 constexpr int kQ = 64;  // tokens of a chunk
 constexpr int kThreads = 256;
-constexpr int kWalkThreads = 512;
 constexpr int kMS = kQ + 4;  // LDS row stride of 64 x 64 matrices
 
 typedef float f4 __attribute__((ext_vector_type(4)));
@@ -199,17 +198,53 @@ struct Eight<float> {
   }
 };
 
+// A lane's 16 values of a column of v, as loaded.
+template <typename Act>
+struct Column;
+template <>
+struct Column<bf16_bits> {
+  uint32_t raw[8];
+  __device__ __forceinline__ float largest() const {  // bf16 magnitudes are ordered as integers
+    u2 m = __builtin_bit_cast(u2, raw[0] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int e = 1; e < 8; ++e)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u2, raw[e] & 0x7FFF7FFFu));
+    return __uint_as_float(static_cast<uint32_t>(m[0] > m[1] ? m[0] : m[1]) << 16);
+  }
+  __device__ __forceinline__ float value(int tt, int r) const {
+    const uint32_t x = raw[2 * tt + (r >> 1)];
+    return __uint_as_float(r & 1 ? x & 0xFFFF0000u : x << 16);
+  }
+};
+template <>
+struct Column<float> {
+  float raw[16];
+  __device__ __forceinline__ float largest() const {
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(raw[e]));
+    return m;
+  }
+  __device__ __forceinline__ float value(int tt, int r) const { return raw[4 * tt + r]; }
+};
+
 // Two pieces of eight values (two accumulators of one column).
 __device__ __forceinline__ h8 first_piece(f4 a, f4 b) {
   return __builtin_shufflevector(__builtin_convertvector(a, h4), __builtin_convertvector(b, h4), 0, 1,
                                  2, 3, 4, 5, 6, 7);
 }
 __device__ __forceinline__ void split8(f4 a, f4 b, h8* hi, h8* lo) {
-  const h4 ha = __builtin_convertvector(a, h4), hb = __builtin_convertvector(b, h4);
-  const h4 la = __builtin_convertvector(a - __builtin_convertvector(ha, f4), h4);
-  const h4 lb = __builtin_convertvector(b - __builtin_convertvector(hb, f4), h4);
-  *hi = __builtin_shufflevector(ha, hb, 0, 1, 2, 3, 4, 5, 6, 7);
-  *lo = __builtin_shufflevector(la, lb, 0, 1, 2, 3, 4, 5, 6, 7);
+  // One v_fma_mix_f32 takes a piece off its value; the compiler, if it knew the factor, would convert
+  // the piece first.
+  float minus = -1.0f;
+  asm volatile("" : "+s"(minus));
+  *hi = first_piece(a, b);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    a[e] = fmaf(static_cast<float>((*hi)[e]), minus, a[e]);
+    b[e] = fmaf(static_cast<float>((*hi)[e + 4]), minus, b[e]);
+  }
+  *lo = first_piece(a, b);
 }
 
 // 16 lanes read 4 rows x 16 fp16 (lane j: row j / 4, columns 4 (j % 4) ..) and lane j gets column j.
@@ -474,47 +509,49 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
 }
 
 // ---- the walk over the chunks -------------------------------------------------------------------
-// 8 waves a workgroup, each with NC tiles of 16 columns of V; HV value heads of one key head share
-// what is brought of k and q. Per chunk the workgroup brings k and q, converted to fp16 pieces on
-// the way, as rows of K fp16 (read as left operand of S k^ and S q^, and k by transposing reads as
-// left operand of the state's sum) and each head's record. Both have two buffers (fp32: k and q
-// one), and the next chunk's rows travel in registers while this one's are used.
+// W waves a workgroup, each with NC tiles of 16 columns of V of one head. Per chunk the workgroup
+// brings k and q, converted to fp16 pieces on the way, as rows of K fp16 (read as left operand of
+// S k^ and S q^, and k by transposing reads as left operand of the state's sum) and the chunk's
+// record (two buffers). The next chunk's rows travel in registers while this one's are used.
 //
 // Row i of tile b of the transposed state is channel 32 (b / 2) + 8 (i / 4) + 4 (b % 2) + i % 4, so
-// that a lane's eight values of two tiles are eight channels in a row: 16 bytes of a k or q row.
-// Those rows would all begin in the same bank: the 16-byte piece c of token t lies at c ^ swizzle(t),
-// which spreads both the 16 rows of an operand and the 4 rows x 4 pieces of a transposing read.
+// that a lane's eight values of two tiles are eight channels in a row of k or q. LDS holds a row's
+// even and odd groups of four channels apart (two halves of 8-byte pieces, kHalf bytes from each
+// other, read by one instruction), and piece c of token t lies at c ^ swizzle(t): any 16 lanes that
+// LDS serves in one cycle (16 tokens of one piece; 4 tokens x 4 pieces of a transposing read; the
+// pieces of a row as they are written) then differ in all banks.
 template <int K>
 __device__ __forceinline__ int swizzle(int t) {
   return K == 128 ? (t & 3) << 2 | ((t >> 2) & 3) : (t & 2) << 1 | ((t >> 2) & 3);
 }
 
-template <typename Act, int K, int HV, int NC>
-__global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(DeltaArgs a) {
+// The blocks of a lower triangular matrix as operands: row block, and pair of contraction blocks.
+constexpr int kLowerRow[6] = {0, 1, 2, 3, 2, 3}, kLowerCol[6] = {0, 0, 0, 0, 1, 1};
+
+template <typename Act, int K, int W, int NC>
+__global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
   constexpr int P = kPieces<Act>;
   constexpr int NB = K / 16, KB = K / 32;
-  constexpr int kRow = 2 * K, kMat = kQ * kRow;  // bytes of a row, of one piece of k or q of a chunk
+  constexpr int kRow = K, kHalf = 16 * kRow;     // bytes of half a row, of one half of 16 rows
+  constexpr int kMat = 8 * kHalf;                // of one piece (of an fp16 pair) of k or q of a chunk
   constexpr int kRec = record_bytes(P), kLds = lds_bytes(P), kLoads = kLds / 1024;
-  constexpr int kWaves = kWalkThreads / 64, kPerHead = kWaves / HV;
-  constexpr int kBufs = P == 1 ? 2 : 1;                    // of k and q
-  constexpr int kUnits = kQ * K / 8 / kWalkThreads;        // 16-byte pieces of k (and q) a thread brings
+  constexpr int kThreadsW = 64 * W;
+  constexpr int kBufs = P == 1 && (W == 8 || K == 64) ? 2 : 1;  // of k and q
+  constexpr int kUnits = kQ * K / 8 / kThreadsW;     // 16-byte pieces of k (and q) a thread brings
   static_assert(kLds % 1024 == 0, "whole wave loads");
   __shared__ __align__(16) char ks[kBufs][P * kMat];
   __shared__ __align__(16) char qs[kBufs][P * kMat];
-  __shared__ __align__(16) char rs2[2][HV][kLds];
-  __shared__ __align__(16) char vs[kWaves][kQ * 16 * NC * sizeof(Act)];
+  __shared__ __align__(16) char rs2[2][kLds];
+  __shared__ __align__(16) char vs[W][kQ * 16 * NC * sizeof(Act)];
 
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-  const int groups = a.hv / HV;
-  const int64_t ng = int64_t(slot / a.col_groups) * 8 + xcd;
-  if (ng >= int64_t(a.sequences) * groups) return;
+  const int64_t nh = int64_t(slot / a.col_groups) * 8 + xcd;
+  if (nh >= int64_t(a.sequences) * a.hv) return;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, i = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n = static_cast<int>(ng / groups);
-  const int hl = w / kPerHead;  // this wave's head of the workgroup
-  const int h = static_cast<int>(ng - int64_t(n) * groups) * HV + hl;
+  const int n = static_cast<int>(nh / a.hv), h = static_cast<int>(nh - int64_t(n) * a.hv);
   const int hk = h / a.ratio;
-  const int col0 = ((slot % a.col_groups) * kPerHead + w % kPerHead) * 16 * NC;
+  const int col0 = ((slot % a.col_groups) * W + w) * 16 * NC;
   int64_t begin, len, row0;
   if (a.starts) {
     begin = a.starts[n];
@@ -531,31 +568,40 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(DeltaArgs a) {
   // The state in units of its columns: S / unit.
   f4 S[NC][NB];
   float unit[NC], inverse[NC];
-  f4 out4[NC];  // scale * unit of the columns 4 g + r, for y
   // Element (z, b, r) is row 32 (b / 2) + 8 g + 4 (b % 2) + r of column col0 + 16 z + i.
   const int64_t slot_in = a.in_slots ? a.in_slots[n] : n;
   const bool have = a.state_in && slot_in >= 0 && slot_in < a.in_count;
+  const int64_t state_at = (int64_t(h) * a.value_dim + col0 + i) * K + 8 * g;
 #pragma unroll
   for (int z = 0; z < NC; ++z) {
     unit[z] = inverse[z] = 1.0f;
-    out4[z] = f4{a.scale, a.scale, a.scale, a.scale};
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       S[z][b] = f4{0.0f, 0.0f, 0.0f, 0.0f};
       if (have && col0 + 16 * z < a.value_dim)
-        S[z][b] = *reinterpret_cast<const f4*>(
-            a.state_in + ((slot_in * a.hv + h) * a.value_dim + col0 + 16 * z + i) * K + 32 * (b >> 1) +
-            8 * g + 4 * (b & 1));
+        S[z][b] = *reinterpret_cast<const f4*>(a.state_in + slot_in * a.hv * a.value_dim * K + state_at +
+                                               16 * z * K + 32 * (b >> 1) + 4 * (b & 1));
     }
   }
 
   constexpr uint32_t es = sizeof(Act);
-  // This thread brings pieces tid, tid + 512, ... of the chunk's rows (K / 8 pieces a row).
+  // This thread brings pieces tid, tid + 64 W, ... of the chunk's rows (K / 8 pieces a row).
   Eight<Act> pk[kUnits], pq[kUnits];
   float2 sh[kUnits];
   float end = 0.0f, end_next = 0.0f;
+  // The record goes to LDS without passing through registers, 1 KiB a wave and instruction.
+  // (Where the pieces are no multiple of the waves, the last one is brought more than once.)
+  auto load_record = [&](int64_t c, int buf) {
+    const char* rec = a.records + ((row0 + c) * a.hv + h) * int64_t(kRec);
+    end_next = *reinterpret_cast<const float*>(rec + rows_at(P) + kRows * kQ * 4);
+#pragma unroll
+    for (int u0 = 0; u0 < kLoads; u0 += W) {
+      const int u = min(u0 + w, kLoads - 1);
+      load_to_lds(rec + u * 1024, lane * 16, &rs2[buf][u * 1024]);
+    }
+  };
   // Rows behind the sequence lie outside the resource's range and read as zeros.
-  auto load = [&](int64_t c, int buf) {
+  auto load = [&](int64_t c) {
     const int64_t first = begin + c * kQ;
     const int count = len - c * kQ < kQ ? static_cast<int>(len - c * kQ) : kQ;
     const uint32_t koff = static_cast<uint32_t>(a.k_stride) * es, qoff = static_cast<uint32_t>(a.q_stride) * es;
@@ -566,18 +612,9 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(DeltaArgs a) {
         const_cast<Act*>(static_cast<const Act*>(a.q) + first * a.q_stride + int64_t(hk) * K),
         (count - 1) * qoff + K * es);
     const char* rec = a.records + ((row0 + c) * a.hv + h) * int64_t(kRec);
-    // The record goes to LDS without passing through registers, 1 KiB a wave and instruction.
-    // (Where the pieces are no multiple of the waves, the last one is brought more than once.)
-#pragma unroll
-    for (int u0 = 0; u0 < kLoads; u0 += kPerHead) {
-      const int u = min(u0 + w % kPerHead, kLoads - 1);
-      load_to_lds(rec + u * 1024, lane * 16, &rs2[buf][hl][u * 1024]);
-    }
-    __builtin_amdgcn_sched_barrier(0);  // before the loads below: see the wait in the loop
-    end_next = *reinterpret_cast<const float*>(rec + rows_at(P) + kRows * kQ * 4);
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-      const int at = tid + u * kWalkThreads, t = at / (K / 8), piece = at % (K / 8);
+      const int at = tid + u * kThreadsW, t = at / (K / 8), piece = at % (K / 8);
       const uint32_t ko = fresh(t * koff + piece * 8 * es), qo = fresh(t * qoff + piece * 8 * es);
       sh[u] = *reinterpret_cast<const float2*>(rec + rows_at(P) + kRowKQ * kQ * 4 + t * 8);
       pk[u].load(kr, ko);
@@ -587,15 +624,21 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(DeltaArgs a) {
   auto store = [&](int buf) {
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-      const int at = tid + u * kWalkThreads, t = at / (K / 8), piece = at % (K / 8);
-      const int to = t * kRow + (piece ^ swizzle<K>(t)) * 16;
+      const int at = tid + u * kThreadsW, t = at / (K / 8), piece = at % (K / 8);
+      const int to = (t >> 4) * 2 * kHalf + (t & 15) * kRow + (piece ^ swizzle<K>(t)) * 8;
       w4 out[P];
       pk[u].pieces(sh[u].x, out);
 #pragma unroll
-      for (int p = 0; p < P; ++p) *reinterpret_cast<w4*>(&ks[buf][p * kMat + to]) = out[p];
+      for (int p = 0; p < P; ++p) {
+        *reinterpret_cast<w2*>(&ks[buf][p * kMat + to]) = w2{out[p][0], out[p][1]};
+        *reinterpret_cast<w2*>(&ks[buf][p * kMat + kHalf + to]) = w2{out[p][2], out[p][3]};
+      }
       pq[u].pieces(sh[u].y, out);
 #pragma unroll
-      for (int p = 0; p < P; ++p) *reinterpret_cast<w4*>(&qs[buf][p * kMat + to]) = out[p];
+      for (int p = 0; p < P; ++p) {
+        *reinterpret_cast<w2*>(&qs[buf][p * kMat + to]) = w2{out[p][0], out[p][1]};
+        *reinterpret_cast<w2*>(&qs[buf][p * kMat + kHalf + to]) = w2{out[p][2], out[p][3]};
+      }
     }
   };
   // This wave's columns of a chunk's v go to LDS as rows of 16 NC values (only this wave reads them):
@@ -619,33 +662,28 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(DeltaArgs a) {
     }
   };
   // Rows 16 tt + 4 g .. + 3 of column 16 z + i.
-  auto v4 = [&](int z, int tt) {
-    f4 v;
+  auto load4 = [&](Column<Act>& v, int z, int tt) {
     if constexpr (P == 1) {
       const w2 x = __builtin_bit_cast(
           w2, read_transposed(vw + (16 * tt + 4 * g + (i >> 2)) * 32 * NC + 32 * z + (i & 3) * 8));
-      v[0] = __uint_as_float(x[0] << 16);
-      v[1] = __uint_as_float(x[0] & 0xFFFF0000u);
-      v[2] = __uint_as_float(x[1] << 16);
-      v[3] = __uint_as_float(x[1] & 0xFFFF0000u);
+      v.raw[2 * tt] = x[0], v.raw[2 * tt + 1] = x[1];
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        v[r] = *reinterpret_cast<const float*>(vw + (16 * tt + 4 * r + g) * 64 * NC + 64 * z + 4 * i);
+        v.raw[4 * tt + r] = *reinterpret_cast<const float*>(vw + (16 * tt + 4 * r + g) * 64 * NC + 64 * z + 4 * i);
     }
-    return v;
   };
   // y is computed transposed (rows: 4 columns 4 g + r, column: token i), so that a lane stores four
   // values in a row. Rows behind the sequence and columns behind V lie outside the range.
   const int64_t y_stride = int64_t(a.hv) * a.value_dim;
   const uint32_t yoff = (i * static_cast<uint32_t>(y_stride) + col0 + 4 * g) * es;
   auto store_y = [&](int64_t c, int z, int tt, f4 o) {
+    const uint32_t off = col0 + 16 * z < a.value_dim ? yoff + 16 * z * es : kNoStore;
     const int64_t first = begin + c * kQ;
     const int left = (len - c * kQ < kQ ? static_cast<int>(len - c * kQ) : kQ) - 16 * tt;
     const rsrc_t yr = make_rsrc_bounded(
         static_cast<char*>(a.y) + ((first + 16 * tt) * y_stride + int64_t(h) * a.value_dim) * int64_t(es),
         left > 0 ? ((left - 1) * static_cast<uint32_t>(y_stride) + a.value_dim) * es : 0);
-    const uint32_t off = col0 + 16 * z < a.value_dim ? yoff + 16 * z * es : kNoStore;
     if constexpr (P == 1) {
       const w2 v = {f32_to_bf16(o[0]) | static_cast<uint32_t>(f32_to_bf16(o[1])) << 16,
                     f32_to_bf16(o[2]) | static_cast<uint32_t>(f32_to_bf16(o[3])) << 16};
@@ -655,19 +693,22 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(DeltaArgs a) {
     }
   };
   // Left operand: rows 16 tt + i, channels 32 kb + 8 g .. + 7.
-  const int srow = i * kRow, sw = swizzle<K>(i);
+  const uint32_t rowop = i * kRow + (g ^ swizzle<K>(i)) * 8;
+  uint32_t rowop_c = rowop, colop_c;  // of this chunk: the sums with them are not kept across chunks
   auto operand = [&](const char* m, int p, int tt, int kb) {
-    return *reinterpret_cast<const h8*>(m + p * kMat + tt * 16 * kRow + srow + ((4 * kb + g) ^ sw) * 16);
+    const char* at = m + p * kMat + tt * 2 * kHalf + (rowop_c ^ (kb * 32));
+    return __builtin_shufflevector(*reinterpret_cast<const h4*>(at),
+                                   *reinterpret_cast<const h4*>(at + kHalf), 0, 1, 2, 3, 4, 5, 6, 7);
   };
   // Left operand: rows of state tile b, tokens 32 s + 4 g + e and 32 s + 16 + 4 g + e. The 16 lanes
   // of group g read 4 tokens x 16 channels, and each gets its own channel's 4 tokens.
-  const int trow = (4 * g + (i >> 2)) * kRow, tsw = swizzle<K>(4 * g + (i >> 2));
+  const uint32_t colop = (4 * g + (i >> 2)) * kRow + ((i & 3) ^ swizzle<K>(4 * g + (i >> 2))) * 8;
   auto transposed = [&](const char* m, int p, int b, int s) {
-    const char* at = m + p * kMat + s * 32 * kRow + trow + ((4 * (b >> 1) + (i & 3)) ^ tsw) * 16 + (b & 1) * 8;
-    const h4 x = read_transposed(at), y = read_transposed(at + 16 * kRow);
+    const char* at = m + p * kMat + s * 4 * kHalf + (colop_c ^ ((b >> 1) * 32)) + (b & 1) * kHalf;
+    const h4 x = read_transposed(at), y = read_transposed(at + 2 * kHalf);
     return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  const char* rs = rs2[0][0];
+  const char* rs = rs2[0];
   // Row block tt, contraction blocks 2 ss and 2 ss + 1 of a lower triangular matrix.
   auto lower = [&](int mat, int tt, int ss) {
     const char* p = rs + (mat * kBlocks + tt * (tt + 1) / 2 + 2 * ss) * kBlockBytes + lane * 8;
@@ -685,37 +726,38 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(DeltaArgs a) {
   // and waves without columns run on zeros.
   if (chunks > 0) {
     load_v(0);
-    load(0, 0);
+    load_record(0, 0);
+    load(0);
   }
   for (int64_t c = 0; c < chunks; ++c) {
     const int kb2 = kBufs == 2 ? c & 1 : 0;
     store(kb2);
     const char *kc = ks[kb2], *qc = qs[kb2];
-    rs = rs2[c & 1][hl];
+    rs = rs2[c & 1];
     end = end_next;
     // This wave's parts of the record and v are in LDS: vector memory operations of a wave complete
-    // in the order of their issue, and behind the last of them, v, only y's 4 NC stores were issued.
+    // in the order of their issue, and behind them and k and q only y's 4 NC stores were issued.
     if (NC == 1)
       asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
     else
       asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
     // Behind this barrier chunk c is complete in LDS and every wave is done with chunk c - 1, whose
-    // buffers the next chunk takes.
+    // record buffer the next chunk takes.
     __syncthreads();
     const int64_t next = c + 1 < chunks ? c + 1 : c;
-    load(next, (c + 1) & 1);
-    f4 X[NC][4], O[NC][4], v[NC][4];
+    rowop_c = fresh(rowop);
+    colop_c = fresh(colop);
+    load_record(next, (c + 1) & 1);
+    f4 X[NC][4], O[NC][4];
 #pragma unroll
     for (int z = 0; z < NC; ++z) {
-      float m = 0.0f, ms = 0.0f;
+      Column<Act> v;
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        v[z][tt] = v4(z, tt);
-        m = max4(m, v[z][tt]);
-      }
+      for (int tt = 0; tt < 4; ++tt) load4(v, z, tt);
+      float m = 0.0f;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) ms = max4(ms, S[z][b]);
-      m = column_max(fmaxf(m, ms * unit[z]));
+      for (int b = 0; b < NB; ++b) m = max4(m, S[z][b]);
+      m = column_max(fmaxf(v.largest(), m * unit[z]));
       // The unit stays while the column's largest is between 2^2 and 2^8 of it.
       const float at = m * inverse[z];
       if (__any(m > 0.0f && !(at >= 0x1p2f && at <= 0x1p8f))) {
@@ -725,107 +767,161 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(DeltaArgs a) {
         unit[z] = to.down * 0x1p-5f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) S[z][b] *= by;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) out4[z][r] = a.scale * __shfl(unit[z], 4 * g + r, 16);
       }
     }
-    // This wave has read its columns of v: the next chunk's may take their place.
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    load_v(next);
+    // X and the state's part of y. Left operands are read ahead of their products (a read from LDS
+    // takes as long as eight products); fences keep the compiler from moving the reads back, or all
+    // of them ahead, which would not fit the registers.
+    constexpr int kSets = P == 1 && NC == 1 ? 2 : 1;
+    h8 kf[kSets][4][P], qf[kSets][4][P];
+    auto fetch = [&](int kb) {
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          kf[kb % kSets][tt][p] = operand(kc, p, tt, kb);
+          qf[kb % kSets][tt][p] = operand(qc, p, tt, kb);
+        }
+    };
+    if (kSets == 2) fetch(0);
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
+      if (kSets == 1) fetch(kb);
+      if (kSets == 2 && kb + 1 < KB) fetch(kb + 1);
       h8 hi[NC], lo[NC];
 #pragma unroll
       for (int z = 0; z < NC; ++z) split8(S[z][2 * kb], S[z][2 * kb + 1], &hi[z], &lo[z]);
+      if (kSets == 2) __builtin_amdgcn_sched_barrier(0);
+      const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+      const auto& k = kf[kb % kSets];
+      const auto& q = qf[kb % kSets];
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        const h8 k0 = operand(kc, 0, tt, kb), q0 = operand(qc, 0, tt, kb);
+      for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-        for (int z = 0; z < NC; ++z) {
-          const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-          X[z][tt] = mfma_h(k0, hi[z], kb ? X[z][tt] : zero);
-          O[z][tt] = mfma_h(hi[z], q0, kb ? O[z][tt] : zero);
-          X[z][tt] = mfma_h(k0, lo[z], X[z][tt]);
-        }
-        if constexpr (P == 2) {
-          const h8 k1 = operand(kc, 1, tt, kb), q1 = operand(qc, 1, tt, kb);
+        for (int z = 0; z < NC; ++z) X[z][tt] = mfma_h(k[tt][0], hi[z], kb ? X[z][tt] : zero);
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int z = 0; z < NC; ++z) X[z][tt] = mfma_h(k[tt][0], lo[z], X[z][tt]);
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int z = 0; z < NC; ++z) O[z][tt] = mfma_h(hi[z], q[tt][0], kb ? O[z][tt] : zero);
+      if constexpr (P == 2) {
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
           for (int z = 0; z < NC; ++z) {
-            X[z][tt] = mfma_h(k1, hi[z], X[z][tt]);
-            O[z][tt] = mfma_h(hi[z], q1, O[z][tt]);
-            O[z][tt] = mfma_h(lo[z], q0, O[z][tt]);
+            O[z][tt] = mfma_h(lo[z], q[tt][0], O[z][tt]);
+            X[z][tt] = mfma_h(k[tt][1], hi[z], X[z][tt]);
+            O[z][tt] = mfma_h(hi[z], q[tt][1], O[z][tt]);
           }
-        }
       }
-      if (NC > 1) __builtin_amdgcn_sched_barrier(0);  // more pieces at once would not fit the registers
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (NC > 1) __builtin_amdgcn_sched_barrier(0);
-    // X, E and the products with them.
+    h8 xh[NC][2], xl[NC][2];
 #pragma unroll
     for (int z = 0; z < NC; ++z) {
+      Column<Act> v;  // read again: it would not fit the registers during the products
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) load4(v, z, tt);
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
         const f4 f = row4(kRowX, tt);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) X[z][tt][r] = fmaf(-f[r], X[z][tt][r], v[z][tt][r] * inverse[z]);
-      }
-      h8 xh[2], xl[2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) split8(X[z][2 * s], X[z][2 * s + 1], &xh[s], &xl[s]);
-      f4 E[4], U[4];
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        f4 e = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s <= tt / 2; ++s) {
-          const h8 t0 = lower(0, tt, s), t1 = lower(1, tt, s);
-          e = mfma_h(t0, xh[s], e);
-          e = mfma_h(t0, xl[s], e);
-          e = mfma_h(t1, xh[s], e);
-        }
-        E[tt] = e;
-        U[tt] = e * row4(kRowS, tt);
-      }
-      h8 eh[2], el[2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if constexpr (P == 1)
-          eh[s] = first_piece(E[2 * s], E[2 * s + 1]);
-        else
-          split8(E[2 * s], E[2 * s + 1], &eh[s], &el[s]);
+        for (int r = 0; r < 4; ++r)
+          X[z][tt][r] = fmaf(-f[r], X[z][tt][r], v.value(tt, r) * inverse[z]);
       }
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        f4 o = O[z][tt] * *reinterpret_cast<const float*>(rs + rows_at(P) + (kRowY * kQ + 16 * tt + i) * 4);
+      for (int s = 0; s < 2; ++s) split8(X[z][2 * s], X[z][2 * s + 1], &xh[z][s], &xl[z][s]);
+    }
+    // This wave has read its columns of v: the next chunk's may take their place.
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    load_v(next);
+    __builtin_amdgcn_sched_barrier(0);
+    // E = T X.
+    f4 E[NC][4];
 #pragma unroll
-        for (int s = 0; s <= tt / 2; ++s) {
-          const h8 a0 = lower(2, tt, s);
-          o = mfma_h(eh[s], a0, o);
-          if constexpr (P == 2) {
-            o = mfma_h(el[s], a0, o);
-            o = mfma_h(eh[s], lower(3, tt, s), o);
-          }
-        }
-        store_y(c, z, tt, o * out4[z]);
+    for (int e = 0; e < 6; ++e) {
+      const int tt = kLowerRow[e], s = kLowerCol[e];
+      const h8 t0 = lower(0, tt, s), t1 = lower(1, tt, s);
+      const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int z = 0; z < NC; ++z) {
+        E[z][tt] = mfma_h(t0, xh[z][s], s ? E[z][tt] : zero);
+        E[z][tt] = mfma_h(t0, xl[z][s], E[z][tt]);
+        E[z][tt] = mfma_h(t1, xh[z][s], E[z][tt]);
       }
-      h8 uh[2], ul[2];
+    }
+    load(next);
+    __builtin_amdgcn_sched_barrier(0);
+    // y, and the writes U.
+    h8 uh[NC][2], ul[NC][2];
+    {
+      h8 eh[NC][2], el[NC][2];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) split8(U[2 * s], U[2 * s + 1], &uh[s], &ul[s]);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        f4 x = S[z][b] * end;
+      for (int z = 0; z < NC; ++z)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const h8 k0 = transposed(kc, 0, b, s);
-          x = mfma_h(k0, uh[s], x);
-          x = mfma_h(k0, ul[s], x);
-          if constexpr (P == 2) x = mfma_h(transposed(kc, 1, b, s), uh[s], x);
+          if constexpr (P == 1)
+            eh[z][s] = first_piece(E[z][2 * s], E[z][2 * s + 1]);
+          else
+            split8(E[z][2 * s], E[z][2 * s + 1], &eh[z][s], &el[z][s]);
+          split8(E[z][2 * s] * row4(kRowS, 2 * s), E[z][2 * s + 1] * row4(kRowS, 2 * s + 1), &uh[z][s],
+                 &ul[z][s]);
         }
-        S[z][b] = x;
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const float f = *reinterpret_cast<const float*>(rs + rows_at(P) + (kRowY * kQ + 16 * tt + i) * 4);
+#pragma unroll
+        for (int z = 0; z < NC; ++z) O[z][tt] *= f;
       }
-      if (NC > 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int e = 0; e < 6; ++e) {
+        const int tt = kLowerRow[e], s = kLowerCol[e];
+        const h8 a0 = lower(2, tt, s);
+#pragma unroll
+        for (int z = 0; z < NC; ++z) O[z][tt] = mfma_h(eh[z][s], a0, O[z][tt]);
+        if constexpr (P == 2) {
+          const h8 a1 = lower(3, tt, s);
+#pragma unroll
+          for (int z = 0; z < NC; ++z) {
+            O[z][tt] = mfma_h(el[z][s], a0, O[z][tt]);
+            O[z][tt] = mfma_h(eh[z][s], a1, O[z][tt]);
+          }
+        }
+      }
     }
-    if (kBufs == 1) __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int z = 0; z < NC; ++z) {
+      f4 out;  // of the columns 4 g + r
+#pragma unroll
+      for (int r = 0; r < 4; ++r) out[r] = a.scale * __shfl(unit[z], 4 * g + r, 16);
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) store_y(c, z, tt, O[z][tt] * out);
+    }
+    // The state.
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      h8 k[2][P];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int p = 0; p < P; ++p) k[s][p] = transposed(kc, p, b, s);
+#pragma unroll
+      for (int z = 0; z < NC; ++z) S[z][b] *= end;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int z = 0; z < NC; ++z) {
+          S[z][b] = mfma_h(k[s][0], uh[z][s], S[z][b]);
+          S[z][b] = mfma_h(k[s][0], ul[z][s], S[z][b]);
+          if constexpr (P == 2) S[z][b] = mfma_h(k[s][1], uh[z][s], S[z][b]);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (kBufs == 1) __syncthreads();  // every wave is done with k and q
   }
   const int64_t slot_out = a.out_slots ? a.out_slots[n] : n;
   if (a.state_out && slot_out >= 0 && slot_out < a.out_count) {
@@ -834,8 +930,8 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(DeltaArgs a) {
 #pragma unroll
       for (int b = 0; b < NB; ++b)
         if (col0 + 16 * z < a.value_dim)
-          *reinterpret_cast<f4*>(a.state_out + ((slot_out * a.hv + h) * a.value_dim + col0 + 16 * z + i) * K +
-                                 32 * (b >> 1) + 8 * g + 4 * (b & 1)) = S[z][b] * unit[z];
+          *reinterpret_cast<f4*>(a.state_out + slot_out * a.hv * a.value_dim * K + state_at + 16 * z * K +
+                                 32 * (b >> 1) + 4 * (b & 1)) = S[z][b] * unit[z];
   }
 }
 
@@ -1028,10 +1124,17 @@ void launch_scan(DeltaArgs a, bool any, hipStream_t st) {
     hipLaunchKernelGGL((prep_kernel<Act, K>), dim3(unsigned(a.rows), unsigned(a.hk)), dim3(kThreads),
                        0, st, a);
   }
-  a.col_groups = (a.value_dim + 127) / 128;
-  const int64_t units = (int64_t(a.sequences) * a.hv + 7) / 8 * 8;
-  hipLaunchKernelGGL((walk_kernel<Act, K, 1, 1>), dim3(unsigned(units * a.col_groups)),
-                     dim3(kWalkThreads), 0, st, a);
+  auto go = [&](auto kernel, int waves, int tiles) {
+    a.col_groups = (a.value_dim + 16 * waves * tiles - 1) / (16 * waves * tiles);
+    const int64_t units = (int64_t(a.sequences) * a.hv + 7) / 8 * 8;
+    hipLaunchKernelGGL(kernel, dim3(unsigned(units * a.col_groups)), dim3(64 * waves), 0, st, a);
+  };
+  if (a.value_dim <= 64)
+    go(walk_kernel<Act, K, 4, 1>, 4, 1);
+  else if constexpr (kPieces<Act> == 1)
+    go(walk_kernel<Act, K, 4, 2>, 4, 2);
+  else
+    go(walk_kernel<Act, K, 8, 1>, 8, 1);
 }
 
 template <typename Act, int K>
