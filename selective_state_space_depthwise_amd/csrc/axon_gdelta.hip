@@ -17,6 +17,12 @@
 //   prep_kernel  per chunk and key head: the Gram products, then per value head T (16 x 16 diagonal
 //                blocks by substitution, which stays accurate where keys are alike and powers of M
 //                would cancel; the blocks below by matrix products), A and the row factors.
+//   join_kernel  where there are few heads and long sequences, segments of a sequence are walked at
+//                once: S behind a segment is S0 M + N (each row of S by itself), M (K x K) and N
+//                being what a walk makes of the rows of the identity with v = 0 and of zeros with v.
+//                A first walk finds M and N of all segments but the last, the join kernel the state
+//                before each segment, a second walk the outputs: 2.6 times the work, spread over
+//                the GPU.
 //   walk_kernel  per sequence, value head and slice of 16 columns of V one wave walks the
 //                chunks with its slice of the state in registers. The state is held transposed
 //                (S^T, K x 16): the result layout of a 16 x 16 product (lane (g, i), g = lane / 16,
@@ -38,6 +44,7 @@
 // bits: 2^-12 against the 2^-9 of y's own rounding.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -87,6 +94,10 @@ struct DeltaArgs {
   int sequences, hk, hv, ratio, value_dim, col_groups;
   int rows;             // chunk rows of the workspace
   int chunks_per_seq;   // uniform batch
+  int seg_chunks;       // chunks of a segment, 0: sequences are walked whole
+  int segs;             // segments of a sequence at most
+  char* seg_m;          // (segment, value head): M^T, two pieces of K x K fp16
+  float* seg_s;         // (segment, value head): N, then the state before the segment, V x K
 };
 
 __device__ __forceinline__ f4 mfma4(float a, float b, f4 c) {
@@ -528,7 +539,8 @@ __device__ __forceinline__ int swizzle(int t) {
 // The blocks of a lower triangular matrix as operands: row block, and pair of contraction blocks.
 constexpr int kLowerRow[6] = {0, 1, 2, 3, 2, 3}, kLowerCol[6] = {0, 0, 0, 0, 1, 1};
 
-template <typename Act, int K, int W, int NC>
+// LOCAL: the first walk over segments: no outputs; columns V .. V + K - 1 are the identity's.
+template <typename Act, int K, int W, int NC, bool LOCAL>
 __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
   constexpr int P = kPieces<Act>;
   constexpr int NB = K / 16, KB = K / 32;
@@ -544,14 +556,24 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
   __shared__ __align__(16) char rs2[2][kLds];
   __shared__ __align__(16) char vs[W][kQ * 16 * NC * sizeof(Act)];
 
-  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-  const int64_t nh = int64_t(slot / a.col_groups) * 8 + xcd;
-  if (nh >= int64_t(a.sequences) * a.hv) return;
+  // The value heads of a key head, and the column groups of each, go to one XCD: k and q come to its
+  // L2 once.
+  const int xcd = blockIdx.x & 7;
+  int slot = blockIdx.x >> 3;
+  const int group = slot % a.col_groups;
+  slot /= a.col_groups;
+  const int vh = slot % a.ratio;
+  slot /= a.ratio;
+  const int seg = a.seg_chunks ? slot % a.segs : 0;
+  if (a.seg_chunks) slot /= a.segs;
+  const int64_t nk = int64_t(slot) * 8 + xcd;
+  if (nk >= int64_t(a.sequences) * a.hk) return;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, i = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n = static_cast<int>(nh / a.hv), h = static_cast<int>(nh - int64_t(n) * a.hv);
-  const int hk = h / a.ratio;
-  const int col0 = ((slot % a.col_groups) * W + w) * 16 * NC;
+  int n = static_cast<int>(nk / a.hk);
+  const int hk = static_cast<int>(nk - int64_t(n) * a.hk), h = hk * a.ratio + vh;
+  const int col0 = (group * W + w) * 16 * NC;
+  const int columns = LOCAL ? a.value_dim + K : a.value_dim;
   int64_t begin, len, row0;
   if (a.starts) {
     begin = a.starts[n];
@@ -564,23 +586,45 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
   }
   int64_t chunks = len > 0 ? (len + kQ - 1) / kQ : 0;
   if (chunks > a.rows - row0) chunks = a.rows - row0;
+  int64_t seg_row = 0;  // of this sequence's first segment: no two sequences share a row
+  bool last = true;
+  if (a.seg_chunks) {
+    seg_row = row0 / a.seg_chunks + n;
+    const int64_t before = int64_t(seg) * a.seg_chunks;
+    if (seg > 0 && before >= chunks) return;
+    last = before + a.seg_chunks >= chunks;
+    if (LOCAL && last) return;
+    begin += before * kQ, len -= before * kQ, row0 += before, chunks -= before;
+    if (!last) chunks = a.seg_chunks, len = int64_t(a.seg_chunks) * kQ;
+  }
 
   // The state in units of its columns: S / unit.
   f4 S[NC][NB];
   float unit[NC], inverse[NC];
   // Element (z, b, r) is row 32 (b / 2) + 8 g + 4 (b % 2) + r of column col0 + 16 z + i.
-  const int64_t slot_in = a.in_slots ? a.in_slots[n] : n;
-  const bool have = a.state_in && slot_in >= 0 && slot_in < a.in_count;
   const int64_t state_at = (int64_t(h) * a.value_dim + col0 + i) * K + 8 * g;
+  const int64_t state_size = int64_t(a.hv) * a.value_dim * K;
+  const float* from = nullptr;
+  if (!LOCAL && a.seg_chunks) {
+    from = a.seg_s + (seg_row + seg) * state_size;
+  } else if (!LOCAL && a.state_in) {
+    const int64_t slot_in = a.in_slots ? a.in_slots[n] : n;
+    if (slot_in >= 0 && slot_in < a.in_count) from = a.state_in + slot_in * state_size;
+  }
 #pragma unroll
   for (int z = 0; z < NC; ++z) {
     unit[z] = inverse[z] = 1.0f;
+    const int one = col0 + 16 * z + i - a.value_dim;  // LOCAL: the identity's row
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       S[z][b] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (have && col0 + 16 * z < a.value_dim)
-        S[z][b] = *reinterpret_cast<const f4*>(a.state_in + slot_in * a.hv * a.value_dim * K + state_at +
-                                               16 * z * K + 32 * (b >> 1) + 4 * (b & 1));
+      if (from && col0 + 16 * z < a.value_dim)
+        S[z][b] = *reinterpret_cast<const f4*>(from + state_at + 16 * z * K + 32 * (b >> 1) + 4 * (b & 1));
+      if (LOCAL) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (32 * (b >> 1) + 8 * g + 4 * (b & 1) + r == one) S[z][b][r] = 1.0f;
+      }
     }
   }
 
@@ -618,7 +662,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
       const uint32_t ko = fresh(t * koff + piece * 8 * es), qo = fresh(t * qoff + piece * 8 * es);
       sh[u] = *reinterpret_cast<const float2*>(rec + rows_at(P) + kRowKQ * kQ * 4 + t * 8);
       pk[u].load(kr, ko);
-      pq[u].load(qr, qo);
+      if (!LOCAL) pq[u].load(qr, qo);
     }
   };
   auto store = [&](int buf) {
@@ -633,6 +677,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
         *reinterpret_cast<w2*>(&ks[buf][p * kMat + to]) = w2{out[p][0], out[p][1]};
         *reinterpret_cast<w2*>(&ks[buf][p * kMat + kHalf + to]) = w2{out[p][2], out[p][3]};
       }
+      if (LOCAL) continue;
       pq[u].pieces(sh[u].y, out);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
@@ -737,7 +782,9 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     end = end_next;
     // This wave's parts of the record and v are in LDS: vector memory operations of a wave complete
     // in the order of their issue, and behind them and k and q only y's 4 NC stores were issued.
-    if (NC == 1)
+    if (LOCAL)
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    else if (NC == 1)
       asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
     else
       asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
@@ -757,7 +804,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
       float m = 0.0f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) m = max4(m, S[z][b]);
-      m = column_max(fmaxf(v.largest(), m * unit[z]));
+      m = column_max(fmaxf(col0 + 16 * z < a.value_dim ? v.largest() : 0.0f, m * unit[z]));
       // The unit stays while the column's largest is between 2^2 and 2^8 of it.
       const float at = m * inverse[z];
       if (__any(m > 0.0f && !(at >= 0x1p2f && at <= 0x1p8f))) {
@@ -780,7 +827,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           kf[kb % kSets][tt][p] = operand(kc, p, tt, kb);
-          qf[kb % kSets][tt][p] = operand(qc, p, tt, kb);
+          if (!LOCAL) qf[kb % kSets][tt][p] = operand(qc, p, tt, kb);
         }
     };
     if (kSets == 2) fetch(0);
@@ -803,18 +850,22 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
       for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
         for (int z = 0; z < NC; ++z) X[z][tt] = mfma_h(k[tt][0], lo[z], X[z][tt]);
+      if constexpr (!LOCAL) {
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt)
+        for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-        for (int z = 0; z < NC; ++z) O[z][tt] = mfma_h(hi[z], q[tt][0], kb ? O[z][tt] : zero);
+          for (int z = 0; z < NC; ++z) O[z][tt] = mfma_h(hi[z], q[tt][0], kb ? O[z][tt] : zero);
+      }
       if constexpr (P == 2) {
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
           for (int z = 0; z < NC; ++z) {
-            O[z][tt] = mfma_h(lo[z], q[tt][0], O[z][tt]);
             X[z][tt] = mfma_h(k[tt][1], hi[z], X[z][tt]);
-            O[z][tt] = mfma_h(hi[z], q[tt][1], O[z][tt]);
+            if constexpr (!LOCAL) {
+              O[z][tt] = mfma_h(lo[z], q[tt][0], O[z][tt]);
+              O[z][tt] = mfma_h(hi[z], q[tt][1], O[z][tt]);
+            }
           }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -825,12 +876,13 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
       Column<Act> v;  // read again: it would not fit the registers during the products
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) load4(v, z, tt);
+      const float up = !LOCAL || col0 + 16 * z < a.value_dim ? inverse[z] : 0.0f;
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
         const f4 f = row4(kRowX, tt);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          X[z][tt][r] = fmaf(-f[r], X[z][tt][r], v.value(tt, r) * inverse[z]);
+          X[z][tt][r] = fmaf(-f[r], X[z][tt][r], v.value(tt, r) * up);
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s) split8(X[z][2 * s], X[z][2 * s + 1], &xh[z][s], &xl[z][s]);
@@ -863,43 +915,47 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
       for (int z = 0; z < NC; ++z)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if constexpr (P == 1)
+          if constexpr (!LOCAL && P == 1)
             eh[z][s] = first_piece(E[z][2 * s], E[z][2 * s + 1]);
-          else
+          else if constexpr (!LOCAL)
             split8(E[z][2 * s], E[z][2 * s + 1], &eh[z][s], &el[z][s]);
           split8(E[z][2 * s] * row4(kRowS, 2 * s), E[z][2 * s + 1] * row4(kRowS, 2 * s + 1), &uh[z][s],
                  &ul[z][s]);
         }
+      if constexpr (!LOCAL) {
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        const float f = *reinterpret_cast<const float*>(rs + rows_at(P) + (kRowY * kQ + 16 * tt + i) * 4);
+        for (int tt = 0; tt < 4; ++tt) {
+          const float f = *reinterpret_cast<const float*>(rs + rows_at(P) + (kRowY * kQ + 16 * tt + i) * 4);
 #pragma unroll
-        for (int z = 0; z < NC; ++z) O[z][tt] *= f;
-      }
+          for (int z = 0; z < NC; ++z) O[z][tt] *= f;
+        }
 #pragma unroll
-      for (int e = 0; e < 6; ++e) {
-        const int tt = kLowerRow[e], s = kLowerCol[e];
-        const h8 a0 = lower(2, tt, s);
+        for (int e = 0; e < 6; ++e) {
+          const int tt = kLowerRow[e], s = kLowerCol[e];
+          const h8 a0 = lower(2, tt, s);
 #pragma unroll
-        for (int z = 0; z < NC; ++z) O[z][tt] = mfma_h(eh[z][s], a0, O[z][tt]);
-        if constexpr (P == 2) {
-          const h8 a1 = lower(3, tt, s);
+          for (int z = 0; z < NC; ++z) O[z][tt] = mfma_h(eh[z][s], a0, O[z][tt]);
+          if constexpr (P == 2) {
+            const h8 a1 = lower(3, tt, s);
 #pragma unroll
-          for (int z = 0; z < NC; ++z) {
-            O[z][tt] = mfma_h(el[z][s], a0, O[z][tt]);
-            O[z][tt] = mfma_h(eh[z][s], a1, O[z][tt]);
+            for (int z = 0; z < NC; ++z) {
+              O[z][tt] = mfma_h(el[z][s], a0, O[z][tt]);
+              O[z][tt] = mfma_h(eh[z][s], a1, O[z][tt]);
+            }
           }
         }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (!LOCAL) {
 #pragma unroll
-    for (int z = 0; z < NC; ++z) {
-      f4 out;  // of the columns 4 g + r
+      for (int z = 0; z < NC; ++z) {
+        f4 out;  // of the columns 4 g + r
 #pragma unroll
-      for (int r = 0; r < 4; ++r) out[r] = a.scale * __shfl(unit[z], 4 * g + r, 16);
+        for (int r = 0; r < 4; ++r) out[r] = a.scale * __shfl(unit[z], 4 * g + r, 16);
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) store_y(c, z, tt, O[z][tt] * out);
+        for (int tt = 0; tt < 4; ++tt) store_y(c, z, tt, O[z][tt] * out);
+      }
     }
     // The state.
 #pragma unroll
@@ -923,16 +979,113 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     __builtin_amdgcn_sched_barrier(0);
     if (kBufs == 1) __syncthreads();  // every wave is done with k and q
   }
+  if constexpr (LOCAL) {
+    float* const to = a.seg_s + (seg_row + seg) * state_size + state_at;
+    _Float16* const mt = reinterpret_cast<_Float16*>(a.seg_m) + ((seg_row + seg) * a.hv + h) * (2 * K * K);
+#pragma unroll
+    for (int z = 0; z < NC; ++z)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int k = 32 * (b >> 1) + 4 * (b & 1);
+        const f4 x = S[z][b] * unit[z];
+        if (col0 + 16 * z < a.value_dim) {
+          *reinterpret_cast<f4*>(to + 16 * z * K + k) = x;
+        } else if (col0 + 16 * z < columns) {
+          const h4 hi = __builtin_convertvector(x, h4);
+          const h4 lo = __builtin_convertvector(x - __builtin_convertvector(hi, f4), h4);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int at = (k + 8 * g + r) * K + col0 + 16 * z + i - a.value_dim;
+            mt[at] = hi[r];
+            mt[K * K + at] = lo[r];
+          }
+        }
+      }
+    return;
+  }
   const int64_t slot_out = a.out_slots ? a.out_slots[n] : n;
-  if (a.state_out && slot_out >= 0 && slot_out < a.out_count) {
+  if (a.state_out && last && slot_out >= 0 && slot_out < a.out_count) {
 #pragma unroll
     for (int z = 0; z < NC; ++z)
 #pragma unroll
       for (int b = 0; b < NB; ++b)
         if (col0 + 16 * z < a.value_dim)
-          *reinterpret_cast<f4*>(a.state_out + slot_out * a.hv * a.value_dim * K + state_at + 16 * z * K +
+          *reinterpret_cast<f4*>(a.state_out + slot_out * state_size + state_at + 16 * z * K +
                                  32 * (b >> 1) + 4 * (b & 1)) = S[z][b] * unit[z];
   }
+}
+
+// ---- the states before the segments -------------------------------------------------------------
+// Grid (sequence and value head, column tiles of V in fours), one wave a tile of 16 columns: segment
+// after segment S <- S M + N, transposed as in the walk, M^T as left operand straight from L2 (one
+// row of M^T per lane and product, 16 bytes). N's place takes the state before the segment: the second
+// walk reads no other, so that the last segment may write the state in place.
+template <int K>
+__global__ __launch_bounds__(kThreads) void join_kernel(DeltaArgs a) {
+  constexpr int NB = K / 16, KB = K / 32;
+  const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+  const int n = blockIdx.x / a.hv, h = blockIdx.x - n * a.hv;
+  const int col0 = (blockIdx.y * 4 + (threadIdx.x >> 6)) * 16;
+  if (col0 >= a.value_dim) return;
+  int64_t len, row0;
+  if (a.starts) {
+    const int64_t begin = a.starts[n];
+    len = a.starts[n + 1] - begin;
+    row0 = a.block_starts[n];
+    if (begin < 0 || begin > a.tokens || row0 < 0 || row0 > a.rows) len = row0 = 0;
+    if (len > a.tokens - begin) len = a.tokens - begin;
+  } else {
+    len = a.seqlen, row0 = int64_t(n) * a.chunks_per_seq;
+  }
+  int64_t chunks = len > 0 ? (len + kQ - 1) / kQ : 0;
+  if (chunks > a.rows - row0) chunks = a.rows - row0;
+  const int64_t seg_row = row0 / a.seg_chunks + n;
+  const int64_t state_at = (int64_t(h) * a.value_dim + col0 + i) * K + 8 * g;
+  const int64_t state_size = int64_t(a.hv) * a.value_dim * K;
+  f4 S[NB];
+  const int64_t slot_in = a.in_slots ? a.in_slots[n] : n;
+  const bool have = a.state_in && slot_in >= 0 && slot_in < a.in_count;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+    S[b] = have ? *reinterpret_cast<const f4*>(a.state_in + slot_in * state_size + state_at +
+                                               32 * (b >> 1) + 4 * (b & 1))
+                : f4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t seg = 0; (seg + 1) * a.seg_chunks < chunks; ++seg) {
+    float* const at = a.seg_s + (seg_row + seg) * state_size + state_at;
+    const _Float16* const mt = reinterpret_cast<const _Float16*>(a.seg_m) +
+                               ((seg_row + seg) * a.hv + h) * (2 * K * K) +
+                               (8 * (i >> 2) + (i & 3)) * K + 8 * g;
+    float m = 0.0f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) m = max4(m, S[b]);
+    const Scale unit = scale_of(column_max(m));
+    h8 hi[KB], lo[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+      split8(S[2 * kb] * (unit.up * 0x1p5f), S[2 * kb + 1] * (unit.up * 0x1p5f), &hi[kb], &lo[kb]);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float* const to = at + 32 * (b >> 1) + 4 * (b & 1);
+      const _Float16* const row = mt + (32 * (b >> 1) + 4 * (b & 1)) * K;
+      f4 x = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        const h8 mh = *reinterpret_cast<const h8*>(row + 32 * kb);
+        const h8 ml = *reinterpret_cast<const h8*>(row + K * K + 32 * kb);
+        x = mfma_h(mh, hi[kb], x);
+        x = mfma_h(mh, lo[kb], x);
+        x = mfma_h(ml, hi[kb], x);
+      }
+      x = x * (unit.down * 0x1p-5f) + *reinterpret_cast<const f4*>(to);
+      *reinterpret_cast<f4*>(to) = S[b];
+      S[b] = x;
+    }
+  }
+  const int64_t final = chunks > 0 ? (chunks - 1) / a.seg_chunks : 0;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+    *reinterpret_cast<f4*>(a.seg_s + (seg_row + final) * state_size + state_at + 32 * (b >> 1) +
+                           4 * (b & 1)) = S[b];
 }
 
 // ---- one token a row ----------------------------------------------------------------------------
@@ -1037,6 +1190,7 @@ constexpr int64_t kMaxGrid = 65535;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 
 constexpr int64_t kMaxRow = int64_t(1) << 22;  // elements between two rows
+constexpr int64_t kSegmentUnits = 64, kSegmentMin = 8;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -1088,9 +1242,28 @@ axon_status check_params(const axon_gated_delta_params* p) {
 // Chunk rows for any lengths (axon_sequence_tables' rows for block 64).
 int64_t rows_of(const axon_gated_delta_shape* s) { return s->tokens / kQ + s->sequences; }
 
-size_t workspace_of(const axon_gated_delta_shape* s) {
-  const size_t record = record_bytes(s->act_dtype == AXON_BF16 ? 1 : 2);
-  return s->tokens ? record * size_t(rows_of(s)) * size_t(s->value_heads) : 0;
+struct ScanPlan {
+  int64_t seg_chunks = 0;  // chunks of a segment, 0: none
+  size_t off_m = 0, off_s = 0, bytes = 0;
+};
+
+// Workspace and segments from the shape alone. Sequences are split where their heads leave most of
+// the 256 CUs idle (a workgroup a head) and they are long enough for it to pay: at 32 heads 16384
+// tokens take @@T1@@ ms in 16 segments and @@T0@@ ms in one.
+ScanPlan plan_scan(const axon_gated_delta_shape* s) {
+  ScanPlan p;
+  if (!s->tokens) return p;
+  const size_t rows = size_t(rows_of(s)), hv = size_t(s->value_heads);
+  p.bytes = record_bytes(s->act_dtype == AXON_BF16 ? 1 : 2) * rows * hv;
+  const int64_t units = s->sequences * s->value_heads, chunks = s->tokens / kQ / s->sequences;
+  if (units > kSegmentUnits || chunks < kSegmentMin * 4) return p;
+  const int64_t segs = std::min<int64_t>(512 / units, chunks / kSegmentMin);
+  p.seg_chunks = (chunks + segs - 1) / segs;
+  const size_t count = (rows / size_t(p.seg_chunks) + size_t(s->sequences)) * hv;
+  p.off_m = (p.bytes + 255) / 256 * 256;
+  p.off_s = p.off_m + count * 4 * size_t(s->key_dim * s->key_dim);
+  p.bytes = p.off_s + count * 4 * size_t(s->value_dim * s->key_dim);
+  return p;
 }
 
 struct Strides {
@@ -1124,17 +1297,35 @@ void launch_scan(DeltaArgs a, bool any, hipStream_t st) {
     hipLaunchKernelGGL((prep_kernel<Act, K>), dim3(unsigned(a.rows), unsigned(a.hk)), dim3(kThreads),
                        0, st, a);
   }
-  auto go = [&](auto kernel, int waves, int tiles) {
-    a.col_groups = (a.value_dim + 16 * waves * tiles - 1) / (16 * waves * tiles);
-    const int64_t units = (int64_t(a.sequences) * a.hv + 7) / 8 * 8;
-    hipLaunchKernelGGL(kernel, dim3(unsigned(units * a.col_groups)), dim3(64 * waves), 0, st, a);
+  const bool split = any && a.segs > 1;
+  if (!split) a.seg_chunks = 0;
+  auto go = [&](auto kernel, int waves, int tiles, int columns) {
+    DeltaArgs b = a;
+    b.col_groups = (columns + 16 * waves * tiles - 1) / (16 * waves * tiles);
+    const int64_t keys = (int64_t(a.sequences) * a.hk + 7) / 8 * 8;
+    const int64_t wgs = keys * a.ratio * b.col_groups * (split ? a.segs : 1);
+    hipLaunchKernelGGL(kernel, dim3(unsigned(wgs)), dim3(64 * waves), 0, st, b);
   };
-  if (a.value_dim <= 64)
-    go(walk_kernel<Act, K, 4, 1>, 4, 1);
-  else if constexpr (kPieces<Act> == 1)
-    go(walk_kernel<Act, K, 4, 2>, 4, 2);
-  else
-    go(walk_kernel<Act, K, 8, 1>, 8, 1);
+  if (split) {
+    if constexpr (kPieces<Act> == 1)
+      go(walk_kernel<Act, K, 4, 2, true>, 4, 2, a.value_dim + K);
+    else
+      go(walk_kernel<Act, K, 8, 1, true>, 8, 1, a.value_dim + K);
+    hipLaunchKernelGGL(join_kernel<K>, dim3(unsigned(a.sequences * a.hv), unsigned((a.value_dim + 63) / 64)),
+                       dim3(kThreads), 0, st, a);
+  }
+  const int64_t units = int64_t(a.sequences) * a.hv * (split ? a.segs : 1);
+  if (a.value_dim <= 64) {
+    go(walk_kernel<Act, K, 4, 1, false>, 4, 1, a.value_dim);
+    return;
+  }
+  if constexpr (kPieces<Act> == 1) {
+    if (units >= 512 && !a.starts) {
+      go(walk_kernel<Act, K, 4, 2, false>, 4, 2, a.value_dim);
+      return;
+    }
+  }
+  go(walk_kernel<Act, K, 8, 1, false>, 8, 1, a.value_dim);
 }
 
 template <typename Act, int K>
@@ -1160,7 +1351,7 @@ extern "C" {
 
 size_t axon_gated_delta_scan_workspace_bytes(const axon_gated_delta_shape* shape) {
   if (axon::check_shape(shape) != AXON_OK) return 0;
-  return axon::workspace_of(shape);
+  return axon::plan_scan(shape).bytes;
 }
 
 axon_status axon_gated_delta_scan(const axon_gated_delta_shape* shape,
@@ -1193,7 +1384,8 @@ axon_status axon_gated_delta_scan(const axon_gated_delta_shape* shape,
       if (!p || !aligned16(p)) return AXON_ERR_INVALID_ARGUMENT;
   }
   const int64_t rows = rows_of(shape);
-  const size_t need = workspace_of(shape);
+  const ScanPlan plan = plan_scan(shape);
+  const size_t need = plan.bytes;
   if (workspace_bytes < need) return AXON_ERR_WORKSPACE_TOO_SMALL;
   if (need && (!workspace || !aligned16(workspace))) return AXON_ERR_INVALID_ARGUMENT;
 
@@ -1238,6 +1430,14 @@ axon_status axon_gated_delta_scan(const axon_gated_delta_shape* shape,
   a.seqlen = s.tokens / s.sequences;
   a.chunks_per_seq = int((a.seqlen + kQ - 1) / kQ);
   a.rows = int(tables ? rows : s.sequences * a.chunks_per_seq);
+  if (plan.seg_chunks) {
+    // The most chunks one sequence can have: all tokens in it.
+    const int64_t most = tables ? (s.tokens + kQ - 1) / kQ : a.chunks_per_seq;
+    a.seg_chunks = int(plan.seg_chunks);
+    a.segs = int((most + plan.seg_chunks - 1) / plan.seg_chunks);
+    a.seg_m = a.records + plan.off_m;
+    a.seg_s = reinterpret_cast<float*>(a.records + plan.off_s);
+  }
   const bool bf = s.act_dtype == AXON_BF16;
   hipStream_t stm = static_cast<hipStream_t>(stream);
   if (s.key_dim == 64)

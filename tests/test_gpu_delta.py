@@ -222,6 +222,45 @@ def test_parts_of_one_projection(act):
     assert torch.equal(p0, p1)
 
 
+@pytest.mark.parametrize("act,K,V", [("f32", 128, 128), ("bf16", 128, 128), ("bf16", 64, 48),
+                                     ("f32", 64, 240), ("bf16", 128, 256)])
+def test_long_sequences_in_segments(act, K, V):
+    """Few heads and long sequences are walked in segments at once: a uniform batch in place, and
+    packed sequences of which some fill many segments and some none."""
+    say(f"[delta] segments {act} K={K} V={V}")
+    axon = _axon()
+    hk, hv, L = 1, 2, 2200
+    d = make((2, L), hk, hv, K, V, act, seed=31)
+    d["A_log"] -= 3.0  # states that live through segments
+    s = state(2, hv, V, K, 6)
+    start = s.clone()
+    y, _ = axon.gated_delta_scan(**d, state_in=s, state_out=s)
+    torch.cuda.synchronize()
+    for b in range(2):
+        yr, sr, big = ref.delta_tokens(start[b], **rows(d, b))
+        close(y[b], yr, 2 * big, f"y[{b}]")
+        close(s[b], sr, 2 * big, f"state[{b}]")
+    p = {x: (t if x in ("A_log", "dt_bias") else t.flatten(0, 1)) for x, t in d.items()}
+    lengths = [3000, 0, 1, 1399]
+    pool = state(6, hv, V, K, 7)
+    before = pool.clone()
+    slots = torch.tensor([5, 0, -1, 2], dtype=torch.int32).cuda()
+    y, _ = axon.gated_delta_scan(**p, lengths=torch.tensor(lengths, dtype=torch.int32).cuda(),
+                                 state_in=pool, in_slots=slots, state_out=pool, out_slots=slots)
+    torch.cuda.synchronize()
+    at = 0
+    for n, length in enumerate(lengths):
+        i = int(slots[n])
+        yr, sr, big = ref.delta_tokens(before[i] if i >= 0 else torch.zeros(hv, V, K),
+                                       **rows(p, slice(at, at + length)))
+        close(y[at:at + length], yr, 2 * big, f"y of sequence {n}")
+        if i >= 0:
+            close(pool[i], sr, 2 * big, f"state of sequence {n}")
+        at += length
+    for i in (1, 3, 4):
+        assert torch.equal(pool[i], before[i])
+
+
 def test_continuation_in_place_and_empty():
     axon = _axon()
     d = make((2, 177), 1, 2, 128, 64, "f32", seed=8)
