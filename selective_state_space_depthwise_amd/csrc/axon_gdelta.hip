@@ -22,7 +22,10 @@
 //                being what a walk makes of the rows of the identity with v = 0 and of zeros with v.
 //                A first walk finds M and N of all segments but the last, the join kernel the state
 //                before each segment, a second walk the outputs: 2.6 times the work, spread over
-//                the GPU.
+//                the GPU. By the contraction of the delta rule a state shrinks at least as its decays
+//                say; where those multiply to less than 2^-160 over a segment's last chunks (beyond
+//                what an fp32 product of them holds) nothing before those chunks is left at its end:
+//                the first walk begins there, and M is zero.
 //   walk_kernel  per sequence, value head and slice of 16 columns of V one wave walks the
 //                chunks with its slice of the state in registers. The state is held transposed
 //                (S^T, K x 16): the result layout of a 16 x 16 product (lane (g, i), g = lane / 16,
@@ -47,6 +50,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "axon_device.h"
 #include "axon_internal.h"
@@ -56,7 +60,6 @@ namespace {
 
 constexpr int kQ = 64;  // tokens of a chunk
 constexpr int kThreads = 256;
-constexpr int kMS = kQ + 4;  // LDS row stride of 64 x 64 matrices
 
 typedef float f4 __attribute__((ext_vector_type(4)));
 
@@ -67,7 +70,8 @@ constexpr int kPieces = sizeof(Act) == 2 ? 1 : 2;
 // What prep leaves for each (chunk, value head): T in two pieces and A in one or two, each as ten
 // 16 x 16 blocks on and below the diagonal (block I (I + 1) / 2 + J), a block as 64 lanes x 4 fp16
 // in left-operand order (lane (g, i): row i, columns 4 g .. 4 g + 3); then the row
-// factors of the 64 tokens, fp32, and e^{g_last}. What the walk keeps in LDS comes first.
+// factors of the 64 tokens, fp32, and e^{g_last} with its base-2 logarithm. What the walk keeps in
+// LDS comes first.
 constexpr int kBlocks = 10;
 constexpr int kBlockBytes = 512;
 enum Row { kRowX, kRowS, kRowY, kRowKQ, kRows = kRowKQ + 2 };
@@ -97,6 +101,7 @@ struct DeltaArgs {
   int seg_chunks;       // chunks of a segment, 0: sequences are walked whole
   int segs;             // segments of a sequence at most
   char* seg_m;          // (segment, value head): M^T, two pieces of K x K fp16
+  int32_t* seg_flag;    // (segment, value head): whether M is not zero
   float* seg_s;         // (segment, value head): N, then the state before the segment, V x K
 };
 
@@ -298,26 +303,59 @@ __device__ __forceinline__ float max4(float m, f4 x) {
 }
 
 // ---- T, A and the row factors of every chunk ----------------------------------------------------
-// Grid (chunk rows, key heads), 4 waves. Wave w owns rows 16 w .. 16 w + 15 of the Gram products
-// and column block w of the inverse. The Gram products of bf16 inputs are exact bf16 products, those
-// of fp32 inputs and the inverse run on v_mfma_f32_16x16x4f32 (layout in axon_ssd.hip).
+// Grid (chunk rows, key heads), 4 waves; the value heads of the key head in pairs. Every 16 x 16
+// block is computed transposed (rows: 4 columns of the block, column: its row i), which is at once
+// the operand order of the record (a lane holds 4 consecutive entries of a row) and the layout in
+// which one product's result is the next one's right operand, so only M and the inverses of its
+// diagonal blocks pass through LDS. Wave w owns rows 16 w .. of the Gram products (bf16: exact bf16
+// products; fp32 and the inverse: v_mfma_f32_16x16x4f32). The diagonal blocks of a head are inverted
+// by one wave, block g by lane group g, a column a lane. From T (I + M) = I the blocks below follow
+// row by row: T_IJ = -(sum_{J < S <= I} T_IS M_SJ) D_J with D_J the inverse of diagonal block J; one
+// wave takes row block 3 of a head (9 products), another its rows 2 and 1 (7).
+constexpr int kHeads = 2;      // value heads at a time
+constexpr int kBlockRow = 20;  // floats between the rows of a block in LDS
+
 template <typename Act, int K>
-__global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kernel(DeltaArgs a) {
   constexpr int P = kPieces<Act>;
-  __shared__ float Ms[kQ * kMS];
-  __shared__ float As[kQ * kMS];
-  __shared__ float Ds[4][16 * 20];
-  __shared__ float hi_s[kQ], lo_s[kQ], beta_s[kQ], rk_s[kQ], rq_s[kQ], mk_s[kQ], mq_s[kQ];
+  __shared__ __align__(16) float Ms[kHeads][kBlocks][16 * kBlockRow];
+  __shared__ __align__(16) float hi_s[kHeads][kQ], lo_s[kHeads][kQ], beta_s[kHeads][kQ];
+  __shared__ __align__(16) float rk_s[kQ], rq_s[kQ], mk_s[kQ], mq_s[kQ];
   int64_t first;
   int count;
   if (!chunk_of(a, blockIdx.x, &first, &count)) return;
   const int hk = blockIdx.y;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, i = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, i = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Act* kp = static_cast<const Act*>(a.k) + first * a.k_stride + int64_t(hk) * K;
   const Act* qp = static_cast<const Act*>(a.q) + first * a.q_stride + int64_t(hk) * K;
+  // Steps, decays and write strengths of one head: lane t is token t.
+  auto gates = [&](int h, int at_head) {
+    float dt = 0.0f, beta = 0.0f;
+    if (lane < count) {
+      const int64_t at = (first + lane) * a.hv + h;
+      dt = gate_step(load_act(static_cast<const Act*>(a.dt_raw), at) + a.dt_bias[h], a.dt_min, a.dt_max);
+      beta = sigmoid(load_act(static_cast<const Act*>(a.beta_raw), at));
+    }
+    // No decay below 2^-16384 differs from 0: the bound keeps the sums finite for any dt_max.
+    float hi = fmaxf(dt * decay_rate_log2(a.A_log[h]), -16384.0f), lo = 0.0f;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const float oh = __shfl_up(hi, d, 64), ol = __shfl_up(lo, d, 64);
+      if (lane >= d) {
+        const float s = hi + oh;
+        const float bv = s - hi;
+        const float err = (hi - (s - bv)) + (oh - bv);
+        hi = s;
+        lo = lo + ol + err;
+      }
+    }
+    hi_s[at_head][lane] = hi, lo_s[at_head][lane] = lo, beta_s[at_head][lane] = beta;
+  };
   f4 gk[4], gq[4];
 #pragma unroll
   for (int st = 0; st < 4; ++st) gk[st] = gq[st] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+  float rk, rq;  // of row 16 w + i
   {
     const int t = 16 * w + i;
     float sk = 0.0f, sq = 0.0f, mk = 0.0f, mq = 0.0f;
@@ -334,6 +372,20 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
         krow[b] = t < count ? *reinterpret_cast<const b8*>(kp + t * a.k_stride + 32 * b + 8 * g) : zero;
         qrow[b] = t < count ? *reinterpret_cast<const b8*>(qp + t * a.q_stride + 32 * b + 8 * g) : zero;
       }
+      if (w < kHeads && w < a.ratio) gates(hk * a.ratio + w, w);  // while k and q are on their way
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {
+        if (st > w) continue;
+        const int ts = 16 * st + i;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          col[b] = ts < count ? *reinterpret_cast<const b8*>(kp + ts * a.k_stride + 32 * b + 8 * g) : zero;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          gk[st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(col[b], krow[b], gk[st], 0, 0, 0);
+          gq[st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(col[b], qrow[b], gq[st], 0, 0, 0);
+        }
+      }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         f4 x, y;
@@ -346,47 +398,40 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
         sums(x, sq, mq);
         sums(y, sq, mq);
       }
-#pragma unroll
-      for (int st = 0; st < 4; ++st) {
-        if (st > w) continue;
-        const int ts = 16 * st + i;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          col[b] = ts < count ? *reinterpret_cast<const b8*>(kp + ts * a.k_stride + 32 * b + 8 * g) : zero;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          gk[st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(krow[b], col[b], gk[st], 0, 0, 0);
-          gq[st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qrow[b], col[b], gq[st], 0, 0, 0);
-        }
-      }
     } else {
       constexpr int NB = K / 16;
-      f4 krow[NB], qrow[NB], col[NB];
+      f4 row[NB], col[NB];
       const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (w < kHeads && w < a.ratio) gates(hk * a.ratio + w, w);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        krow[b] = t < count ? *reinterpret_cast<const f4*>(kp + t * a.k_stride + 16 * b + 4 * g) : zero;
-        qrow[b] = t < count ? *reinterpret_cast<const f4*>(qp + t * a.q_stride + 16 * b + 4 * g) : zero;
-      }
+      for (int b = 0; b < NB; ++b)
+        row[b] = t < count ? *reinterpret_cast<const f4*>(kp + t * a.k_stride + 16 * b + 4 * g) : zero;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        sums(krow[b], sk, mk);
-        sums(qrow[b], sq, mq);
-      }
+      for (int b = 0; b < NB; ++b) sums(row[b], sk, mk);
 #pragma unroll
-      for (int st = 0; st < 4; ++st) {
-        if (st > w) continue;
-        const int ts = 16 * st + i;
+      for (int which = 0; which < 2; ++which) {
+        if (which == 1) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          col[b] = ts < count ? *reinterpret_cast<const f4*>(kp + ts * a.k_stride + 16 * b + 4 * g) : zero;
+          for (int b = 0; b < NB; ++b)
+            row[b] = t < count ? *reinterpret_cast<const f4*>(qp + t * a.q_stride + 16 * b + 4 * g) : zero;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+          for (int b = 0; b < NB; ++b) sums(row[b], sq, mq);
+        }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            gk[st] = mfma4(krow[b][e], col[b][e], gk[st]);
-            gq[st] = mfma4(qrow[b][e], col[b][e], gq[st]);
-          }
+        for (int st = 0; st < 4; ++st) {
+          if (st > w) continue;
+          const int ts = 16 * st + i;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            col[b] = ts < count ? *reinterpret_cast<const f4*>(kp + ts * a.k_stride + 16 * b + 4 * g) : zero;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f4& to = which ? gq[st] : gk[st];
+              to = mfma4(col[b][e], row[b][e], to);
+            }
+        }
       }
     }
     sk += __shfl_xor(sk, 16, 64);
@@ -395,126 +440,115 @@ __global__ __launch_bounds__(kThreads) void prep_kernel(DeltaArgs a) {
     sq += __shfl_xor(sq, 32, 64);
     mk = column_max(mk);
     mq = column_max(mq);
-    if (g == 0) {
-      rk_s[t] = 1.0f / sqrtf(sk + a.eps);
-      rq_s[t] = 1.0f / sqrtf(sq + a.eps);
-      mk_s[t] = mk;
-      mq_s[t] = mq;
-    }
+    rk = 1.0f / sqrtf(sk + a.eps);
+    rq = 1.0f / sqrtf(sq + a.eps);
+    if (g == 0) rk_s[t] = rk, rq_s[t] = rq, mk_s[t] = mk, mq_s[t] = mq;
   }
-  for (int vh = 0; vh < a.ratio; ++vh) {
-    const int h = hk * a.ratio + vh;
-    char* rec = a.records + (int64_t(blockIdx.x) * a.hv + h) * record_bytes(P);
-    __syncthreads();  // the previous head's matrices and factors have been read; the norms are in
-    if (w == 0) {
-      float dt = 0.0f, beta = 0.0f;
-      if (lane < count) {
-        const int64_t at = (first + lane) * a.hv + h;
-        dt = gate_step(load_act(static_cast<const Act*>(a.dt_raw), at) + a.dt_bias[h], a.dt_min,
-                       a.dt_max);
-        beta = sigmoid(load_act(static_cast<const Act*>(a.beta_raw), at));
-      }
-      // No decay below 2^-16384 differs from 0: the bound keeps the sums finite for any dt_max.
-      float hi = fmaxf(dt * decay_rate_log2(a.A_log[h]), -16384.0f), lo = 0.0f;
+  for (int v0 = 0; v0 < a.ratio; v0 += kHeads) {
+    const int heads = min(kHeads, a.ratio - v0);
+    if (v0 > 0) {
+      __syncthreads();  // every wave is done with the heads before
+      if (w < heads) gates(hk * a.ratio + v0 + w, w);
+    }
+    __syncthreads();  // gates and norms are in
+    for (int hh = 0; hh < heads; ++hh) {
+      char* rec = a.records + (int64_t(blockIdx.x) * a.hv + hk * a.ratio + v0 + hh) * record_bytes(P);
+      const int t = 16 * w + i;
+      const float ht = hi_s[hh][t], lt = lo_s[hh][t];
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const float oh = __shfl_up(hi, d, 64), ol = __shfl_up(lo, d, 64);
-        if (lane >= d) {
-          const float s = hi + oh;
-          const float bv = s - hi;
-          const float err = (hi - (s - bv)) + (oh - bv);
-          hi = s;
-          lo = lo + ol + err;
+      for (int st = 0; st < 4; ++st) {
+        if (st > w) continue;
+        const int s = 16 * st + 4 * g, blk = w * (w + 1) / 2 + st;
+        const f4 hs = *reinterpret_cast<const f4*>(&hi_s[hh][s]), ls = *reinterpret_cast<const f4*>(&lo_s[hh][s]);
+        const f4 bs = *reinterpret_cast<const f4*>(&beta_s[hh][s]), ks = *reinterpret_cast<const f4*>(&rk_s[s]);
+        f4 m, x;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float e = exp2_diff(ht, lt, hs[r], ls[r]) * (ks[r] * bs[r]);
+          m[r] = s + r < t ? rk * e * gk[st][r] : 0.0f;
+          x[r] = s + r <= t ? rq * e * gq[st][r] : 0.0f;
         }
+        *reinterpret_cast<f4*>(&Ms[hh][blk][i * kBlockRow + 4 * g]) = m;
+        const h4 hi = __builtin_convertvector(x, h4);
+        char* dst = rec + (2 * kBlocks + blk) * kBlockBytes + lane * 8;
+        *reinterpret_cast<h4*>(dst) = hi;
+        if (P == 2)
+          *reinterpret_cast<h4*>(dst + kBlocks * kBlockBytes) =
+              __builtin_convertvector(x - __builtin_convertvector(hi, f4), h4);
       }
-      hi_s[lane] = hi, lo_s[lane] = lo, beta_s[lane] = beta;
-      const float last_hi = __shfl(hi, 63, 64), last_lo = __shfl(lo, 63, 64);
-      const float e = __builtin_amdgcn_exp2f(hi + lo);
-      const Scale k2 = scale_of(mk_s[lane]), q2 = scale_of(mq_s[lane]);
-      float* row = reinterpret_cast<float*>(rec + rows_at(P)) + lane;
-      row[kRowX * kQ] = e * (rk_s[lane] * k2.down);
-      row[kRowS * kQ] = beta * exp2_diff(last_hi, last_lo, hi, lo) * (rk_s[lane] * k2.down);
-      row[kRowY * kQ] = e * (rq_s[lane] * q2.down);
-      *reinterpret_cast<float2*>(row + kRowKQ * kQ + lane) = make_float2(k2.up, q2.up);
-      if (lane == 63) row[kRows * kQ - 63] = e;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int st = 0; st < 4; ++st) {
-      if (st > w) continue;
-      const int s = 16 * st + i;
-      const float hs = hi_s[s], ls = lo_s[s], rks = rk_s[s] * beta_s[s];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * w + 4 * g + r;
-        const float e = exp2_diff(hi_s[t], lo_s[t], hs, ls) * rks;
-        Ms[t * kMS + s] = s < t ? rk_s[t] * e * gk[st][r] : 0.0f;
-        As[t * kMS + s] = s <= t ? rq_s[t] * e * gq[st][r] : 0.0f;
+      if (w == 2 + hh) {  // the row factors: lane t is token t
+        const float hi = hi_s[hh][lane], lo = lo_s[hh][lane];
+        const float e = __builtin_amdgcn_exp2f(hi + lo);
+        const Scale k2 = scale_of(mk_s[lane]), q2 = scale_of(mq_s[lane]);
+        float* row = reinterpret_cast<float*>(rec + rows_at(P)) + lane;
+        row[kRowX * kQ] = e * (rk_s[lane] * k2.down);
+        row[kRowS * kQ] = beta_s[hh][lane] * exp2_diff(hi_s[hh][63], lo_s[hh][63], hi, lo) *
+                          (rk_s[lane] * k2.down);
+        row[kRowY * kQ] = e * (rq_s[lane] * q2.down);
+        *reinterpret_cast<float2*>(row + kRowKQ * kQ + lane) = make_float2(k2.up, q2.up);
+        if (lane == 63) *reinterpret_cast<float2*>(row + kRows * kQ - 63) = make_float2(e, hi + lo);
       }
     }
     __syncthreads();
-    // Diagonal block w: column i of (I + M_ww)^-1 by substitution (the four lane groups alike).
-    {
+    // Column i of the inverse of diagonal block g, in the block's place.
+    if (w < heads) {
+      float* m = Ms[w][g * (g + 1) / 2 + g];
       float x[16];
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         float acc = r == i ? 1.0f : 0.0f;
 #pragma unroll
-        for (int s = 0; s < r; ++s) acc = fmaf(-Ms[(16 * w + r) * kMS + 16 * w + s], x[s], acc);
+        for (int s4 = 0; s4 < r; s4 += 4) {
+          const f4 row = *reinterpret_cast<const f4*>(m + r * kBlockRow + s4);
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            if (s4 + s < r) acc = fmaf(-row[s], x[s4 + s], acc);
+        }
         x[r] = acc;
       }
-      if (g == 0) {
+      // One wave: its reads above are done before these writes are issued.
 #pragma unroll
-        for (int r = 0; r < 16; ++r) Ds[w][r * 20 + i] = x[r];
-      }
+      for (int r = 0; r < 16; ++r) m[r * kBlockRow + i] = x[r];
     }
     __syncthreads();
-    // Column block w of the inverse: X_I = -D_I sum_{w <= S < I} M_IS X_S.
-    f4 X[4];
-#pragma unroll
-    for (int I = 0; I < 4; ++I) {
-      if (I < w) {
-        X[I] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-      } else if (I == w) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) X[I][r] = Ds[I][(4 * g + r) * 20 + i];
-      } else {
-        f4 p = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int S = 0; S < I; ++S) {
-          if (S < w) continue;
-          const f4 m = *reinterpret_cast<const f4*>(&Ms[(16 * I + i) * kMS + 16 * S + 4 * g]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) p = mfma4(m[r], X[S][r], p);
-        }
-        const f4 d = *reinterpret_cast<const f4*>(&Ds[I][i * 20 + 4 * g]);
-        f4 x = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x = mfma4(d[r], p[r], x);
-        X[I] = -x;
-      }
-    }
-    __syncthreads();  // M has been read: T takes its place
-#pragma unroll
-    for (int I = 0; I < 4; ++I) {
-      if (I < w) continue;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) Ms[(16 * I + 4 * g + r) * kMS + 16 * w + i] = X[I][r];
-    }
-    __syncthreads();
-    for (int b = w; b < 2 * kBlocks; b += 4) {
-      const bool is_t = b < kBlocks;
-      const int bb = is_t ? b : b - kBlocks;
-      const int I = bb < 1 ? 0 : bb < 3 ? 1 : bb < 6 ? 2 : 3;
-      const int J = bb - I * (I + 1) / 2;
-      const float* src = (is_t ? Ms : As) + (16 * I + i) * kMS + 16 * J + 4 * g;
-      const f4 x = *reinterpret_cast<const f4*>(src);
-      const h4 hi = __builtin_convertvector(x, h4);
-      char* dst = rec + ((is_t ? 0 : 2 * kBlocks) + bb) * kBlockBytes + lane * 8;
-      *reinterpret_cast<h4*>(dst) = hi;
-      if (is_t || P == 2)
+    const int hh = w & 1;
+    if (hh < heads) {
+      char* rec = a.records + (int64_t(blockIdx.x) * a.hv + hk * a.ratio + v0 + hh) * record_bytes(P);
+      const float(*m)[16 * kBlockRow] = Ms[hh];
+      auto put = [&](int blk, f4 x) {
+        const h4 hi = __builtin_convertvector(x, h4);
+        char* dst = rec + blk * kBlockBytes + lane * 8;
+        *reinterpret_cast<h4*>(dst) = hi;
         *reinterpret_cast<h4*>(dst + kBlocks * kBlockBytes) =
             __builtin_convertvector(x - __builtin_convertvector(hi, f4), h4);
+      };
+      // Row block I of T, from the diagonal leftwards.
+      auto row_block = [&](auto index) {
+        constexpr int I = decltype(index)::value;
+        f4 T[I + 1];
+        T[I] = *reinterpret_cast<const f4*>(m[I * (I + 1) / 2 + I] + i * kBlockRow + 4 * g);
+        put(I * (I + 1) / 2 + I, T[I]);
+#pragma unroll
+        for (int J = I - 1; J >= 0; --J) {
+          f4 p = f4{0.0f, 0.0f, 0.0f, 0.0f}, x = p;
+#pragma unroll
+          for (int S = J + 1; S <= I; ++S)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              p = mfma4(m[S * (S + 1) / 2 + J][(4 * g + r) * kBlockRow + i], T[S][r], p);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) x = mfma4(m[J * (J + 1) / 2 + J][(4 * g + r) * kBlockRow + i], p[r], x);
+          T[J] = -x;
+          put(I * (I + 1) / 2 + J, T[J]);
+        }
+      };
+      if (w < 2) {
+        row_block(std::integral_constant<int, 3>{});
+      } else {
+        row_block(std::integral_constant<int, 2>{});
+        row_block(std::integral_constant<int, 1>{});
+        row_block(std::integral_constant<int, 0>{});
+      }
     }
   }
 }
@@ -597,12 +631,36 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     begin += before * kQ, len -= before * kQ, row0 += before, chunks -= before;
     if (!last) chunks = a.seg_chunks, len = int64_t(a.seg_chunks) * kQ;
   }
+  bool cut = false;
+  if constexpr (LOCAL) {
+    // Lane l: chunk l from the segment's end; the decays of it and of those behind it.
+    const int64_t c = chunks - 1 - lane;
+    float sum = 0.0f;
+    if (c >= 0)
+      sum = *reinterpret_cast<const float*>(a.records + ((row0 + c) * a.hv + h) * int64_t(kRec) + rows_at(P) +
+                                            (kRows * kQ + 1) * 4);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const float o = __shfl_up(sum, d, 64);
+      if (lane >= d) sum += o;
+    }
+    const uint64_t small = __ballot(c >= 0 && sum < -160.0f);
+    cut = small != 0;
+    if (group == 0 && tid == 0) a.seg_flag[(seg_row + seg) * a.hv + h] = !cut;
+    if (cut) {
+      if (group * W * 16 * NC >= a.value_dim) return;
+      const int64_t skip = chunks - 1 - __builtin_ctzll(small);
+      begin += skip * kQ, len -= skip * kQ, row0 += skip, chunks -= skip;
+    }
+  }
 
   // The state in units of its columns: S / unit.
   f4 S[NC][NB];
   float unit[NC], inverse[NC];
   // Element (z, b, r) is row 32 (b / 2) + 8 g + 4 (b % 2) + r of column col0 + 16 z + i.
-  const int64_t state_at = (int64_t(h) * a.value_dim + col0 + i) * K + 8 * g;
+  // Element (z, b, r) of the lane in a state, and the size of a state.
+  const uint32_t state_lane = i * K + 8 * g;
+  const int64_t state_head = (int64_t(h) * a.value_dim + col0) * K;
   const int64_t state_size = int64_t(a.hv) * a.value_dim * K;
   const float* from = nullptr;
   if (!LOCAL && a.seg_chunks) {
@@ -619,11 +677,12 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     for (int b = 0; b < NB; ++b) {
       S[z][b] = f4{0.0f, 0.0f, 0.0f, 0.0f};
       if (from && col0 + 16 * z < a.value_dim)
-        S[z][b] = *reinterpret_cast<const f4*>(from + state_at + 16 * z * K + 32 * (b >> 1) + 4 * (b & 1));
+        S[z][b] = *reinterpret_cast<const f4*>(from + state_head + state_lane + 16 * z * K + 32 * (b >> 1) +
+                                               4 * (b & 1));
       if (LOCAL) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (32 * (b >> 1) + 8 * g + 4 * (b & 1) + r == one) S[z][b][r] = 1.0f;
+          if (!cut && 32 * (b >> 1) + 8 * g + 4 * (b & 1) + r == one) S[z][b][r] = 1.0f;
       }
     }
   }
@@ -721,7 +780,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
   // y is computed transposed (rows: 4 columns 4 g + r, column: token i), so that a lane stores four
   // values in a row. Rows behind the sequence and columns behind V lie outside the range.
   const int64_t y_stride = int64_t(a.hv) * a.value_dim;
-  const uint32_t yoff = (i * static_cast<uint32_t>(y_stride) + col0 + 4 * g) * es;
+  uint32_t yoff = 0;  // computed where it is used
   auto store_y = [&](int64_t c, int z, int tt, f4 o) {
     const uint32_t off = col0 + 16 * z < a.value_dim ? yoff + 16 * z * es : kNoStore;
     const int64_t first = begin + c * kQ;
@@ -948,6 +1007,8 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (!LOCAL) {
+      const uint32_t l = fresh(lane);
+      yoff = ((l & 15) * static_cast<uint32_t>(y_stride) + col0 + 4 * (l >> 4)) * es;
 #pragma unroll
       for (int z = 0; z < NC; ++z) {
         f4 out;  // of the columns 4 g + r
@@ -980,7 +1041,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     if (kBufs == 1) __syncthreads();  // every wave is done with k and q
   }
   if constexpr (LOCAL) {
-    float* const to = a.seg_s + (seg_row + seg) * state_size + state_at;
+    float* const to = a.seg_s + (seg_row + seg) * state_size + state_head + fresh(lane & 15) * K + 8 * g;
     _Float16* const mt = reinterpret_cast<_Float16*>(a.seg_m) + ((seg_row + seg) * a.hv + h) * (2 * K * K);
 #pragma unroll
     for (int z = 0; z < NC; ++z)
@@ -990,12 +1051,14 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
         const f4 x = S[z][b] * unit[z];
         if (col0 + 16 * z < a.value_dim) {
           *reinterpret_cast<f4*>(to + 16 * z * K + k) = x;
-        } else if (col0 + 16 * z < columns) {
+        } else if (!cut && col0 + 16 * z < columns) {
           const h4 hi = __builtin_convertvector(x, h4);
           const h4 lo = __builtin_convertvector(x - __builtin_convertvector(hi, f4), h4);
+          // Operand (b, row / 32) of M^T: lane (row / 8 % 4, this row of the tile), entry row % 8.
+          const int row = col0 + 16 * z + i - a.value_dim;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int at = (k + 8 * g + r) * K + col0 + 16 * z + i - a.value_dim;
+            const int at = ((b * KB + (row >> 5)) * 64 + ((row >> 3) & 3) * 16 + 4 * g + r) * 8 + (row & 7);
             mt[at] = hi[r];
             mt[K * K + at] = lo[r];
           }
@@ -1005,28 +1068,31 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
   }
   const int64_t slot_out = a.out_slots ? a.out_slots[n] : n;
   if (a.state_out && last && slot_out >= 0 && slot_out < a.out_count) {
+    const uint32_t l = fresh(lane);  // not kept through the loop
+    float* const to = a.state_out + slot_out * state_size + state_head + (l & 15) * K + 8 * (l >> 4);
 #pragma unroll
     for (int z = 0; z < NC; ++z)
 #pragma unroll
       for (int b = 0; b < NB; ++b)
         if (col0 + 16 * z < a.value_dim)
-          *reinterpret_cast<f4*>(a.state_out + slot_out * state_size + state_at + 16 * z * K +
-                                 32 * (b >> 1) + 4 * (b & 1)) = S[z][b] * unit[z];
+          *reinterpret_cast<f4*>(to + 16 * z * K + 32 * (b >> 1) + 4 * (b & 1)) = S[z][b] * unit[z];
   }
 }
 
 // ---- the states before the segments -------------------------------------------------------------
-// Grid (sequence and value head, column tiles of V in fours), one wave a tile of 16 columns: segment
-// after segment S <- S M + N, transposed as in the walk, M^T as left operand straight from L2 (one
-// row of M^T per lane and product, 16 bytes). N's place takes the state before the segment: the second
-// walk reads no other, so that the last segment may write the state in place.
+// Grid (sequence and value head, groups of 128 columns of V), 4 waves of two column tiles: segment
+// after segment S <- S M + N, transposed as in the walk, with M^T in LDS in operand order (the next
+// segment's on its way meanwhile). N's place takes the state before the segment: the second walk
+// reads no other, so that the last segment may write the state in place.
 template <int K>
 __global__ __launch_bounds__(kThreads) void join_kernel(DeltaArgs a) {
-  constexpr int NB = K / 16, KB = K / 32;
+  constexpr int NB = K / 16, KB = K / 32, NC = 2;
+  constexpr int kBytes = 4 * K * K, kLoads = kBytes / 1024;  // of M^T: two pieces
+  __shared__ __align__(16) char ms[2][kBytes];
   const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = blockIdx.x / a.hv, h = blockIdx.x - n * a.hv;
-  const int col0 = (blockIdx.y * 4 + (threadIdx.x >> 6)) * 16;
-  if (col0 >= a.value_dim) return;
+  const int col0 = (blockIdx.y * 4 + w) * 16 * NC;
   int64_t len, row0;
   if (a.starts) {
     const int64_t begin = a.starts[n];
@@ -1040,52 +1106,128 @@ __global__ __launch_bounds__(kThreads) void join_kernel(DeltaArgs a) {
   int64_t chunks = len > 0 ? (len + kQ - 1) / kQ : 0;
   if (chunks > a.rows - row0) chunks = a.rows - row0;
   const int64_t seg_row = row0 / a.seg_chunks + n;
-  const int64_t state_at = (int64_t(h) * a.value_dim + col0 + i) * K + 8 * g;
+  const int64_t final = chunks > 0 ? (chunks - 1) / a.seg_chunks : 0;
   const int64_t state_size = int64_t(a.hv) * a.value_dim * K;
-  f4 S[NB];
+  // Tiles behind the columns work on the last one's and store nothing.
+  // (State sizes are below 2^31 bytes here: a split scan has at most kSegmentUnits heads.)
+  uint32_t state_at[NC], store_at[NC];
+#pragma unroll
+  for (int z = 0; z < NC; ++z) {
+    const bool in = col0 + 16 * z < a.value_dim;
+    const int col = in ? col0 + 16 * z + i : a.value_dim - 16 + i;
+    state_at[z] = (static_cast<uint32_t>(h) * a.value_dim + col) * K + 8 * g;
+    store_at[z] = in ? state_at[z] * 4 : kNoStore;
+  }
+  auto store = [&](rsrc_t to, int z, int b, f4 x) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(w4, x), to,
+                                           store_at[z] + 128 * (b >> 1) + 16 * (b & 1), 0, 0);
+  };
+  auto nonzero = [&](int64_t seg) {
+    return __builtin_amdgcn_readfirstlane(a.seg_flag[(seg_row + seg) * a.hv + h]) != 0;
+  };
+  auto load = [&](int64_t seg, int buf) {
+    const char* from = a.seg_m + ((seg_row + seg) * a.hv + h) * int64_t(kBytes);
+#pragma unroll
+    for (int u = 0; u < kLoads; u += 4)
+      load_to_lds(from + (u + w) * 1024, lane * 16, &ms[buf][(u + w) * 1024]);
+  };
+  f4 S[NC][NB], N[2][NC][NB];
+  auto load_n = [&](int64_t seg, int buf) {
+    const float* from = a.seg_s + (seg_row + seg) * state_size;
+#pragma unroll
+    for (int z = 0; z < NC; ++z)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        N[buf][z][b] = *reinterpret_cast<const f4*>(from + state_at[z] + 32 * (b >> 1) + 4 * (b & 1));
+  };
   const int64_t slot_in = a.in_slots ? a.in_slots[n] : n;
   const bool have = a.state_in && slot_in >= 0 && slot_in < a.in_count;
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-    S[b] = have ? *reinterpret_cast<const f4*>(a.state_in + slot_in * state_size + state_at +
-                                               32 * (b >> 1) + 4 * (b & 1))
-                : f4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t seg = 0; (seg + 1) * a.seg_chunks < chunks; ++seg) {
-    float* const at = a.seg_s + (seg_row + seg) * state_size + state_at;
-    const _Float16* const mt = reinterpret_cast<const _Float16*>(a.seg_m) +
-                               ((seg_row + seg) * a.hv + h) * (2 * K * K) +
-                               (8 * (i >> 2) + (i & 3)) * K + 8 * g;
-    float m = 0.0f;
+  for (int z = 0; z < NC; ++z)
 #pragma unroll
-    for (int b = 0; b < NB; ++b) m = max4(m, S[b]);
-    const Scale unit = scale_of(column_max(m));
-    h8 hi[KB], lo[KB];
+    for (int b = 0; b < NB; ++b)
+      S[z][b] = have ? *reinterpret_cast<const f4*>(a.state_in + slot_in * state_size + state_at[z] +
+                                                    32 * (b >> 1) + 4 * (b & 1))
+                     : f4{0.0f, 0.0f, 0.0f, 0.0f};
+  // One segment; m1: whether its M is not zero, m2: whether the next one's is.
+  auto step = [&](int64_t seg, int buf, bool m1, bool m2) {
+    const rsrc_t to = make_rsrc_bounded(a.seg_s + (seg_row + seg) * state_size,
+                                        static_cast<uint32_t>(state_size * 4));
+    // This wave's copies have arrived (behind them only the NC NB stores of the step before were
+    // issued); behind the barrier all waves' have, and the other buffer is free.
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NC * NB) : "memory");
+    __syncthreads();
+    const int64_t next = seg + 1 < final ? seg + 1 : seg;
+    load_n(next, buf ^ 1);
+    if (m2) load(next, buf ^ 1);
+    if (!m1) {
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-      split8(S[2 * kb] * (unit.up * 0x1p5f), S[2 * kb + 1] * (unit.up * 0x1p5f), &hi[kb], &lo[kb]);
+      for (int z = 0; z < NC; ++z)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          store(to, z, b, S[z][b]);
+          S[z][b] = N[buf][z][b];
+        }
+      return;
+    }
+    const char* m = ms[buf] + lane * 16;
+    Scale unit[NC];
+    h8 hi[NC][KB], lo[NC][KB];
+#pragma unroll
+    for (int z = 0; z < NC; ++z) {
+      float big = 0.0f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) big = max4(big, S[z][b]);
+      unit[z] = scale_of(column_max(big));
+      const float up = unit[z].up * 0x1p5f;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+        split8(S[z][2 * kb] * up, S[z][2 * kb + 1] * up, &hi[z][kb], &lo[z][kb]);
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      float* const to = at + 32 * (b >> 1) + 4 * (b & 1);
-      const _Float16* const row = mt + (32 * (b >> 1) + 4 * (b & 1)) * K;
-      f4 x = f4{0.0f, 0.0f, 0.0f, 0.0f};
+      f4 x[NC];
+#pragma unroll
+      for (int z = 0; z < NC; ++z) x[z] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        const h8 mh = *reinterpret_cast<const h8*>(row + 32 * kb);
-        const h8 ml = *reinterpret_cast<const h8*>(row + K * K + 32 * kb);
-        x = mfma_h(mh, hi[kb], x);
-        x = mfma_h(mh, lo[kb], x);
-        x = mfma_h(ml, hi[kb], x);
-      }
-      x = x * (unit.down * 0x1p-5f) + *reinterpret_cast<const f4*>(to);
-      *reinterpret_cast<f4*>(to) = S[b];
-      S[b] = x;
-    }
-  }
-  const int64_t final = chunks > 0 ? (chunks - 1) / a.seg_chunks : 0;
+        const h8 mh = *reinterpret_cast<const h8*>(m + (b * KB + kb) * 1024);
+        const h8 ml = *reinterpret_cast<const h8*>(m + 2 * K * K + (b * KB + kb) * 1024);
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-    *reinterpret_cast<f4*>(a.seg_s + (seg_row + final) * state_size + state_at + 32 * (b >> 1) +
-                           4 * (b & 1)) = S[b];
+        for (int z = 0; z < NC; ++z) {
+          x[z] = mfma_h(mh, hi[z][kb], x[z]);
+          x[z] = mfma_h(mh, lo[z][kb], x[z]);
+          x[z] = mfma_h(ml, hi[z][kb], x[z]);
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < NC; ++z) {
+        store(to, z, b, S[z][b]);
+        S[z][b] = x[z] * (unit[z].down * 0x1p-5f) + N[buf][z][b];
+      }
+    }
+  };
+  bool m1 = false, m2 = false;
+  if (final > 0) {
+    m1 = nonzero(0);
+    load_n(0, 0);
+    if (m1) load(0, 0);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+  // Two segments a turn: the buffers' indexes are constants.
+  for (int64_t seg = 0; seg < final; seg += 2) {
+    m2 = seg + 1 < final && nonzero(seg + 1);
+    step(seg, 0, m1, m2);
+    if (seg + 1 >= final) break;
+    m1 = seg + 2 < final && nonzero(seg + 2);
+    step(seg + 1, 1, m2, m1);
+  }
+  const rsrc_t to = make_rsrc_bounded(a.seg_s + (seg_row + final) * state_size,
+                                      static_cast<uint32_t>(state_size * 4));
+#pragma unroll
+  for (int z = 0; z < NC; ++z)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) store(to, z, b, S[z][b]);
 }
 
 // ---- one token a row ----------------------------------------------------------------------------
@@ -1244,7 +1386,7 @@ int64_t rows_of(const axon_gated_delta_shape* s) { return s->tokens / kQ + s->se
 
 struct ScanPlan {
   int64_t seg_chunks = 0;  // chunks of a segment, 0: none
-  size_t off_m = 0, off_s = 0, bytes = 0;
+  size_t off_m = 0, off_s = 0, off_flag = 0, bytes = 0;
 };
 
 // Workspace and segments from the shape alone. Sequences are split where their heads leave most of
@@ -1257,12 +1399,13 @@ ScanPlan plan_scan(const axon_gated_delta_shape* s) {
   p.bytes = record_bytes(s->act_dtype == AXON_BF16 ? 1 : 2) * rows * hv;
   const int64_t units = s->sequences * s->value_heads, chunks = s->tokens / kQ / s->sequences;
   if (units > kSegmentUnits || chunks < kSegmentMin * 4) return p;
-  const int64_t segs = std::min<int64_t>(512 / units, chunks / kSegmentMin);
+  const int64_t segs = std::min<int64_t>(256 / units, chunks / kSegmentMin);
   p.seg_chunks = (chunks + segs - 1) / segs;
   const size_t count = (rows / size_t(p.seg_chunks) + size_t(s->sequences)) * hv;
   p.off_m = (p.bytes + 255) / 256 * 256;
   p.off_s = p.off_m + count * 4 * size_t(s->key_dim * s->key_dim);
-  p.bytes = p.off_s + count * 4 * size_t(s->value_dim * s->key_dim);
+  p.off_flag = p.off_s + count * 4 * size_t(s->value_dim * s->key_dim);
+  p.bytes = p.off_flag + (count * 4 + 255) / 256 * 256;
   return p;
 }
 
@@ -1311,7 +1454,7 @@ void launch_scan(DeltaArgs a, bool any, hipStream_t st) {
       go(walk_kernel<Act, K, 4, 2, true>, 4, 2, a.value_dim + K);
     else
       go(walk_kernel<Act, K, 8, 1, true>, 8, 1, a.value_dim + K);
-    hipLaunchKernelGGL(join_kernel<K>, dim3(unsigned(a.sequences * a.hv), unsigned((a.value_dim + 63) / 64)),
+    hipLaunchKernelGGL(join_kernel<K>, dim3(unsigned(a.sequences * a.hv), unsigned((a.value_dim + 127) / 128)),
                        dim3(kThreads), 0, st, a);
   }
   const int64_t units = int64_t(a.sequences) * a.hv * (split ? a.segs : 1);
@@ -1437,6 +1580,7 @@ axon_status axon_gated_delta_scan(const axon_gated_delta_shape* shape,
     a.segs = int((most + plan.seg_chunks - 1) / plan.seg_chunks);
     a.seg_m = a.records + plan.off_m;
     a.seg_s = reinterpret_cast<float*>(a.records + plan.off_s);
+    a.seg_flag = reinterpret_cast<int32_t*>(a.records + plan.off_flag);
   }
   const bool bf = s.act_dtype == AXON_BF16;
   hipStream_t stm = static_cast<hipStream_t>(stream);

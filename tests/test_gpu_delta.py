@@ -224,14 +224,16 @@ def test_parts_of_one_projection(act):
 
 @pytest.mark.parametrize("act,K,V", [("f32", 128, 128), ("bf16", 128, 128), ("bf16", 64, 48),
                                      ("f32", 64, 240), ("bf16", 128, 256)])
-def test_long_sequences_in_segments(act, K, V):
+@pytest.mark.parametrize("slow", [3.0, 0.0, 1.5])
+def test_long_sequences_in_segments(act, K, V, slow):
     """Few heads and long sequences are walked in segments at once: a uniform batch in place, and
-    packed sequences of which some fill many segments and some none."""
-    say(f"[delta] segments {act} K={K} V={V}")
+    packed sequences of which some fill many segments and some none. Decays are such that states
+    live through segments (slow), that they end within a few chunks, and between."""
+    say(f"[delta] segments {act} K={K} V={V} slow={slow}")
     axon = _axon()
     hk, hv, L = 1, 2, 2200
     d = make((2, L), hk, hv, K, V, act, seed=31)
-    d["A_log"] -= 3.0  # states that live through segments
+    d["A_log"] -= slow
     s = state(2, hv, V, K, 6)
     start = s.clone()
     y, _ = axon.gated_delta_scan(**d, state_in=s, state_out=s)
