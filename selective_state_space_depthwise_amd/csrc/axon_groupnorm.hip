@@ -34,30 +34,48 @@ struct NormArgs {
   int centered, silu_out, gate, shared;
 };
 
-template <int VEC>
-__device__ __forceinline__ void load_vec(const float* p, float* v) {
-  if constexpr (VEC == 4) {
-    const float4 t = *reinterpret_cast<const float4*>(p);
-    v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-  } else if constexpr (VEC == 8) {
-    load_vec<4>(p, v);
-    load_vec<4>(p + 4, v + 4);
-  } else {
-    v[0] = p[0];
+// VEC consecutive values as loaded, and as fp32. Loads are issued for everything a lane holds before
+// the first value is used (their addresses are clamped instead of branched around).
+template <typename Act, int VEC>
+struct Raw;
+template <typename Act>
+struct Raw<Act, 1> {
+  Act v;
+  __device__ __forceinline__ void load(const Act* p) { v = *p; }
+  __device__ __forceinline__ void get(float* out) const {
+    if constexpr (sizeof(Act) == 4) out[0] = v;
+    else out[0] = bf16_to_f32(v);
   }
-}
-template <int VEC>
-__device__ __forceinline__ void load_vec(const bf16_bits* p, float* v) {
-  if constexpr (VEC == 8) {
-    const uint4 t = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+};
+template <>
+struct Raw<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float* out) const { out[0] = v.x, out[1] = v.y, out[2] = v.z, out[3] = v.w; }
+};
+template <>
+struct Raw<bf16_bits, 8> {
+  uint4 v;
+  __device__ __forceinline__ void load(const bf16_bits* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* out) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      out[2 * i] = __uint_as_float(w[i] << 16);
+      out[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
+  }
+};
+template <int VEC>
+__device__ __forceinline__ void load_params(const float* p, float* v) {
+  if constexpr (VEC == 1) {
+    v[0] = p[0];
   } else {
-    v[0] = bf16_to_f32(p[0]);
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4) {
+      const float4 t = *reinterpret_cast<const float4*>(p + j);
+      v[j] = t.x, v[j + 1] = t.y, v[j + 2] = t.z, v[j + 3] = t.w;
+    }
   }
 }
 template <int VEC>
@@ -98,12 +116,12 @@ __device__ __forceinline__ void finish(const NormArgs& a, int64_t row, int grp, 
   const int wi = (a.shared ? 0 : grp * a.width) + c;
   float t[VEC];
   if (a.weight) {
-    load_vec<VEC>(a.weight + wi, t);
+    load_params<VEC>(a.weight + wi, t);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) n[e] *= t[e];
   }
   if (a.bias) {
-    load_vec<VEC>(a.bias + wi, t);
+    load_params<VEC>(a.bias + wi, t);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) n[e] += t[e];
   }
@@ -119,43 +137,55 @@ __device__ __forceinline__ void finish(const NormArgs& a, int64_t row, int grp, 
   store_vec<VEC>(y, n);
 }
 
-// u (gated before) and SiLU(z) of VEC channels from c on.
+// x and z of VEC channels from c on, and then u (gated before) and SiLU(z).
 template <typename Act, int VEC>
-__device__ __forceinline__ void fetch(const NormArgs& a, int64_t row, int grp, int c, float* u,
-                                      float* gz) {
-  const int64_t off = int64_t(grp) * a.width + c;
-  load_vec<VEC>(static_cast<const Act*>(a.x) + row * a.x_stride + off, u);
-  if (a.gate != AXON_GATE_NONE) {
-    load_vec<VEC>(static_cast<const Act*>(a.z) + row * a.z_stride + off, gz);
+struct Fetched {
+  Raw<Act, VEC> x, z;
+  __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int grp, int c) {
+    const int64_t off = int64_t(grp) * a.width + c;
+    x.load(static_cast<const Act*>(a.x) + row * a.x_stride + off);
+    if (a.gate != AXON_GATE_NONE) z.load(static_cast<const Act*>(a.z) + row * a.z_stride + off);
+  }
+  __device__ __forceinline__ void get(const NormArgs& a, float* u, float* gz) const {
+    x.get(u);
+    if (a.gate != AXON_GATE_NONE) {
+      z.get(gz);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) gz[e] = silu(gz[e]);
-    if (a.gate == AXON_GATE_BEFORE) {
+      for (int e = 0; e < VEC; ++e) gz[e] = silu(gz[e]);
+      if (a.gate == AXON_GATE_BEFORE) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) u[e] *= gz[e];
+        for (int e = 0; e < VEC; ++e) u[e] *= gz[e];
+      }
     }
   }
-}
+};
 
 __device__ __forceinline__ float reduce_lanes(float v, int lanes) {
   for (int d = lanes >> 1; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
   return v;
 }
 
+// (Four groups a lane set, all loaded before the first is reduced, gained nothing: 5001 x 8 groups of
+// 236 fp32 take 20 us either way.)
 template <typename Act, int VEC, int R>
 __global__ __launch_bounds__(256) void norm_lanes_kernel(NormArgs a) {
   const int l = threadIdx.x & (a.lanes - 1);
   const int64_t gi = wg_index() * (256 / a.lanes) + threadIdx.x / a.lanes;
-  // Lanes without a group take part in the exchanges with zeros.
+  // Lanes without a group take part in the exchanges with the last one's values.
   const bool live = gi < a.total;
-  const int64_t row = live ? gi / a.groups : 0;
-  const int grp = live ? static_cast<int>(gi - row * a.groups) : 0;
-  float u[R * VEC], gz[R * VEC];
+  const int64_t row = (live ? gi : a.total - 1) / a.groups;
+  const int grp = static_cast<int>((live ? gi : a.total - 1) - row * a.groups);
+  Fetched<Act, VEC> f[R];
 #pragma unroll
   for (int j = 0; j < R; ++j) {
     const int c = (j * a.lanes + l) * VEC;
-    if (live && c < a.width) {
-      fetch<Act, VEC>(a, row, grp, c, u + j * VEC, gz + j * VEC);
-    } else {
+    f[j].load(a, row, grp, c < a.width ? c : 0);
+  }
+  float u[R * VEC], gz[R * VEC];
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    f[j].get(a, u + j * VEC, gz + j * VEC);
+    if ((j * a.lanes + l) * VEC >= a.width) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) u[j * VEC + e] = 0.0f;
     }
@@ -210,13 +240,17 @@ __global__ __launch_bounds__(THREADS) void norm_wide_kernel(NormArgs a) {
   const int step = THREADS * VEC, first = threadIdx.x * VEC;
   float u[R * VEC], gz[R * VEC];
   float s = 0.0f, mean = 0.0f;
+  Fetched<Act, VEC> f[R];
   if constexpr (HELD) {
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const int c = j * step + first;
-      if (c < a.width) {
-        fetch<Act, VEC>(a, row, grp, c, u + j * VEC, gz + j * VEC);
-      } else {
+      f[j].load(a, row, grp, c < a.width ? c : 0);
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      f[j].get(a, u + j * VEC, gz + j * VEC);
+      if (j * step + first >= a.width) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) u[j * VEC + e] = 0.0f;
       }
@@ -248,7 +282,8 @@ __global__ __launch_bounds__(THREADS) void norm_wide_kernel(NormArgs a) {
   } else {
     if (a.centered) {
       for (int64_t c = first; c < a.width; c += step) {
-        fetch<Act, VEC>(a, row, grp, static_cast<int>(c), u, gz);
+        f[0].load(a, row, grp, static_cast<int>(c));
+        f[0].get(a, u, gz);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) s += u[e];
       }
@@ -256,7 +291,8 @@ __global__ __launch_bounds__(THREADS) void norm_wide_kernel(NormArgs a) {
     }
     float q = 0.0f;
     for (int64_t c = first; c < a.width; c += step) {
-      fetch<Act, VEC>(a, row, grp, static_cast<int>(c), u, gz);
+      f[0].load(a, row, grp, static_cast<int>(c));
+        f[0].get(a, u, gz);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float d = u[e] - mean;
@@ -267,7 +303,8 @@ __global__ __launch_bounds__(THREADS) void norm_wide_kernel(NormArgs a) {
     // In place a thread overwrites only what it alone reads in this pass; the passes before it
     // ended at the barriers of the sums.
     for (int64_t c = first; c < a.width; c += step) {
-      fetch<Act, VEC>(a, row, grp, static_cast<int>(c), u, gz);
+      f[0].load(a, row, grp, static_cast<int>(c));
+        f[0].get(a, u, gz);
       float n[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) n[e] = (u[e] - mean) * rs;
