@@ -13,19 +13,39 @@ from .api import _act_dtype, _check, _keep_for, _stream_handle
 
 DELTA_CHUNK = 64
 _NOTHING = contextlib.nullcontext()
+# A decode step's kernels take a few microseconds, so what is looked up on every call is kept short:
+# the current stream's handle without a Stream object around it, and one test of a good tensor before
+# the checks that name what is wrong with a bad one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _on(device):
     """Kernels are launched with the tensors' device as the current one."""
-    if device.index is None or device.index == torch.cuda.current_device():
+    if device.index == torch.cuda.current_device():
         return _NOTHING
     return torch.cuda.device(device)
+
+
+def _handle(device, stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream_handle(device, stream)
+
+
+def _dense(t, name, shape, dtype, device):
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype
+            and t.device == device and t.is_contiguous()):
+        _check(t, name, shape, dtype, device)
+
+
+def _lib():
+    return _abi._lib or _abi.load()
 
 
 def _gpu(t, name, what):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what} runs on the GPU only; {name} is on {t.device}")
     return t.device
 
@@ -58,15 +78,17 @@ def _row_stride(t, name, tail):
 
 def _rows(t, name, lead, tail, dtype, device):
     """Check t of shape lead + tail, whose rows may lie apart; returns the stride (0 = dense)."""
+    shape = lead + tail
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype
+            and t.device == device):
+        return 0 if t.is_contiguous() else _row_stride(t, name, tail)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if tuple(t.shape) != (*lead, *tail):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(*lead, *tail)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    return _row_stride(t, name, tail)
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
 
 
 class SequenceTables:
@@ -74,12 +96,24 @@ class SequenceTables:
     (sequences + 1), ``block_seq`` and ``block_first`` (total_tokens // block + sequences), int32
     parts of the one tensor ``buffer``."""
 
+    __slots__ = ("buffer", "sequences", "total_tokens", "block", "_parts")
+
     def __init__(self, buffer, sequences, total_tokens, block):
         self.buffer = buffer
         self.sequences, self.total_tokens, self.block = sequences, total_tokens, block
-        rows = total_tokens // block + sequences
-        self.starts, self.block_starts, self.block_seq, self.block_first = buffer.split_with_sizes(
-            [sequences + 1, sequences + 1, rows, rows])
+        self._parts = None
+
+    def _part(self, index):
+        if self._parts is None:
+            rows = self.total_tokens // self.block + self.sequences
+            self._parts = self.buffer.split_with_sizes(
+                [self.sequences + 1, self.sequences + 1, rows, rows])
+        return self._parts[index]
+
+    starts = property(lambda self: self._part(0))
+    block_starts = property(lambda self: self._part(1))
+    block_seq = property(lambda self: self._part(2))
+    block_first = property(lambda self: self._part(3))
 
 
 def sequence_tables(lengths, total_tokens, *, block=DELTA_CHUNK, stream=None) -> SequenceTables:
@@ -90,17 +124,17 @@ def sequence_tables(lengths, total_tokens, *, block=DELTA_CHUNK, stream=None) ->
     if lengths.dim() != 1:
         raise ValueError("lengths must be (sequences,)")
     n = lengths.shape[0]
-    _check(lengths, "lengths", (n,), torch.int32, device)
+    _dense(lengths, "lengths", (n,), torch.int32, device)
     total_tokens, block = int(total_tokens), int(block)
-    count = _abi.sequence_tables_count(n, total_tokens, block)
+    count = _lib().axon_sequence_tables_count(n, total_tokens, block)
     if count == 0:
         raise ValueError(f"unsupported packed sequences: {n} sequences, {total_tokens} tokens, "
                          f"block {block}")
     with _on(device):
         buffer = torch.empty(count, dtype=torch.int32, device=device)
         _keep_for(device, stream, buffer)
-        st = _abi.raw_sequence_tables(n, total_tokens, block, lengths.data_ptr(),
-                                      buffer.data_ptr(), _stream_handle(device, stream))
+        st = _lib().axon_sequence_tables(n, total_tokens, block, lengths.data_ptr(),
+                                         buffer.data_ptr(), _handle(device, stream))
     if st != _abi.AXON_OK:
         raise AxonError(st, "axon_sequence_tables")
     return SequenceTables(buffer, n, total_tokens, block)
@@ -115,9 +149,9 @@ def _delta_inputs(q, k, v, dt_raw, beta_raw, A_log, dt_bias, lead, device):
     ks = _rows(k, "k", lead, (hk, K), q.dtype, device)
     vs = _rows(v, "v", lead, (hv, V), q.dtype, device)
     for t, n in ((dt_raw, "dt_raw"), (beta_raw, "beta_raw")):
-        _check(t, n, (*lead, hv), q.dtype, device)
+        _dense(t, n, lead + (hv,), q.dtype, device)
     for t, n in ((A_log, "A_log"), (dt_bias, "dt_bias")):
-        _check(t, n, (hv,), torch.float32, device)
+        _dense(t, n, (hv,), torch.float32, device)
     return _abi.GatedDeltaShape(1, math.prod(lead), hk, hv, K, V, qs, ks, vs, 0, 0,
                                 _abi.AXON_BF16 if bf16 else _abi.AXON_F32)
 
@@ -130,7 +164,7 @@ def _delta_params(A_log, dt_bias, dt_min, dt_max, scale, eps, K):
 def _slots(t, name, n, device):
     if t is None:
         return None
-    _check(t, name, (n,), torch.int32, device)
+    _dense(t, name, (n,), torch.int32, device)
     return t.data_ptr()
 
 
@@ -140,7 +174,7 @@ def _pool(t, name, shape, device):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 4:
         raise ValueError(f"{name} must be (states, {', '.join(map(str, shape))})")
-    _check(t, name, (t.shape[0], *shape), torch.float32, device)
+    _dense(t, name, (t.shape[0], *shape), torch.float32, device)
     return t.shape[0]
 
 
@@ -208,7 +242,7 @@ def gated_delta_scan(q, k, v, dt_raw, beta_raw, A_log, dt_bias, *, dt_min=1e-4, 
             y = torch.empty(v.shape, dtype=v.dtype, device=device)
             mine.append(y)
         else:
-            _check(y, "y", tuple(v.shape), v.dtype, device)
+            _dense(y, "y", v.shape, v.dtype, device)
         if state_out is None:
             if out_slots is not None:
                 raise ValueError("out_slots address a pool: give state_out")
@@ -220,14 +254,14 @@ def gated_delta_scan(q, k, v, dt_raw, beta_raw, A_log, dt_bias, *, dt_min=1e-4, 
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
             mine.append(workspace)
         _keep_for(device, stream, *mine)
-        st = _abi.raw_gated_delta_scan(
+        st = _lib().axon_gated_delta_scan(
             shape, _delta_params(A_log, dt_bias, dt_min, dt_max, scale, eps, K), q.data_ptr(),
             k.data_ptr(), v.data_ptr(), dt_raw.data_ptr(), beta_raw.data_ptr(),
             tables.buffer.data_ptr() if tables is not None else None, _ptr(state_in),
             _slots(in_slots, "in_slots", n, device), y.data_ptr(), state_out.data_ptr(),
             _slots(out_slots, "out_slots", n, device), _ptr(workspace),
             workspace.numel() * workspace.element_size() if workspace is not None else 0,
-            _stream_handle(device, stream))
+            _handle(device, stream))
     if st != _abi.AXON_OK:
         raise AxonError(st, "axon_gated_delta_scan")
     return y, state_out
@@ -252,11 +286,11 @@ def gated_delta_step(q, k, v, dt_raw, beta_raw, A_log, dt_bias, state, *, slots=
             y = torch.empty(v.shape, dtype=v.dtype, device=device)
             _keep_for(device, stream, y)
         else:
-            _check(y, "y", tuple(v.shape), v.dtype, device)
-        st = _abi.raw_gated_delta_step(
+            _dense(y, "y", v.shape, v.dtype, device)
+        st = _lib().axon_gated_delta_step(
             shape, _delta_params(A_log, dt_bias, dt_min, dt_max, scale, eps, K), q.data_ptr(),
             k.data_ptr(), v.data_ptr(), dt_raw.data_ptr(), beta_raw.data_ptr(), state.data_ptr(),
-            _slots(slots, "slots", n, device), y.data_ptr(), _stream_handle(device, stream))
+            _slots(slots, "slots", n, device), y.data_ptr(), _handle(device, stream))
     if st != _abi.AXON_OK:
         raise AxonError(st, "axon_gated_delta_step")
     return y
@@ -296,19 +330,19 @@ def group_norm(x, groups, weight=None, bias=None, z=None, *, eps=1e-5, centered=
             shared = True
     for t, n in ((weight, "weight"), (bias, "bias")):
         if t is not None:
-            _check(t, n, (C // groups if shared else C,), torch.float32, device)
+            _dense(t, n, (C // groups if shared else C,), torch.float32, device)
     with _on(device):
         if y is None:
             y = torch.empty(x.shape, dtype=x.dtype, device=device)
             _keep_for(device, stream, y)
         else:
-            _check(y, "y", tuple(x.shape), x.dtype, device)
+            _dense(y, "y", x.shape, x.dtype, device)
         desc = _abi.GroupNormDesc(math.prod(lead), groups, C // groups, xs, zs, float(eps),
                                   _abi.AXON_BF16 if bf16 else _abi.AXON_F32, 1 if centered else 0,
                                   _abi.NORM_ACTIVATIONS[activation], _abi.NORM_GATES[gate],
                                   1 if shared else 0)
-        st = _abi.raw_group_norm(desc, x.data_ptr(), _ptr(z), _ptr(weight), _ptr(bias),
-                                 y.data_ptr(), _stream_handle(device, stream))
+        st = _lib().axon_group_norm(desc, x.data_ptr(), _ptr(z), _ptr(weight), _ptr(bias),
+                                    y.data_ptr(), _handle(device, stream))
     if st != _abi.AXON_OK:
         raise AxonError(st, "axon_group_norm")
     return y
