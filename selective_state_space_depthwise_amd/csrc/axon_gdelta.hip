@@ -573,6 +573,8 @@ __device__ __forceinline__ int swizzle(int t) {
 // The blocks of a lower triangular matrix as operands: row block, and pair of contraction blocks.
 constexpr int kLowerRow[6] = {0, 1, 2, 3, 2, 3}, kLowerCol[6] = {0, 0, 0, 0, 1, 1};
 
+constexpr int kOrdered = 1024;  // packed sequences that are put in order
+
 // LOCAL: the first walk over segments: no outputs; columns V .. V + K - 1 are the identity's.
 template <typename Act, int K, int W, int NC, bool LOCAL>
 __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
@@ -602,10 +604,29 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
   if (a.seg_chunks) slot /= a.segs;
   const int64_t nk = int64_t(slot) * 8 + xcd;
   if (nk >= int64_t(a.sequences) * a.hk) return;
+  int n = static_cast<int>(nk / a.hk);
+  if (a.starts && a.sequences > 1 && a.sequences <= kOrdered) {
+    // Packed sequences start in the order of their lengths, the longest first, so that no long one
+    // is left to run alone at the end. The n-th longest is found here: every thread compares some
+    // sequences with all others. (In the order of the buffer 24 sequences of 32768 tokens took
+    // 555 us instead of 506 us.)
+    int* const lens = reinterpret_cast<int*>(rs2[0]);
+    int* const found = lens + kOrdered;
+    for (int j = threadIdx.x; j < a.sequences; j += kThreadsW)
+      lens[j] = a.block_starts[j + 1] - a.block_starts[j];
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.sequences; j += kThreadsW) {
+      int before = 0;
+      for (int o = 0; o < a.sequences; ++o) before += lens[o] > lens[j] || (lens[o] == lens[j] && o < j);
+      if (before == n) *found = j;
+    }
+    __syncthreads();
+    n = __builtin_amdgcn_readfirstlane(*found);
+    __syncthreads();  // read before the records take the place
+  }
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, i = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int n = static_cast<int>(nk / a.hk);
-  const int hk = static_cast<int>(nk - int64_t(n) * a.hk), h = hk * a.ratio + vh;
+  const int hk = static_cast<int>(nk % a.hk), h = hk * a.ratio + vh;
   const int col0 = (group * W + w) * 16 * NC;
   const int columns = LOCAL ? a.value_dim + K : a.value_dim;
   int64_t begin, len, row0;
@@ -854,6 +875,8 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     rowop_c = fresh(rowop);
     colop_c = fresh(colop);
     load_record(next, (c + 1) & 1);
+    // k and q have the whole chunk's time to arrive, where their registers fit.
+    if (NC == 1 && P == 1) load(next);
     f4 X[NC][4], O[NC][4];
 #pragma unroll
     for (int z = 0; z < NC; ++z) {
@@ -964,7 +987,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
         E[z][tt] = mfma_h(t1, xh[z][s], E[z][tt]);
       }
     }
-    load(next);
+    if (NC > 1 || P > 1) load(next);
     __builtin_amdgcn_sched_barrier(0);
     // y, and the writes U.
     h8 uh[NC][2], ul[NC][2];
@@ -1245,7 +1268,8 @@ struct StepArgs {
   int rows, hv, ratio, value_dim, waves_per_head;
 };
 
-template <typename Act, int K, int R>
+// STREAM: states pass by the caches (no call finds them there again).
+template <typename Act, int K, int R, bool STREAM>
 __global__ __launch_bounds__(kThreads) void step_kernel(StepArgs a) {
   constexpr int LR = K / 16;      // lanes of a state row
   constexpr int RW = 64 / LR;     // state rows of a wave and pass
@@ -1259,13 +1283,14 @@ __global__ __launch_bounds__(kThreads) void step_kernel(StepArgs a) {
   if (slot < 0 || slot >= a.slots) return;
   const int v0 = part * RW * R + rr;
   float* sp = a.state + ((slot * a.hv + h) * a.value_dim) * int64_t(K) + 4 * l;
-  float4 s[R][4];
+  f4 s[R][4];
 #pragma unroll
   for (int p = 0; p < R; ++p)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int v = v0 + p * RW;
-      s[p][j] = v < a.value_dim ? load4(sp + int64_t(v) * K + 4 * LR * j) : float4{};
+      const f4* at = reinterpret_cast<const f4*>(sp + int64_t(v) * K + 4 * LR * j);
+      s[p][j] = v >= a.value_dim ? f4{} : STREAM ? __builtin_nontemporal_load(at) : *at;
     }
   const int hk = h / a.ratio;
   float4 kv[4], qv[4];
@@ -1299,8 +1324,8 @@ __global__ __launch_bounds__(kThreads) void step_kernel(StepArgs a) {
     float pk = 0.0f, pq = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      pk += s[p][j].x * kv[j].x + s[p][j].y * kv[j].y + s[p][j].z * kv[j].z + s[p][j].w * kv[j].w;
-      pq += s[p][j].x * qv[j].x + s[p][j].y * qv[j].y + s[p][j].z * qv[j].z + s[p][j].w * qv[j].w;
+      pk += s[p][j][0] * kv[j].x + s[p][j][1] * kv[j].y + s[p][j][2] * kv[j].z + s[p][j][3] * kv[j].w;
+      pq += s[p][j][0] * qv[j].x + s[p][j][1] * qv[j].y + s[p][j][2] * qv[j].z + s[p][j][3] * qv[j].w;
     }
 #pragma unroll
     for (int d = 1; d < LR; d <<= 1) {
@@ -1313,12 +1338,15 @@ __global__ __launch_bounds__(kThreads) void step_kernel(StepArgs a) {
       const float dk = d * rk;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float4 t = s[p][j];
-        t.x = fmaf(dk, kv[j].x, decay * t.x);
-        t.y = fmaf(dk, kv[j].y, decay * t.y);
-        t.z = fmaf(dk, kv[j].z, decay * t.z);
-        t.w = fmaf(dk, kv[j].w, decay * t.w);
-        *reinterpret_cast<float4*>(sp + int64_t(v) * K + 4 * LR * j) = t;
+        const f4 k4 = {kv[j].x, kv[j].y, kv[j].z, kv[j].w};
+        f4 t = s[p][j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = fmaf(dk, k4[e], decay * t[e]);
+        f4* at = reinterpret_cast<f4*>(sp + int64_t(v) * K + 4 * LR * j);
+        if (STREAM)
+          __builtin_nontemporal_store(t, at);
+        else
+          *at = t;
       }
       if (l == 0)
         store_act(static_cast<Act*>(a.y), rh * a.value_dim + v,
@@ -1391,7 +1419,7 @@ struct ScanPlan {
 
 // Workspace and segments from the shape alone. Sequences are split where their heads leave most of
 // the 256 CUs idle (a workgroup a head) and they are long enough for it to pay: at 32 heads 16384
-// tokens take @@T1@@ ms in 16 segments and @@T0@@ ms in one.
+// tokens take 0.43 ms in 8 segments and 1.09 ms in one.
 ScanPlan plan_scan(const axon_gated_delta_shape* s) {
   ScanPlan p;
   if (!s->tokens) return p;
@@ -1450,6 +1478,7 @@ void launch_scan(DeltaArgs a, bool any, hipStream_t st) {
     hipLaunchKernelGGL(kernel, dim3(unsigned(wgs)), dim3(64 * waves), 0, st, b);
   };
   if (split) {
+    // (bf16 with eight waves of one tile: 217 us against 187 us at 32 heads and 16384 tokens.)
     if constexpr (kPieces<Act> == 1)
       go(walk_kernel<Act, K, 4, 2, true>, 4, 2, a.value_dim + K);
     else
@@ -1481,10 +1510,16 @@ void launch_step(StepArgs a, hipStream_t st) {
   const bool wide = heads * w4 >= 2048;
   a.waves_per_head = wide ? w4 : (a.value_dim + RW - 1) / RW;
   const unsigned wgs = static_cast<unsigned>((heads * a.waves_per_head + 3) / 4);
-  if (wide)
-    hipLaunchKernelGGL((step_kernel<Act, K, 4>), dim3(wgs), dim3(kThreads), 0, st, a);
+  // A layer's states stream where those of a model's layers together pass the 256 MB cache (512 rows
+  // x 32 heads: 327 us against 355 us; 56 rows, states of three calls in turn: 45 us against 48 us,
+  // of one call again and again 43 us against 38 us).
+  const bool stream = heads * a.value_dim * K * 4 > (int64_t(16) << 20);
+  if (!wide)
+    hipLaunchKernelGGL((step_kernel<Act, K, 1, false>), dim3(wgs), dim3(kThreads), 0, st, a);
+  else if (stream)
+    hipLaunchKernelGGL((step_kernel<Act, K, 4, true>), dim3(wgs), dim3(kThreads), 0, st, a);
   else
-    hipLaunchKernelGGL((step_kernel<Act, K, 1>), dim3(wgs), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((step_kernel<Act, K, 4, false>), dim3(wgs), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace

@@ -172,7 +172,7 @@ axon_status axon_sequence_tables(int64_t sequences, int64_t total_tokens, int64_
   a.rows = static_cast<uint32_t>(rows);
   hipStream_t st = static_cast<hipStream_t>(stream);
   // Rows a workgroup writes: enough workgroups that none writes more than a few rows a thread.
-  a.rows_per_wg = 1024;
+  a.rows_per_wg = sequences <= 256 ? 256 : 1024;
   int64_t wgs = (rows + a.rows_per_wg - 1) / a.rows_per_wg;
   if (wgs > 1024) {
     a.rows_per_wg = static_cast<uint32_t>((rows + 1023) / 1024);
