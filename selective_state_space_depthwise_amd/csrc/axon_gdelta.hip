@@ -68,7 +68,7 @@ template <typename Act>
 constexpr int kPieces = sizeof(Act) == 2 ? 1 : 2;
 
 // What prep leaves for each (chunk, value head): T in two pieces and A in one or two, each as ten
-// 16 x 16 blocks on and below the diagonal (block I (I + 1) / 2 + J), a block as 64 lanes x 4 fp16
+// 16 x 16 blocks on and below the diagonal (at block_at), a block as 64 lanes x 4 fp16
 // in left-operand order (lane (g, i): row i, columns 4 g .. 4 g + 3); then the row
 // factors of the 64 tokens, fp32, and e^{g_last} with its base-2 logarithm. What the walk keeps in
 // LDS comes first.
@@ -79,6 +79,11 @@ enum Row { kRowX, kRowS, kRowY, kRowKQ, kRows = kRowKQ + 2 };
 //   kRowS  beta e^{g_last-g} / |k| / 2^s   of E in the state's sum
 //   kRowY  e^g / |q| / 2^s                 of S0 q in y
 //   kRowKQ 2^s of k and of q, in pairs
+// Pairs of blocks that make one operand (32 contraction indices) lie side by side, so that one
+// instruction reads both; the two diagonal blocks without a partner come last.
+__host__ __device__ constexpr int block_at(int I, int J) {
+  return I == 0 ? 8 : I == 1 ? J : I == 3 ? 4 + J : J < 2 ? 2 + J : 9;
+}
 constexpr int rows_at(int pieces) { return (2 + pieces) * kBlocks * kBlockBytes; }
 constexpr int lds_bytes(int pieces) { return rows_at(pieces) + 4 * kQ * 4; }
 constexpr int record_bytes(int pieces) { return rows_at(pieces) + kRows * kQ * 4 + 64; }
@@ -470,7 +475,7 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
         }
         *reinterpret_cast<f4*>(&Ms[hh][blk][i * kBlockRow + 4 * g]) = m;
         const h4 hi = __builtin_convertvector(x, h4);
-        char* dst = rec + (2 * kBlocks + blk) * kBlockBytes + lane * 8;
+        char* dst = rec + (2 * kBlocks + block_at(w, st)) * kBlockBytes + lane * 8;
         *reinterpret_cast<h4*>(dst) = hi;
         if (P == 2)
           *reinterpret_cast<h4*>(dst + kBlocks * kBlockBytes) =
@@ -527,7 +532,7 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
         constexpr int I = decltype(index)::value;
         f4 T[I + 1];
         T[I] = *reinterpret_cast<const f4*>(m[I * (I + 1) / 2 + I] + i * kBlockRow + 4 * g);
-        put(I * (I + 1) / 2 + I, T[I]);
+        put(block_at(I, I), T[I]);
 #pragma unroll
         for (int J = I - 1; J >= 0; --J) {
           f4 p = f4{0.0f, 0.0f, 0.0f, 0.0f}, x = p;
@@ -539,7 +544,7 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
 #pragma unroll
           for (int r = 0; r < 4; ++r) x = mfma4(m[J * (J + 1) / 2 + J][(4 * g + r) * kBlockRow + i], p[r], x);
           T[J] = -x;
-          put(I * (I + 1) / 2 + J, T[J]);
+          put(block_at(I, J), T[J]);
         }
       };
       if (w < 2) {
@@ -810,9 +815,9 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
         static_cast<char*>(a.y) + ((first + 16 * tt) * y_stride + int64_t(h) * a.value_dim) * int64_t(es),
         left > 0 ? ((left - 1) * static_cast<uint32_t>(y_stride) + a.value_dim) * es : 0);
     if constexpr (P == 1) {
-      const w2 v = {f32_to_bf16(o[0]) | static_cast<uint32_t>(f32_to_bf16(o[1])) << 16,
-                    f32_to_bf16(o[2]) | static_cast<uint32_t>(f32_to_bf16(o[3])) << 16};
-      __builtin_amdgcn_raw_buffer_store_b64(v, yr, off, 0, 0);
+      typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(w2, __builtin_convertvector(o, b4)), yr,
+                                            off, 0, 0);
     } else {
       __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(w4, o), yr, off, 0, 0);
     }
@@ -836,7 +841,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
   const char* rs = rs2[0];
   // Row block tt, contraction blocks 2 ss and 2 ss + 1 of a lower triangular matrix.
   auto lower = [&](int mat, int tt, int ss) {
-    const char* p = rs + (mat * kBlocks + tt * (tt + 1) / 2 + 2 * ss) * kBlockBytes + lane * 8;
+    const char* p = rs + (mat * kBlocks + block_at(tt, 2 * ss)) * kBlockBytes + lane * 8;
     const h4 x = *reinterpret_cast<const h4*>(p);
     h4 y = {};
     if (2 * ss + 1 <= tt) y = *reinterpret_cast<const h4*>(p + kBlockBytes);
@@ -877,6 +882,10 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     load_record(next, (c + 1) & 1);
     // k and q have the whole chunk's time to arrive, where their registers fit.
     if (NC == 1 && P == 1) load(next);
+    // A SIMD's waves serve a chunk together; the one that is behind goes first (its priority falls
+    // from phase to phase), so that they reach the barrier together: 346 -> 333 us for 32768 packed
+    // tokens.
+    __builtin_amdgcn_s_setprio(3);
     f4 X[NC][4], O[NC][4];
 #pragma unroll
     for (int z = 0; z < NC; ++z) {
@@ -952,6 +961,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_s_setprio(2);
     h8 xh[NC][2], xl[NC][2];
 #pragma unroll
     for (int z = 0; z < NC; ++z) {
@@ -973,6 +983,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     load_v(next);
     __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
     // E = T X.
     f4 E[NC][4];
 #pragma unroll
@@ -1041,6 +1052,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
         for (int tt = 0; tt < 4; ++tt) store_y(c, z, tt, O[z][tt] * out);
       }
     }
+    __builtin_amdgcn_s_setprio(0);
     // The state.
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -1491,6 +1503,10 @@ void launch_scan(DeltaArgs a, bool any, hipStream_t st) {
     go(walk_kernel<Act, K, 4, 1, false>, 4, 1, a.value_dim);
     return;
   }
+  // Two tiles a wave read each operand from LDS once for both, and two such workgroups share a CU:
+  // 16 x 2048 tokens x 32 heads 439 us against 458 us. A workgroup of 8 waves with one tile takes
+  // less time a chunk, which counts where there are fewer workgroups or one long sequence is left at
+  // the end (32768 packed tokens: walk 333 us against 387 us).
   if constexpr (kPieces<Act> == 1) {
     if (units >= 512 && !a.starts) {
       go(walk_kernel<Act, K, 4, 2, false>, 4, 2, a.value_dim);
