@@ -292,7 +292,7 @@ __global__ __launch_bounds__(THREADS) void norm_wide_kernel(NormArgs a) {
     float q = 0.0f;
     for (int64_t c = first; c < a.width; c += step) {
       f[0].load(a, row, grp, static_cast<int>(c));
-        f[0].get(a, u, gz);
+      f[0].get(a, u, gz);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float d = u[e] - mean;
@@ -304,7 +304,7 @@ __global__ __launch_bounds__(THREADS) void norm_wide_kernel(NormArgs a) {
     // ended at the barriers of the sums.
     for (int64_t c = first; c < a.width; c += step) {
       f[0].load(a, row, grp, static_cast<int>(c));
-        f[0].get(a, u, gz);
+      f[0].get(a, u, gz);
       float n[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) n[e] = (u[e] - mean) * rs;

@@ -253,6 +253,8 @@ def gated_delta_scan(q, k, v, dt_raw, beta_raw, A_log, dt_bias, *, dt_min=1e-4, 
         if workspace is None and need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
             mine.append(workspace)
+        elif workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
         _keep_for(device, stream, *mine)
         st = _lib().axon_gated_delta_scan(
             shape, _delta_params(A_log, dt_bias, dt_min, dt_max, scale, eps, K), q.data_ptr(),

@@ -443,3 +443,54 @@ def test_refused_tensors():
     with pytest.raises((ValueError, TypeError)):
         axon.gated_delta_step(**p, state=None)
     torch.cuda.synchronize()
+
+
+def test_two_calls_at_once():
+    """Two scans that share inputs and the pool, each with its own workspace and slots, on two
+    streams: both as if alone. One is split into segments, the other packed."""
+    axon = _axon()
+    hk, hv, K, V, L = 1, 2, 128, 128, 4096
+    d = make((1, L), hk, hv, K, V, "bf16", seed=31)
+    p = {x: (t if x in ("A_log", "dt_bias") else t.flatten(0, 1)) for x, t in d.items()}
+    lengths = torch.tensor([L // 2 + 5, 0, L // 4], dtype=torch.int32).cuda()
+    pool = state(6, hv, V, K, 3)
+    one = torch.tensor([2], dtype=torch.int32).cuda()
+    three = torch.tensor([0, 5, 3], dtype=torch.int32).cuda()
+    y = [torch.zeros(1, L, hv, V, dtype=torch.bfloat16).cuda(), torch.zeros(L, hv, V, dtype=torch.bfloat16).cuda()]
+
+    def a(stream=None):
+        axon.gated_delta_scan(**d, state_in=pool, in_slots=one, y=y[0], state_out=pool, out_slots=one,
+                              stream=stream)
+
+    def b(stream=None):
+        axon.gated_delta_scan(**p, lengths=lengths, state_in=pool, in_slots=three, y=y[1], state_out=pool,
+                              out_slots=three, stream=stream)
+
+    start = pool.clone()
+    a()
+    b()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (*y, pool)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for rep in range(3):
+        pool.copy_(start)
+        for t in y:
+            t.zero_()
+        torch.cuda.synchronize()
+        a(streams[0])
+        b(streams[1])
+        torch.cuda.synchronize()
+        for got, w, what in zip((*y, pool), want, ("y", "packed y", "pool")):
+            assert torch.equal(got, w), f"run {rep}: {what} differs"
+
+
+@pytest.mark.parametrize("where", ["host", "spread"])
+def test_refused_workspace(where):
+    """A workspace that the kernels could not use is refused before any launch."""
+    axon = _axon()
+    d = make((2, 10), 1, 2, 64, 32, "f32", seed=1)
+    need = axon.gated_delta_workspace_bytes(2, 20, 1, 2, 64, 32)
+    ws = (torch.empty(need, dtype=torch.uint8) if where == "host"
+          else torch.empty(2 * need, dtype=torch.uint8).cuda()[::2])
+    with pytest.raises(ValueError):
+        axon.gated_delta_scan(**d, workspace=ws)
