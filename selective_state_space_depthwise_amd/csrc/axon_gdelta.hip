@@ -311,12 +311,12 @@ __device__ __forceinline__ float max4(float m, f4 x) {
 // Grid (chunk rows, key heads), 4 waves; the value heads of the key head in pairs. Every 16 x 16
 // block is computed transposed (rows: 4 columns of the block, column: its row i), which is at once
 // the operand order of the record (a lane holds 4 consecutive entries of a row) and the layout in
-// which one product's result is the next one's right operand, so only M and the inverses of its
-// diagonal blocks pass through LDS. Wave w owns rows 16 w .. of the Gram products (bf16: exact bf16
-// products; fp32 and the inverse: v_mfma_f32_16x16x4f32). The diagonal blocks of a head are inverted
-// by one wave, block g by lane group g, a column a lane. From T (I + M) = I the blocks below follow
-// row by row: T_IJ = -(sum_{J < S <= I} T_IS M_SJ) D_J with D_J the inverse of diagonal block J; one
-// wave takes row block 3 of a head (9 products), another its rows 2 and 1 (7).
+// which one product's result is the next one's right operand, so only -M and the inverses of the
+// diagonal blocks of I + M pass through LDS. Wave w owns rows 16 w .. of the Gram products (bf16:
+// exact bf16 products; fp32 and the inverse: v_mfma_f32_16x16x4f32). The diagonal blocks of a head
+// are inverted by one wave, block g by lane group g, a column a lane. From T (I + M) = I the blocks
+// below follow row by row: T_IJ = (sum_{J < S <= I} T_IS (-M)_SJ) D_J with D_J the inverse of
+// diagonal block J; one wave takes row block 3 of a head (9 products), another its rows 2 and 1 (7).
 constexpr int kHeads = 2;      // value heads at a time
 constexpr int kBlockRow = 20;  // floats between the rows of a block in LDS
 
@@ -332,8 +332,15 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
   const int hk = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, i = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Act* kp = static_cast<const Act*>(a.k) + first * a.k_stride + int64_t(hk) * K;
-  const Act* qp = static_cast<const Act*>(a.q) + first * a.q_stride + int64_t(hk) * K;
+  // Rows behind the sequence lie outside the resources' ranges and read as zeros.
+  constexpr uint32_t es = sizeof(Act);
+  const uint32_t kst = static_cast<uint32_t>(a.k_stride) * es, qst = static_cast<uint32_t>(a.q_stride) * es;
+  const rsrc_t kr = make_rsrc_bounded(
+      const_cast<Act*>(static_cast<const Act*>(a.k) + first * a.k_stride + int64_t(hk) * K),
+      (count - 1) * kst + K * es);
+  const rsrc_t qr = make_rsrc_bounded(
+      const_cast<Act*>(static_cast<const Act*>(a.q) + first * a.q_stride + int64_t(hk) * K),
+      (count - 1) * qst + K * es);
   // Steps, decays and write strengths of one head: lane t is token t.
   auto gates = [&](int h, int at_head) {
     float dt = 0.0f, beta = 0.0f;
@@ -364,71 +371,76 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
   {
     const int t = 16 * w + i;
     float sk = 0.0f, sq = 0.0f, mk = 0.0f, mq = 0.0f;
-    auto sums = [](f4 x, float& s, float& m) {
-      s += x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
-      m = max4(m, x);
-    };
     if constexpr (P == 1) {
       constexpr int NB = K / 32;
-      b8 krow[NB], qrow[NB], col[NB];
-      const b8 zero = {};
+      auto load = [&](rsrc_t r, uint32_t off, b8* to) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        krow[b] = t < count ? *reinterpret_cast<const b8*>(kp + t * a.k_stride + 32 * b + 8 * g) : zero;
-        qrow[b] = t < count ? *reinterpret_cast<const b8*>(qp + t * a.q_stride + 32 * b + 8 * g) : zero;
-      }
+        for (int b = 0; b < NB; ++b)
+          to[b] = __builtin_bit_cast(b8, __builtin_amdgcn_raw_buffer_load_b128(r, off + 64 * b, 0, 0));
+      };
+      b8 krow[NB], qrow[NB], col[NB];
+      load(kr, t * kst + 16 * g, krow);
+      load(qr, t * qst + 16 * g, qrow);
       if (w < kHeads && w < a.ratio) gates(hk * a.ratio + w, w);  // while k and q are on their way
+      f4 dk, dq = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int st = 0; st < 4; ++st) {
         if (st > w) continue;
-        const int ts = 16 * st + i;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          col[b] = ts < count ? *reinterpret_cast<const b8*>(kp + ts * a.k_stride + 32 * b + 8 * g) : zero;
+        load(kr, (16 * st + i) * kst + 16 * g, col);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           gk[st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(col[b], krow[b], gk[st], 0, 0, 0);
           gq[st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(col[b], qrow[b], gq[st], 0, 0, 0);
         }
+        dk = gk[st];  // of the last one, st = w
       }
+      // The squared norms are the diagonals of the Gram products: row i's in lane (i / 4, i).
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        f4 x, y;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = krow[b][e], y[e] = krow[b][e + 4];
-        sums(x, sk, mk);
-        sums(y, sk, mk);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = qrow[b][e], y[e] = qrow[b][e + 4];
-        sums(x, sq, mq);
-        sums(y, sq, mq);
+      for (int b = 0; b < NB; ++b) dq = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qrow[b], qrow[b], dq, 0, 0, 0);
+      if (g == i >> 2) {
+        sk = i & 2 ? (i & 1 ? dk[3] : dk[2]) : (i & 1 ? dk[1] : dk[0]);
+        sq = i & 2 ? (i & 1 ? dq[3] : dq[2]) : (i & 1 ? dq[1] : dq[0]);
       }
+      auto largest = [](const b8* x) {  // bf16 magnitudes are ordered as integers
+        u2 m = {0, 0};
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const w4 raw = __builtin_bit_cast(w4, x[b]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u2, raw[e] & 0x7FFF7FFFu));
+        }
+        return __uint_as_float(static_cast<uint32_t>(m[0] > m[1] ? m[0] : m[1]) << 16);
+      };
+      mk = largest(krow);
+      mq = largest(qrow);
     } else {
       constexpr int NB = K / 16;
-      f4 row[NB], col[NB];
-      const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (w < kHeads && w < a.ratio) gates(hk * a.ratio + w, w);
+      auto load = [&](rsrc_t r, uint32_t off, f4* to) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        row[b] = t < count ? *reinterpret_cast<const f4*>(kp + t * a.k_stride + 16 * b + 4 * g) : zero;
+        for (int b = 0; b < NB; ++b)
+          to[b] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 64 * b, 0, 0));
+      };
+      auto sums = [](f4 x, float& s, float& m) {
+        s += x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
+        m = max4(m, x);
+      };
+      f4 row[NB], col[NB];
+      load(kr, t * kst + 16 * g, row);
+      if (w < kHeads && w < a.ratio) gates(hk * a.ratio + w, w);
 #pragma unroll
       for (int b = 0; b < NB; ++b) sums(row[b], sk, mk);
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         if (which == 1) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            row[b] = t < count ? *reinterpret_cast<const f4*>(qp + t * a.q_stride + 16 * b + 4 * g) : zero;
+          load(qr, t * qst + 16 * g, row);
 #pragma unroll
           for (int b = 0; b < NB; ++b) sums(row[b], sq, mq);
         }
 #pragma unroll
         for (int st = 0; st < 4; ++st) {
           if (st > w) continue;
-          const int ts = 16 * st + i;
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            col[b] = ts < count ? *reinterpret_cast<const f4*>(kp + ts * a.k_stride + 16 * b + 4 * g) : zero;
+          load(kr, (16 * st + i) * kst + 16 * g, col);
 #pragma unroll
           for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -456,6 +468,15 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
       if (w < heads) gates(hk * a.ratio + v0 + w, w);
     }
     __syncthreads();  // gates and norms are in
+    if (v0 == 0) {
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {
+        if (st > w) continue;
+        const f4 ks = *reinterpret_cast<const f4*>(&rk_s[16 * st + 4 * g]);
+        gk[st] *= ks * -rk;
+        gq[st] *= ks * rq;
+      }
+    }
     for (int hh = 0; hh < heads; ++hh) {
       char* rec = a.records + (int64_t(blockIdx.x) * a.hv + hk * a.ratio + v0 + hh) * record_bytes(P);
       const int t = 16 * w + i;
@@ -465,13 +486,20 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
         if (st > w) continue;
         const int s = 16 * st + 4 * g, blk = w * (w + 1) / 2 + st;
         const f4 hs = *reinterpret_cast<const f4*>(&hi_s[hh][s]), ls = *reinterpret_cast<const f4*>(&lo_s[hh][s]);
-        const f4 bs = *reinterpret_cast<const f4*>(&beta_s[hh][s]), ks = *reinterpret_cast<const f4*>(&rk_s[s]);
+        const f4 bs = *reinterpret_cast<const f4*>(&beta_s[hh][s]);
         f4 m, x;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float e = exp2_diff(ht, lt, hs[r], ls[r]) * (ks[r] * bs[r]);
-          m[r] = s + r < t ? rk * e * gk[st][r] : 0.0f;
-          x[r] = s + r <= t ? rq * e * gq[st][r] : 0.0f;
+          const float e = exp2_diff(ht, lt, hs[r], ls[r]) * bs[r];
+          m[r] = e * gk[st][r];
+          x[r] = e * gq[st][r];
+        }
+        if (st == w) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            m[r] = 4 * g + r < i ? m[r] : 0.0f;
+            x[r] = 4 * g + r <= i ? x[r] : 0.0f;
+          }
         }
         *reinterpret_cast<f4*>(&Ms[hh][blk][i * kBlockRow + 4 * g]) = m;
         const h4 hi = __builtin_convertvector(x, h4);
@@ -507,7 +535,7 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
           const f4 row = *reinterpret_cast<const f4*>(m + r * kBlockRow + s4);
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            if (s4 + s < r) acc = fmaf(-row[s], x[s4 + s], acc);
+            if (s4 + s < r) acc = fmaf(row[s], x[s4 + s], acc);
         }
         x[r] = acc;
       }
@@ -543,7 +571,7 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
               p = mfma4(m[S * (S + 1) / 2 + J][(4 * g + r) * kBlockRow + i], T[S][r], p);
 #pragma unroll
           for (int r = 0; r < 4; ++r) x = mfma4(m[J * (J + 1) / 2 + J][(4 * g + r) * kBlockRow + i], p[r], x);
-          T[J] = -x;
+          T[J] = x;
           put(block_at(I, J), T[J]);
         }
       };
