@@ -7,7 +7,9 @@
 // One launch: every workgroup scans all lengths by itself (N <= 65535 int32 values, 256 KiB at
 // most, from L2) in tiles of 4096 and writes a slice of its own of the block rows, each row found
 // by a binary search among the tile's block starts in LDS. A scan split over workgroups would need
-// a second launch or a wait between workgroups, which costs more than the repeated reads.
+// a second launch or a wait between workgroups, which costs more than the repeated reads. Bound by
+// the launch and the scan's chain of barriers: 7 sequences 2.6 us, 4096 sequences and 68111
+// block rows 6.7 us.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
