@@ -199,7 +199,8 @@ def gated_delta_scan(q, k, v, dt_raw, beta_raw, A_log, dt_bias, *, dt_min=1e-4, 
     A uniform batch: q, k (B, L, Hk, K), v (B, L, Hv, V), dt_raw, beta_raw (B, L, Hv). Packed
     sequences: the same without the batch axis, (T, ...), with ``lengths`` (N,) int32 on the GPU, or
     ``tables`` = sequence_tables(lengths, T) built once for many layers. float32 or bfloat16, all the
-    same; the rows of q, k, v may lie apart (parts of one projection). A_log, dt_bias (Hv,) float32.
+    same; the rows of q, k, v may lie apart (parts of one projection, each 16-byte aligned, strides a
+    multiple of 8 elements). A_log, dt_bias (Hv,) float32.
     K is 64 or 128, V a multiple of 16 up to 256, Hv a multiple of Hk; ``scale`` defaults to
     K ** -0.5.
     States are float32 (N, Hv, V, K). ``state_in`` None starts from zeros; ``in_slots`` /
