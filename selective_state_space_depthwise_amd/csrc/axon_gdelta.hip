@@ -42,9 +42,10 @@
 // makes of its v (X, E and the writes), is kept in a unit of its own, a power of two that takes the
 // larger of S and v to about 2^5. By the contraction of the delta rule (0 <= beta <= 1) no entry of
 // S, X or E exceeds 2^8 sqrt(K) + 64 2^8 < 2^15 before the next chunk looks at the unit again, so
-// nothing leaves the range of fp16. The states, every accumulator and every factor are fp32. For
-// bf16 activations the operands that only y sees (S, A and E of its two products) are one piece, 11
-// bits: 2^-12 against the 2^-9 of y's own rounding.
+// nothing leaves the range of fp16. The states, every accumulator and every factor are fp32. This
+// holds for bf16 activations too, the operands that only y sees among them: y is what fp32 gives,
+// rounded once. (With S, A and E of y's products in one piece, 2^-11, a value in twenty of y came out
+// as another bf16 number; 16384 tokens took 406 us and 32768 packed ones 487 us.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -63,13 +64,12 @@ constexpr int kThreads = 256;
 
 typedef float f4 __attribute__((ext_vector_type(4)));
 
-// fp16 pieces of an activation (bf16: exact in one) and of A (see above).
+// fp16 pieces of an activation (bf16: exact in one).
 template <typename Act>
 constexpr int kPieces = sizeof(Act) == 2 ? 1 : 2;
 
-// What prep leaves for each (chunk, value head): T in two pieces and A in one or two, each as ten
-// 16 x 16 blocks on and below the diagonal (at block_at), a block as 64 lanes x 4 fp16
-// in left-operand order (lane (g, i): row i, columns 4 g .. 4 g + 3); then the row
+// What prep leaves for each (chunk, value head): T and A in two pieces, each as ten 16 x 16 blocks
+// on and below the diagonal (at block_at), a block as 64 lanes x 4 fp16 in left-operand order (lane (g, i): row i, columns 4 g .. 4 g + 3); then the row
 // factors of the 64 tokens, fp32, and e^{g_last} with its base-2 logarithm. What the walk keeps in
 // LDS comes first.
 constexpr int kBlocks = 10;
@@ -84,9 +84,9 @@ enum Row { kRowX, kRowS, kRowY, kRowKQ, kRows = kRowKQ + 2 };
 __host__ __device__ constexpr int block_at(int I, int J) {
   return I == 0 ? 8 : I == 1 ? J : I == 3 ? 4 + J : J < 2 ? 2 + J : 9;
 }
-constexpr int rows_at(int pieces) { return (2 + pieces) * kBlocks * kBlockBytes; }
-constexpr int lds_bytes(int pieces) { return rows_at(pieces) + 4 * kQ * 4; }
-constexpr int record_bytes(int pieces) { return rows_at(pieces) + kRows * kQ * 4 + 64; }
+constexpr int kRowsAt = 4 * kBlocks * kBlockBytes;
+constexpr int kRecordLds = kRowsAt + 4 * kQ * 4;
+constexpr int kRecordBytes = kRowsAt + kRows * kQ * 4 + 64;
 
 struct DeltaArgs {
   const void *q, *k, *v, *dt_raw, *beta_raw;
@@ -481,7 +481,7 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
       }
     }
     for (int hh = 0; hh < heads; ++hh) {
-      char* rec = a.records + (int64_t(blockIdx.x) * a.hv + hk * a.ratio + v0 + hh) * record_bytes(P);
+      char* rec = a.records + (int64_t(blockIdx.x) * a.hv + hk * a.ratio + v0 + hh) * kRecordBytes;
       const int t = 16 * w + i;
       const float ht = hi_s[hh][t], lt = lo_s[hh][t];
 #pragma unroll
@@ -508,15 +508,14 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
         const h4 hi = __builtin_convertvector(x, h4);
         char* dst = rec + (2 * kBlocks + block_at(w, st)) * kBlockBytes + lane * 8;
         *reinterpret_cast<h4*>(dst) = hi;
-        if (P == 2)
-          *reinterpret_cast<h4*>(dst + kBlocks * kBlockBytes) =
-              __builtin_convertvector(x - __builtin_convertvector(hi, f4), h4);
+        *reinterpret_cast<h4*>(dst + kBlocks * kBlockBytes) =
+            __builtin_convertvector(x - __builtin_convertvector(hi, f4), h4);
       }
       if (w == 2 + hh) {  // the row factors: lane t is token t
         const float hi = hi_s[hh][lane], lo = lo_s[hh][lane];
         const float e = __builtin_amdgcn_exp2f(hi + lo);
         const Scale k2 = scale_of(mk_s[lane]), q2 = scale_of(mq_s[lane]);
-        float* row = reinterpret_cast<float*>(rec + rows_at(P)) + lane;
+        float* row = reinterpret_cast<float*>(rec + kRowsAt) + lane;
         row[kRowX * kQ] = e * (rk_s[lane] * k2.down);
         row[kRowS * kQ] = beta_s[hh][lane] * exp2_diff(hi_s[hh][63], lo_s[hh][63], hi, lo) *
                           (rk_s[lane] * k2.down);
@@ -549,7 +548,7 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
     __syncthreads();
     const int hh = w & 1;
     if (hh < heads) {
-      char* rec = a.records + (int64_t(blockIdx.x) * a.hv + hk * a.ratio + v0 + hh) * record_bytes(P);
+      char* rec = a.records + (int64_t(blockIdx.x) * a.hv + hk * a.ratio + v0 + hh) * kRecordBytes;
       const float(*m)[16 * kBlockRow] = Ms[hh];
       auto put = [&](int blk, f4 x) {
         const h4 hi = __builtin_convertvector(x, h4);
@@ -593,10 +592,11 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
 // Bound by a chunk's chain of dependent products and the LDS reads and conversions that feed them:
 // 32768 packed tokens x 32 heads, bf16, K = V = 128: 333 us, of a CU's about 9800 clocks a chunk the
 // matrix cores are busy for a third, the vector units for half.
-// W waves a workgroup, each with NC tiles of 16 columns of V of one head. Per chunk the workgroup
-// brings k and q, converted to fp16 pieces on the way, as rows of K fp16 (read as left operand of
-// S k^ and S q^, and k by transposing reads as left operand of the state's sum) and the chunk's
-// record (two buffers). The next chunk's rows travel in registers while this one's are used.
+// W waves a workgroup, each with NC tiles of 16 columns of V of one head (two in the first walk over
+// segments of bf16, which has no outputs to sum). Per chunk the workgroup brings k and q, converted to
+// fp16 pieces on the way, as rows of K fp16 (read as left operand of S k^ and S q^, and k by
+// transposing reads as left operand of the state's sum) and the chunk's record (two buffers). The next
+// chunk's rows travel in registers while this one's are used.
 //
 // Row i of tile b of the transposed state is channel 32 (b / 2) + 8 (i / 4) + 4 (b % 2) + i % 4, so
 // that a lane's eight values of two tiles are eight channels in a row of k or q. LDS holds a row's
@@ -616,19 +616,19 @@ constexpr int kOrdered = 1024;  // packed sequences that are put in order
 
 // LOCAL: the first walk over segments: no outputs; columns V .. V + K - 1 are the identity's.
 template <typename Act, int K, int W, int NC, bool LOCAL>
-__global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(64 * W, W == 4 && !LOCAL ? 1 : 2) void walk_kernel(DeltaArgs a) {
   constexpr int P = kPieces<Act>;
   constexpr int NB = K / 16, KB = K / 32;
   constexpr int kRow = K, kHalf = 16 * kRow;     // bytes of half a row, of one half of 16 rows
   constexpr int kMat = 8 * kHalf;                // of one piece (of an fp16 pair) of k or q of a chunk
-  constexpr int kRec = record_bytes(P), kLds = lds_bytes(P), kLoads = kLds / 1024;
+  constexpr int kLoads = kRecordLds / 1024;
   constexpr int kThreadsW = 64 * W;
   constexpr int kBufs = P == 1 && (W == 8 || K == 64) ? 2 : 1;  // of k and q
   constexpr int kUnits = kQ * K / 8 / kThreadsW;     // 16-byte pieces of k (and q) a thread brings
-  static_assert(kLds % 1024 == 0, "whole wave loads");
+  static_assert(kRecordLds % 1024 == 0, "whole wave loads");
   __shared__ __align__(16) char ks[kBufs][P * kMat];
   __shared__ __align__(16) char qs[kBufs][P * kMat];
-  __shared__ __align__(16) char rs2[2][kLds];
+  __shared__ __align__(16) char rs2[2][kRecordLds];
   __shared__ __align__(16) char vs[W][kQ * 16 * NC * sizeof(Act)];
 
   // The value heads of a key head, and the column groups of each, go to one XCD: k and q come to its
@@ -697,7 +697,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     const int64_t c = chunks - 1 - lane;
     float sum = 0.0f;
     if (c >= 0)
-      sum = *reinterpret_cast<const float*>(a.records + ((row0 + c) * a.hv + h) * int64_t(kRec) + rows_at(P) +
+      sum = *reinterpret_cast<const float*>(a.records + ((row0 + c) * a.hv + h) * int64_t(kRecordBytes) + kRowsAt +
                                             (kRows * kQ + 1) * 4);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -755,8 +755,8 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
   // The record goes to LDS without passing through registers, 1 KiB a wave and instruction.
   // (Where the pieces are no multiple of the waves, the last one is brought more than once.)
   auto load_record = [&](int64_t c, int buf) {
-    const char* rec = a.records + ((row0 + c) * a.hv + h) * int64_t(kRec);
-    end_next = *reinterpret_cast<const float*>(rec + rows_at(P) + kRows * kQ * 4);
+    const char* rec = a.records + ((row0 + c) * a.hv + h) * int64_t(kRecordBytes);
+    end_next = *reinterpret_cast<const float*>(rec + kRowsAt + kRows * kQ * 4);
 #pragma unroll
     for (int u0 = 0; u0 < kLoads; u0 += W) {
       const int u = min(u0 + w, kLoads - 1);
@@ -774,12 +774,12 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     const rsrc_t qr = make_rsrc_bounded(
         const_cast<Act*>(static_cast<const Act*>(a.q) + first * a.q_stride + int64_t(hk) * K),
         (count - 1) * qoff + K * es);
-    const char* rec = a.records + ((row0 + c) * a.hv + h) * int64_t(kRec);
+    const char* rec = a.records + ((row0 + c) * a.hv + h) * int64_t(kRecordBytes);
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
       const int at = tid + u * kThreadsW, t = at / (K / 8), piece = at % (K / 8);
       const uint32_t ko = fresh(t * koff + piece * 8 * es), qo = fresh(t * qoff + piece * 8 * es);
-      sh[u] = *reinterpret_cast<const float2*>(rec + rows_at(P) + kRowKQ * kQ * 4 + t * 8);
+      sh[u] = *reinterpret_cast<const float2*>(rec + kRowsAt + kRowKQ * kQ * 4 + t * 8);
       pk[u].load(kr, ko);
       if (!LOCAL) pq[u].load(qr, qo);
     }
@@ -882,7 +882,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
   };
   auto row4 = [&](int row, int tt) {
-    return *reinterpret_cast<const f4*>(rs + rows_at(P) + (row * kQ + 16 * tt + 4 * g) * 4);
+    return *reinterpret_cast<const f4*>(rs + kRowsAt + (row * kQ + 16 * tt + 4 * g) * 4);
   };
 
   // No branch inside the loop but the loop itself, so that the waits for loads count exactly and
@@ -900,13 +900,12 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
     rs = rs2[c & 1];
     end = end_next;
     // This wave's parts of the record and v are in LDS: vector memory operations of a wave complete
-    // in the order of their issue, and behind them and k and q only y's 4 NC stores were issued.
+    // in the order of their issue, and behind them and k and q only y's 4 stores were issued.
+    static_assert(LOCAL || NC == 1, "stores counted");
     if (LOCAL)
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    else if (NC == 1)
-      asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
     else
-      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
     // Behind this barrier chunk c is complete in LDS and every wave is done with chunk c - 1, whose
     // record buffer the next chunk takes.
     __syncthreads();
@@ -980,6 +979,10 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
         for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
           for (int z = 0; z < NC; ++z) O[z][tt] = mfma_h(hi[z], q[tt][0], kb ? O[z][tt] : zero);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+          for (int z = 0; z < NC; ++z) O[z][tt] = mfma_h(lo[z], q[tt][0], O[z][tt]);
       }
       if constexpr (P == 2) {
 #pragma unroll
@@ -987,10 +990,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
 #pragma unroll
           for (int z = 0; z < NC; ++z) {
             X[z][tt] = mfma_h(k[tt][1], hi[z], X[z][tt]);
-            if constexpr (!LOCAL) {
-              O[z][tt] = mfma_h(lo[z], q[tt][0], O[z][tt]);
-              O[z][tt] = mfma_h(hi[z], q[tt][1], O[z][tt]);
-            }
+            if constexpr (!LOCAL) O[z][tt] = mfma_h(hi[z], q[tt][1], O[z][tt]);
           }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -1042,9 +1042,7 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
       for (int z = 0; z < NC; ++z)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if constexpr (!LOCAL && P == 1)
-            eh[z][s] = first_piece(E[z][2 * s], E[z][2 * s + 1]);
-          else if constexpr (!LOCAL)
+          if constexpr (!LOCAL)
             split8(E[z][2 * s], E[z][2 * s + 1], &eh[z][s], &el[z][s]);
           split8(E[z][2 * s] * row4(kRowS, 2 * s), E[z][2 * s + 1] * row4(kRowS, 2 * s + 1), &uh[z][s],
                  &ul[z][s]);
@@ -1052,23 +1050,19 @@ __global__ __launch_bounds__(64 * W, 2) void walk_kernel(DeltaArgs a) {
       if constexpr (!LOCAL) {
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
-          const float f = *reinterpret_cast<const float*>(rs + rows_at(P) + (kRowY * kQ + 16 * tt + i) * 4);
+          const float f = *reinterpret_cast<const float*>(rs + kRowsAt + (kRowY * kQ + 16 * tt + i) * 4);
 #pragma unroll
           for (int z = 0; z < NC; ++z) O[z][tt] *= f;
         }
 #pragma unroll
         for (int e = 0; e < 6; ++e) {
           const int tt = kLowerRow[e], s = kLowerCol[e];
-          const h8 a0 = lower(2, tt, s);
+          const h8 a0 = lower(2, tt, s), a1 = lower(3, tt, s);
 #pragma unroll
-          for (int z = 0; z < NC; ++z) O[z][tt] = mfma_h(eh[z][s], a0, O[z][tt]);
-          if constexpr (P == 2) {
-            const h8 a1 = lower(3, tt, s);
-#pragma unroll
-            for (int z = 0; z < NC; ++z) {
-              O[z][tt] = mfma_h(el[z][s], a0, O[z][tt]);
-              O[z][tt] = mfma_h(eh[z][s], a1, O[z][tt]);
-            }
+          for (int z = 0; z < NC; ++z) {
+            O[z][tt] = mfma_h(eh[z][s], a0, O[z][tt]);
+            O[z][tt] = mfma_h(el[z][s], a0, O[z][tt]);
+            O[z][tt] = mfma_h(eh[z][s], a1, O[z][tt]);
           }
         }
       }
@@ -1472,7 +1466,7 @@ ScanPlan plan_scan(const axon_gated_delta_shape* s) {
   ScanPlan p;
   if (!s->tokens) return p;
   const size_t rows = size_t(rows_of(s)), hv = size_t(s->value_heads);
-  p.bytes = record_bytes(s->act_dtype == AXON_BF16 ? 1 : 2) * rows * hv;
+  p.bytes = kRecordBytes * rows * hv;
   const int64_t units = s->sequences * s->value_heads, chunks = s->tokens / kQ / s->sequences;
   if (units > kSegmentUnits || chunks < kSegmentMin * 4) return p;
   const int64_t segs = std::min<int64_t>(256 / units, chunks / kSegmentMin);
@@ -1534,22 +1528,13 @@ void launch_scan(DeltaArgs a, bool any, hipStream_t st) {
     hipLaunchKernelGGL(join_kernel<K>, dim3(unsigned(a.sequences * a.hv), unsigned((a.value_dim + 127) / 128)),
                        dim3(kThreads), 0, st, a);
   }
-  const int64_t units = int64_t(a.sequences) * a.hv * (split ? a.segs : 1);
-  if (a.value_dim <= 64) {
+  // Four waves hold up to 64 columns (K = 128, V = 64, 16 x 2048 tokens x 32 heads: 445 us; eight
+  // waves, half of them idle, 548 us). Eight waves of one tile beat four of two, which fill a CU's LDS
+  // alone (V = 128: 491 us against 570 us).
+  if (a.value_dim <= 64)
     go(walk_kernel<Act, K, 4, 1, false>, 4, 1, a.value_dim);
-    return;
-  }
-  // Two tiles a wave read each operand from LDS once for both, and two such workgroups share a CU:
-  // 16 x 2048 tokens x 32 heads 439 us against 458 us. A workgroup of 8 waves with one tile takes
-  // less time a chunk, which counts where there are fewer workgroups or one long sequence is left at
-  // the end (32768 packed tokens: walk 333 us against 387 us).
-  if constexpr (kPieces<Act> == 1) {
-    if (units >= 512 && !a.starts) {
-      go(walk_kernel<Act, K, 4, 2, false>, 4, 2, a.value_dim);
-      return;
-    }
-  }
-  go(walk_kernel<Act, K, 8, 1, false>, 8, 1, a.value_dim);
+  else
+    go(walk_kernel<Act, K, 8, 1, false>, 8, 1, a.value_dim);
 }
 
 template <typename Act, int K>

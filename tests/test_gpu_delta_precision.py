@@ -1,0 +1,79 @@
+"""The gated delta scan to the precision of its fp32 arithmetic: y and the states against the 64-bit
+recurrence with bounds of the size of y, and bf16 outputs that are the rounding of such a y.
+
+Tolerance. A state behind a chunk is the end of three sums over K or 64 products (S k, T X and the
+state's own), y of two more (S q, A E), and the chunk before it has gone through its own three: eight
+sums. Their operands are held to 2^-23 of the largest of a column or row (two fp16 pieces), a product
+leaves out the two low pieces (2^-22 at most, 2^-24 in the mean), and accumulators are fp32. The
+roundings of one sum are independent and of either sign, so that their total stays below 8 times the
+largest of them, 2^-23 R with R the largest row norm of a state (keys and queries have length one, and
+the writes are no larger than R allows). That is 8 * 8 * 2^-23 R for a state, times the scale for y;
+older chunks are forgotten by the decays and the writes. The last rounding of an fp32 value adds
+2^-24 of it, and the decays' exponents (all below 2^4 here where they matter) no more. A bf16 output
+must be a rounding of a number within this bound: nearer to the exact value than half a step only
+helps where the exact value lies next to a border between two bf16 numbers."""
+from __future__ import annotations
+
+import pytest
+
+from gpu_util import say
+
+torch = pytest.importorskip("torch")
+
+import delta_ref as ref  # noqa: E402
+from test_gpu_delta import _axon, _gpu, make, rows, state  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+STEP = 2.0 ** -23
+
+
+def near(got, want, size, what):
+    got, bf = got.detach().double().cpu(), got.dtype == torch.bfloat16
+    off = 64 * STEP * size + STEP * want.abs()
+    low, high = want - off, want + off
+    if bf:
+        low, high = (t.bfloat16().double() for t in (low, high))
+    bad = ~((got >= low) & (got <= high))
+    assert not bool(bad.any()), (f"{what}: {int(bad.sum())} of {bad.numel()} outside, largest error "
+                                 f"{float((got - want).abs().max()):.3e}, size {size:.3e}")
+
+
+CASES = [
+    # (B, L, hk, hv, K, V)
+    (1, 260, 2, 4, 128, 128),
+    (1, 260, 2, 4, 64, 64),
+    (1, 200, 1, 2, 128, 48),
+    (2, 130, 1, 3, 64, 240),
+    (2, 2200, 1, 2, 128, 128),   # walked in segments
+    (32, 130, 8, 16, 128, 128),  # a large uniform batch
+    (32, 70, 8, 16, 64, 80),
+]
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,hk,hv,K,V", CASES)
+def test_precision(B, L, hk, hv, K, V, act):
+    say(f"[delta precision] B={B} L={L} heads {hk}/{hv} K={K} V={V} {act}")
+    d = make((B, L), hk, hv, K, V, act, seed=L + V)
+    s0 = state(B, hv, V, K, L)
+    y, s1 = _axon().gated_delta_scan(**d, state_in=s0)
+    torch.cuda.synchronize()
+    for b in range(0, B, 15):
+        yr, sr, big = ref.delta_tokens(s0[b], **rows(d, b))
+        near(s1[b], sr, big, f"state[{b}]")
+        near(y[b], yr, K ** -0.5 * big, f"y[{b}]")
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_precision_of_packed_sequences(act):
+    lengths = [100, 0, 1, 64, 257, 40]
+    hk, hv, K, V = 2, 4, 128, 64
+    d = make((sum(lengths),), hk, hv, K, V, act, seed=17)
+    y, s1 = _axon().gated_delta_scan(**d, lengths=torch.tensor(lengths, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    at = 0
+    for n, length in enumerate(lengths):
+        yr, sr, big = ref.delta_tokens(torch.zeros(hv, V, K), **rows(d, slice(at, at + length)))
+        near(s1[n], sr, big, f"state {n}")
+        near(y[at:at + length], yr, K ** -0.5 * big, f"y of sequence {n}")
+        at += length
