@@ -88,6 +88,11 @@ constexpr int kRowsAt = 4 * kBlocks * kBlockBytes;
 constexpr int kRecordLds = kRowsAt + 4 * kQ * 4;
 constexpr int kRecordBytes = kRowsAt + kRows * kQ * 4 + 64;
 
+// Bytes of a segment's M: each row in units of its own, a power of two that takes its largest entry
+// to [1, 2) (M shrinks with the decays of its segment, down to 2^-160, and pieces without a unit end at
+// 2^-25), then the units as K floats.
+constexpr int carry_bytes(int k) { return 4 * k * k + 4 * k; }
+
 struct DeltaArgs {
   const void *q, *k, *v, *dt_raw, *beta_raw;
   const float *A_log, *dt_bias;
@@ -105,7 +110,7 @@ struct DeltaArgs {
   int chunks_per_seq;   // uniform batch
   int seg_chunks;       // chunks of a segment, 0: sequences are walked whole
   int segs;             // segments of a sequence at most
-  char* seg_m;          // (segment, value head): M^T, two pieces of K x K fp16
+  char* seg_m;          // (segment, value head): M^T, two pieces of K x K fp16, and M's row factors
   int32_t* seg_flag;    // (segment, value head): whether M is not zero
   float* seg_s;         // (segment, value head): N, then the state before the segment, V x K
 };
@@ -1105,20 +1110,27 @@ __global__ __launch_bounds__(64 * W, W == 4 && !LOCAL ? 1 : 2) void walk_kernel(
   }
   if constexpr (LOCAL) {
     float* const to = a.seg_s + (seg_row + seg) * state_size + state_head + fresh(lane & 15) * K + 8 * g;
-    _Float16* const mt = reinterpret_cast<_Float16*>(a.seg_m) + ((seg_row + seg) * a.hv + h) * (2 * K * K);
+    char* const carry = a.seg_m + ((seg_row + seg) * a.hv + h) * int64_t(carry_bytes(K));
+    _Float16* const mt = reinterpret_cast<_Float16*>(carry);
 #pragma unroll
-    for (int z = 0; z < NC; ++z)
+    for (int z = 0; z < NC; ++z) {
+      if (col0 + 16 * z < a.value_dim) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int k = 32 * (b >> 1) + 4 * (b & 1);
-        const f4 x = S[z][b] * unit[z];
-        if (col0 + 16 * z < a.value_dim) {
-          *reinterpret_cast<f4*>(to + 16 * z * K + k) = x;
-        } else if (!cut && col0 + 16 * z < columns) {
+        for (int b = 0; b < NB; ++b)
+          *reinterpret_cast<f4*>(to + 16 * z * K + 32 * (b >> 1) + 4 * (b & 1)) = S[z][b] * unit[z];
+      } else if (!cut && col0 + 16 * z < columns) {
+        const int row = col0 + 16 * z + i - a.value_dim;
+        float m = 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) m = max4(m, S[z][b]);
+        const Scale of_row = scale_of(column_max(m) * unit[z]);
+        if (g == 0) reinterpret_cast<float*>(carry + 4 * K * K)[row] = of_row.down;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const f4 x = S[z][b] * (unit[z] * of_row.up);
           const h4 hi = __builtin_convertvector(x, h4);
           const h4 lo = __builtin_convertvector(x - __builtin_convertvector(hi, f4), h4);
           // Operand (b, row / 32) of M^T: lane (row / 8 % 4, this row of the tile), entry row % 8.
-          const int row = col0 + 16 * z + i - a.value_dim;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int at = ((b * KB + (row >> 5)) * 64 + ((row >> 3) & 3) * 16 + 4 * g + r) * 8 + (row & 7);
@@ -1127,6 +1139,7 @@ __global__ __launch_bounds__(64 * W, W == 4 && !LOCAL ? 1 : 2) void walk_kernel(
           }
         }
       }
+    }
     return;
   }
   const int64_t slot_out = a.out_slots ? a.out_slots[n] : n;
@@ -1189,13 +1202,16 @@ __global__ __launch_bounds__(kThreads) void join_kernel(DeltaArgs a) {
   auto nonzero = [&](int64_t seg) {
     return __builtin_amdgcn_readfirstlane(a.seg_flag[(seg_row + seg) * a.hv + h]) != 0;
   };
+  f4 S[NC][NB], N[2][NC][NB], F[2][NB];  // F: M's row factors
   auto load = [&](int64_t seg, int buf) {
-    const char* from = a.seg_m + ((seg_row + seg) * a.hv + h) * int64_t(kBytes);
+    const char* from = a.seg_m + ((seg_row + seg) * a.hv + h) * int64_t(carry_bytes(K));
 #pragma unroll
     for (int u = 0; u < kLoads; u += 4)
       load_to_lds(from + (u + w) * 1024, lane * 16, &ms[buf][(u + w) * 1024]);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      F[buf][b] = *reinterpret_cast<const f4*>(from + kBytes + (32 * (b >> 1) + 8 * g + 4 * (b & 1)) * 4);
   };
-  f4 S[NC][NB], N[2][NC][NB];
   auto load_n = [&](int64_t seg, int buf) {
     const float* from = a.seg_s + (seg_row + seg) * state_size;
 #pragma unroll
@@ -1241,12 +1257,13 @@ __global__ __launch_bounds__(kThreads) void join_kernel(DeltaArgs a) {
     for (int z = 0; z < NC; ++z) {
       float big = 0.0f;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) big = max4(big, S[z][b]);
+      for (int b = 0; b < NB; ++b) big = max4(big, S[z][b] * F[buf][b]);
       unit[z] = scale_of(column_max(big));
       const float up = unit[z].up * 0x1p5f;
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
-        split8(S[z][2 * kb] * up, S[z][2 * kb + 1] * up, &hi[z][kb], &lo[z][kb]);
+        split8(S[z][2 * kb] * F[buf][2 * kb] * up, S[z][2 * kb + 1] * F[buf][2 * kb + 1] * up, &hi[z][kb],
+               &lo[z][kb]);
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -1473,7 +1490,7 @@ ScanPlan plan_scan(const axon_gated_delta_shape* s) {
   p.seg_chunks = (chunks + segs - 1) / segs;
   const size_t count = (rows / size_t(p.seg_chunks) + size_t(s->sequences)) * hv;
   p.off_m = (p.bytes + 255) / 256 * 256;
-  p.off_s = p.off_m + count * 4 * size_t(s->key_dim * s->key_dim);
+  p.off_s = p.off_m + count * size_t(carry_bytes(int(s->key_dim)));
   p.off_flag = p.off_s + count * 4 * size_t(s->value_dim * s->key_dim);
   p.bytes = p.off_flag + (count * 4 + 255) / 256 * 256;
   return p;

@@ -77,3 +77,35 @@ def test_precision_of_packed_sequences(act):
         near(s1[n], sr, big, f"state {n}")
         near(y[at:at + length], yr, K ** -0.5 * big, f"y of sequence {n}")
         at += length
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [64, 128])
+@pytest.mark.parametrize("halvings", [3.3, 6.3, 12.6, 19.7])
+def test_states_that_only_decay(halvings, K, act):
+    """A state that nothing is written to loses `halvings` powers of two every 576 tokens (a segment of
+    this call) and is carried through the segments: errors count against what is left of it, token by
+    token. Each decay's exponent is a product of rounded factors (step, rate, log2 e), each off by 2^-24
+    of it and the step by twice that, all of them alike, so the bound grows by 4 * 2^-23 of the sum of
+    the exponents; the products with M of every segment are sums of their own (8 * 2^-23 each, four at
+    most)."""
+    say(f"[delta precision] {halvings} halvings a segment, K={K} {act}")
+    L, hv, V = 2200, 2, 32
+    d = make((1, L), 1, hv, K, V, act, seed=5)
+    d["v"].zero_()
+    d["beta_raw"].fill_(-20.0)
+    d["A_log"].zero_()
+    d["dt_bias"].zero_()
+    d["dt_raw"].fill_(float(torch.tensor(halvings * 0.6931 / 576, dtype=torch.float64).expm1().log()))
+    s0 = state(1, hv, V, K, 1)
+    y, s1 = _axon().gated_delta_scan(**d, state_in=s0)
+    torch.cuda.synchronize()
+    yr, sr, _ = ref.delta_tokens(s0[0], **rows(d, 0))
+    gone = torch.log1p(torch.exp(d["dt_raw"][0, :, 0].double().cpu())).cumsum(0)
+    left = float(s0[0].double().norm(dim=-1).max()) * torch.exp(-gone)
+    bound = (64 + 4 * 8 + 4 * gone) * STEP * left
+    off = float((s1[0].double().cpu() - sr).abs().max())
+    assert off <= float(bound[-1]), f"state: {off / float(bound[-1]):.2f} times the bound"
+    bound = (K ** -0.5 * bound)[:, None, None] + (2.0 ** -8 * yr.abs() if act == "bf16" else 0.0)
+    off = float(((y[0].double().cpu() - yr).abs() / bound).max())
+    assert off <= 1.0, f"y: {off:.2f} times the bound"
