@@ -937,12 +937,14 @@ __global__ __launch_bounds__(64 * W, W == 4 && !LOCAL ? 1 : 2) void walk_kernel(
       // The unit stays while the column's largest is between 2^2 and 2^8 of it.
       const float at = m * inverse[z];
       if (__any(m > 0.0f && !(at >= 0x1p2f && at <= 0x1p8f))) {
+        // Columns of zeros keep theirs: from a large unit to the smallest the factor is infinite. Where
+        // little is left of a state in a large unit it is as well, hence two steps.
         const Scale to = scale_of(m);
-        const float by = unit[z] * (to.up * 0x1p5f);
-        inverse[z] = to.up * 0x1p5f;
-        unit[z] = to.down * 0x1p-5f;
+        const float up = m > 0.0f ? to.up * 0x1p5f : inverse[z], from = unit[z];
+        inverse[z] = up;
+        unit[z] = m > 0.0f ? to.down * 0x1p-5f : from;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) S[z][b] *= by;
+        for (int b = 0; b < NB; ++b) S[z][b] = S[z][b] * from * up;
       }
     }
     // X and the state's part of y. Left operands are read ahead of their products (a read from LDS

@@ -109,3 +109,33 @@ def test_states_that_only_decay(halvings, K, act):
     bound = (K ** -0.5 * bound)[:, None, None] + (2.0 ** -8 * yr.abs() if act == "bf16" else 0.0)
     off = float(((y[0].double().cpu() - yr).abs() / bound).max())
     assert off <= 1.0, f"y: {off:.2f} times the bound"
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("halvings", [135, 100000])
+def test_large_values_that_are_forgotten(halvings, act):
+    """One column of v is large, then one token's decay takes nearly all or all of its state away, and
+    other columns grow afterwards: the first column stays finite, and no larger than what is left.
+    The unit of a column holds for a chunk, here the one that begins with that decay: its writes are
+    2^-135 of the unit where pieces end at 2^-25, so they are lost, and the state behind the chunk is
+    the decayed one without what the later tokens take off. Either is at most 2^-halvings R long, with R
+    the largest row norm before, so they differ by twice that; the decay is a subnormal fp32 number of
+    14 bits, which the factor of 2.01 covers. The outputs are those of such a state."""
+    L, hv, K, V = 200, 1, 128, 32
+    d = make((1, L), 1, hv, K, V, act, seed=5)
+    d["v"][:, :64, :, 0] *= 1e30
+    d["v"][:, 64:, :, 0] = 0
+    d["v"][:, 128:, :, 1:] *= 4096
+    d["dt_raw"][:, 64] = 300.0  # cut to dt_max = 100
+    d["A_log"].fill_(float(torch.tensor(halvings * 0.69314718 / 100).log()))
+    d["dt_bias"].fill_(-30.0 if halvings > 1000 else -9.0)
+    y, s1 = _axon().gated_delta_scan(**d)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(s1).all())
+    column = rows({x: (t if x in ("A_log", "dt_bias") else t[0])
+                   for x, t in dict(d, v=d["v"][..., :1]).items()}, slice(None))
+    yr, sr, big = ref.delta_tokens(torch.zeros(hv, 1, K), **column)
+    bound = 2.01 * big * 2.0 ** -halvings
+    assert float((s1[0, :, :1].double().cpu() - sr).abs().max()) <= bound
+    off = (y[0, 65:, :, :1].double().cpu() - yr[65:]).abs()
+    assert float(off.max()) <= K ** -0.5 * bound * (1 + 2.0 ** -8)
