@@ -355,8 +355,11 @@ axon_status axon_sequence_tables(int64_t sequences, int64_t total_tokens, int64_
  * sequence may read a slot that another one writes; else those states and outputs are
  * unspecified (no other memory is touched).
  *
- * A value that is not finite in a token makes the outputs of its head in the whole 64-token chunk
- * and after it unspecified (a step: of its row and head); no other sequence or head sees it. */
+ * NaN in a token's k, v, dt_raw or beta_raw makes the state NaN (that of v its own row v), and with
+ * it the outputs of its head from there on (a scan: those of its 64-token chunk may be as well); so
+ * does an infinity, unless dt_raw or beta_raw has it, where it is their limit. One exception: a long
+ * sequence of few heads is walked in segments, and the state behind one forgets what decays have
+ * since multiplied by less than 2^-160, NaN too. No other sequence or head sees it. */
 typedef struct {
   int64_t sequences;    /* batch rows, or packed sequences */
   int64_t tokens;       /* rows of q, k, v: sequences * seqlen, or the packed buffer's rows */

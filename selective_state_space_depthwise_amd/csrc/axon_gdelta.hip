@@ -128,9 +128,11 @@ __device__ __forceinline__ float4 load4(const bf16_bits* p) {
                      __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
 }
 
-// softplus to the last bits: the step enters the exponent of the decay multiplied by the rate.
+// softplus to the last bits: the step enters the exponent of the decay multiplied by the rate. NaN
+// stays NaN (fminf and fmaxf would make a bound of it).
 __device__ __forceinline__ float gate_step(float v, float lo, float hi) {
-  return fminf(fmaxf(fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))), lo), hi);
+  const float dt = fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v)));
+  return dt < lo ? lo : dt > hi ? hi : dt;
 }
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
 
@@ -358,7 +360,8 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
       beta = sigmoid(load_act(static_cast<const Act*>(a.beta_raw), at));
     }
     // No decay below 2^-16384 differs from 0: the bound keeps the sums finite for any dt_max.
-    float hi = fmaxf(dt * decay_rate_log2(a.A_log[h]), -16384.0f), lo = 0.0f;
+    float hi = dt * decay_rate_log2(a.A_log[h]), lo = 0.0f;
+    if (hi < -16384.0f) hi = -16384.0f;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const float oh = __shfl_up(hi, d, 64), ol = __shfl_up(lo, d, 64);

@@ -139,3 +139,58 @@ def test_large_values_that_are_forgotten(halvings, act):
     assert float((s1[0, :, :1].double().cpu() - sr).abs().max()) <= bound
     off = (y[0, 65:, :, :1].double().cpu() - yr[65:]).abs()
     assert float(off.max()) <= K ** -0.5 * bound * (1 + 2.0 ** -8)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("what", ["q", "k", "v", "dt_raw", "beta_raw"])
+@pytest.mark.parametrize("L", [200, 2300])  # whole, and in segments
+def test_nan_is_not_lost(L, what, act):
+    """NaN at one token: the outputs from there on and the state are NaN in its head (for q the output
+    of the token alone has to be), and those before its chunk and of the other head do not change."""
+    d = make((1, L), 2, 2, 64, 32, act, seed=5)
+    d["A_log"][0] = -10.0  # nothing is forgotten
+    y0, s0 = _axon().gated_delta_scan(**d)
+    d[what][0, 70, 0] = float("nan")
+    y, s1 = _axon().gated_delta_scan(**d)
+    torch.cuda.synchronize()
+    assert torch.equal(y[:, :, 1], y0[:, :, 1]) and torch.equal(s1[:, 1], s0[:, 1])
+    assert torch.equal(y[:, :64], y0[:, :64])
+    if what == "q":
+        assert bool(y[0, 70, 0].isnan().all()) and torch.equal(s1, s0)
+        assert torch.equal(y[:, 128:], y0[:, 128:])
+    else:
+        assert bool(y[0, 70:, 0].isnan().all()) and bool(s1[0, 0].isnan().all())
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("what", ["q", "k", "v", "dt_raw", "beta_raw"])
+def test_nan_is_not_lost_by_a_step(what, act):
+    d = make((3,), 2, 2, 64, 32, act, seed=6)
+    s0, s = state(3, 2, 32, 64), state(3, 2, 32, 64)
+    y0 = _axon().gated_delta_step(**d, state=s0)
+    d[what][1, 0] = float("nan")
+    y = _axon().gated_delta_step(**d, state=s)
+    torch.cuda.synchronize()
+    assert bool(y[1, 0].isnan().all())
+    assert torch.equal(s, s0) if what == "q" else bool(s[1, 0].isnan().all())
+    y[1, 0], s[1, 0] = y0[1, 0], s0[1, 0]
+    assert torch.equal(y, y0) and torch.equal(s, s0)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_infinite_gates_are_their_limits(act):
+    """dt_raw of either infinity is dt_max or dt_min, beta_raw 1 or 0."""
+    d = make((1, 100), 1, 2, 64, 32, act, seed=7)
+    d["dt_raw"][:, 30], d["dt_raw"][:, 50] = float("inf"), float("-inf")
+    d["beta_raw"][:, 31], d["beta_raw"][:, 51] = float("inf"), float("-inf")
+    s0 = state(1, 2, 32, 64)
+    y, s1 = _axon().gated_delta_scan(**d, state_in=s0, dt_max=2.0)
+    one = state(1, 2, 32, 64)
+    step = [_axon().gated_delta_step(**{x: (t if x in ("A_log", "dt_bias") else t[:, j].clone())
+                                        for x, t in d.items()}, state=one, dt_max=2.0) for j in range(100)]
+    torch.cuda.synchronize()
+    yr, sr, big = ref.delta_tokens(s0[0], **rows(d, 0), dt_max=2.0)
+    near(y[0], yr, 64 ** -0.5 * big, "y")
+    near(torch.cat(step), yr, 64 ** -0.5 * big, "y of the steps")
+    near(s1[0], sr, big, "state")
+    near(one[0], sr, big, "state of the steps")
