@@ -29,7 +29,8 @@ ARCH = "gfx950"
 ROCM_LIB = "/opt/rocm/lib"  # hipBLASLt (the layer's projection GEMMs)
 # Packed-FP32 instructions stay off: the compiler would otherwise form v_pk_* FP32 ops on its own.
 HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Xclang", "-target-feature",
-             "-Xclang", "-packed-fp32-ops", "-Wall", "-Wno-unused-command-line-argument"]
+             "-Xclang", "-packed-fp32-ops", "-Wall", "-Werror=inline-asm",
+             "-Wno-unused-command-line-argument"]
 
 
 # Sanitizer build (host code only; the GPU code is built as usual): AddressSanitizer and

@@ -290,14 +290,15 @@ __device__ __forceinline__ uint32_t fresh(uint32_t v) {
 
 // 16 bytes a lane from `base + off` to the wave's consecutive 1024 bytes at `to` in LDS. Written out
 // because the compiler would wait for the copy before any read of LDS, also of another buffer; the
-// caller waits for it (no register is written).
+// caller waits for it (no register is written). m0, where the instruction takes the place in LDS from,
+// is an operand, so that the compiler knows when it is in use.
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, char* to) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane(
       static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)to)));
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
-               : "s"(m0), "v"(off), "s"(base)
-               : "m0", "memory");
+               : "{m0}"(m0), "v"(off), "s"(base)
+               : "memory");
 }
 
 // The largest over the four lanes (g = 0 .. 3) that share a column.
