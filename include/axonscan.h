@@ -319,6 +319,15 @@ size_t axon_sequence_tables_count(int64_t sequences, int64_t total_tokens, int64
 axon_status axon_sequence_tables(int64_t sequences, int64_t total_tokens, int64_t block,
                                  const int32_t* lengths, int32_t* tables, void* stream);
 
+/* Zeros the rows of a packed buffer that lie behind its last sequence, for an output that nothing was
+ * written to before (axon_gated_delta_scan leaves these rows as they were): rows starts[sequences] ..
+ * total_tokens - 1 of `rows`, row_bytes each. tables: of axon_sequence_tables for these sequences (only
+ * that entry is read; it is cut to [0, total_tokens]). Limits: sequences and total_tokens as above;
+ * row_bytes a positive multiple of 16; total_tokens * row_bytes <= 2^42; rows 16-byte aligned and not
+ * overlapping the tables' starts. */
+axon_status axon_clear_behind_sequences(int64_t sequences, int64_t total_tokens, int64_t row_bytes,
+                                        const int32_t* tables, void* rows, void* stream);
+
 /* ---- Gated delta rule ------------------------------------------------------------------------
  * The scalar-decay recurrence of the SSD core with the delta rule's write: what the state already
  * answers for a key is taken off before the value is written. For every sequence and value head h

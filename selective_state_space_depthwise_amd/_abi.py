@@ -149,6 +149,8 @@ def load():
         lib.axon_sequence_tables_count.argtypes = [I, I, I]
         lib.axon_sequence_tables.restype = ctypes.c_int
         lib.axon_sequence_tables.argtypes = [I, I, I, P, P, P]
+        lib.axon_clear_behind_sequences.restype = ctypes.c_int
+        lib.axon_clear_behind_sequences.argtypes = [I, I, I, P, P, P]
         lib.axon_gated_delta_scan_workspace_bytes.restype = ctypes.c_size_t
         lib.axon_gated_delta_scan_workspace_bytes.argtypes = [ctypes.POINTER(GatedDeltaShape)]
         lib.axon_gated_delta_scan.restype = ctypes.c_int
@@ -277,6 +279,11 @@ def sequence_tables_count(sequences, total_tokens, block) -> int:
 def raw_sequence_tables(sequences, total_tokens, block, lengths, tables, stream) -> int:
     """axon_sequence_tables with integer pointers. Returns the status code."""
     return load().axon_sequence_tables(sequences, total_tokens, block, lengths, tables, stream)
+
+
+def raw_clear_behind_sequences(sequences, total_tokens, row_bytes, tables, rows, stream) -> int:
+    """axon_clear_behind_sequences with integer pointers. Returns the status code."""
+    return load().axon_clear_behind_sequences(sequences, total_tokens, row_bytes, tables, rows, stream)
 
 
 def gated_delta_workspace_bytes(shape: GatedDeltaShape) -> int:

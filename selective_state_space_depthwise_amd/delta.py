@@ -205,9 +205,9 @@ def gated_delta_scan(q, k, v, dt_raw, beta_raw, A_log, dt_bias, *, dt_min=1e-4, 
     K ** -0.5.
     States are float32 (N, Hv, V, K). ``state_in`` None starts from zeros; ``in_slots`` /
     ``out_slots`` (N,) int32 address pools of states (a slot outside the pool: zeros / not stored).
-    ``state_out`` may be ``state_in``. Returns (y, state_out); y has v's shape, its rows behind the
-    last packed sequence are left as they were. Asynchronous on ``stream`` (default: torch's
-    current stream)."""
+    ``state_out`` may be ``state_in``. Returns (y, state_out); y has v's shape. Rows behind the last
+    packed sequence are zeros in a y made here, and left as they were in a given one. Asynchronous on
+    ``stream`` (default: torch's current stream)."""
     device = _gpu(q, "q", "gated_delta_scan")
     packed = lengths is not None or tables is not None
     if q.dim() != (3 if packed else 4) or v.dim() != q.dim():
@@ -239,7 +239,8 @@ def gated_delta_scan(q, k, v, dt_raw, beta_raw, A_log, dt_bias, *, dt_min=1e-4, 
         shape.state_slots = _pool(state_in, "state_in", (hv, V, K), device)
     with _on(device):
         mine = []
-        if y is None:
+        own_y = y is None
+        if own_y:
             y = torch.empty(v.shape, dtype=v.dtype, device=device)
             mine.append(y)
         else:
@@ -265,6 +266,10 @@ def gated_delta_scan(q, k, v, dt_raw, beta_raw, A_log, dt_bias, *, dt_min=1e-4, 
             _slots(out_slots, "out_slots", n, device), _ptr(workspace),
             workspace.numel() * workspace.element_size() if workspace is not None else 0,
             _handle(device, stream))
+        if st == _abi.AXON_OK and own_y and packed:
+            st = _lib().axon_clear_behind_sequences(n, lead[0], hv * V * y.element_size(),
+                                                    tables.buffer.data_ptr(), y.data_ptr(),
+                                                    _handle(device, stream))
     if st != _abi.AXON_OK:
         raise AxonError(st, "axon_gated_delta_scan")
     return y, state_out
@@ -274,8 +279,8 @@ def gated_delta_step(q, k, v, dt_raw, beta_raw, A_log, dt_bias, state, *, slots=
                      dt_max=100.0, scale=None, eps=1e-6, y=None, stream=None):
     """One token for each of B rows: q, k (B, Hk, K), v (B, Hv, V), dt_raw, beta_raw (B, Hv); the
     states (pool, Hv, V, K) float32 are updated in place, row b's at ``slots[b]`` (int32; default
-    b). A row whose slot lies outside the pool is idle: its y stays as it was. Returns y (B, Hv,
-    V)."""
+    b). A row whose slot lies outside the pool is idle: a given y stays as it was there, one made here
+    is zero. Returns y (B, Hv, V)."""
     device = _gpu(q, "q", "gated_delta_step")
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k, v must be (batch, heads, dim)")
@@ -288,6 +293,9 @@ def gated_delta_step(q, k, v, dt_raw, beta_raw, A_log, dt_bias, state, *, slots=
         if y is None:
             y = torch.empty(v.shape, dtype=v.dtype, device=device)
             _keep_for(device, stream, y)
+            if slots is not None:  # rows may be idle
+                with _NOTHING if stream is None else torch.cuda.stream(stream):
+                    y.zero_()
         else:
             _dense(y, "y", v.shape, v.dtype, device)
         st = _lib().axon_gated_delta_step(
