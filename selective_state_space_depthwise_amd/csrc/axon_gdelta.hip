@@ -621,7 +621,12 @@ __device__ __forceinline__ int swizzle(int t) {
 // The blocks of a lower triangular matrix as operands: row block, and pair of contraction blocks.
 constexpr int kLowerRow[6] = {0, 1, 2, 3, 2, 3}, kLowerCol[6] = {0, 0, 0, 0, 1, 1};
 
-constexpr int kOrdered = 1024;  // packed sequences that are put in order
+// Packed sequences that are put in order at most. Every workgroup ranks them all, so the cost grows
+// with the square of their number, and the gain is that of one long sequence left to run alone: 32
+// heads, lengths skewed, in order and as they lie, 24 of 1300 tokens in the mean 546 and 564 us, 48 of
+// 700 536 and 580 us, 64 of 500 531 and 548 us, 96 of 350 592 us both, 256 of 128 918 and 716 us; all of
+// 32 tokens, 64 115 and 100 us, 1024 7.8 and 1.4 ms.
+constexpr int kOrdered = 64;
 
 // LOCAL: the first walk over segments: no outputs; columns V .. V + K - 1 are the identity's.
 template <typename Act, int K, int W, int NC, bool LOCAL>
@@ -655,15 +660,15 @@ __global__ __launch_bounds__(64 * W, W == 4 && !LOCAL ? 1 : 2) void walk_kernel(
   int n = static_cast<int>(nk / a.hk);
   if (a.starts && a.sequences > 1 && a.sequences <= kOrdered) {
     // Packed sequences start in the order of their lengths, the longest first, so that no long one
-    // is left to run alone at the end. The n-th longest is found here: every thread compares some
-    // sequences with all others. (In the order of the buffer 24 sequences of 32768 tokens took
-    // 555 us instead of 506 us.)
+    // is left to run alone at the end. The n-th longest is found here: each of the first threads
+    // compares a sequence with all others.
+    static_assert(kOrdered <= kThreadsW, "a thread a sequence");
     int* const lens = reinterpret_cast<int*>(rs2[0]);
     int* const found = lens + kOrdered;
-    for (int j = threadIdx.x; j < a.sequences; j += kThreadsW)
-      lens[j] = a.block_starts[j + 1] - a.block_starts[j];
+    const int j = threadIdx.x;
+    if (j < a.sequences) lens[j] = a.block_starts[j + 1] - a.block_starts[j];
     __syncthreads();
-    for (int j = threadIdx.x; j < a.sequences; j += kThreadsW) {
+    if (j < a.sequences) {
       int before = 0;
       for (int o = 0; o < a.sequences; ++o) before += lens[o] > lens[j] || (lens[o] == lens[j] && o < j);
       if (before == n) *found = j;
