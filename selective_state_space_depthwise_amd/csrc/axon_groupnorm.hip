@@ -240,9 +240,10 @@ __global__ __launch_bounds__(THREADS) void norm_wide_kernel(NormArgs a) {
   const int grp = static_cast<int>(gi - row * a.groups);
   const int step = THREADS * VEC, first = threadIdx.x * VEC;
   float u[R * VEC], gz[R * VEC];
-  float s = 0.0f, mean = 0.0f;
+  float mean = 0.0f;
   Fetched<Act, VEC> f[R];
   if constexpr (HELD) {
+    float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const int c = j * step + first;
@@ -281,26 +282,29 @@ __global__ __launch_bounds__(THREADS) void norm_wide_kernel(NormArgs a) {
       }
     }
   } else {
+    // A thread adds up to 2^20 values here, often alike, where the roundings of an fp32 sum would not
+    // average out: its own part of a sum is held in 64 bits (8192 x 8201 bf16: 149 -> 151 us).
     if (a.centered) {
+      double sum = 0.0;
       for (int64_t c = first; c < a.width; c += step) {
         f[0].load(a, row, grp, static_cast<int>(c));
         f[0].get(a, u, gz);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s += u[e];
+        for (int e = 0; e < VEC; ++e) sum += u[e];
       }
-      mean = reduce_wg<THREADS>(s, part) * a.inv_width;
+      mean = reduce_wg<THREADS>(static_cast<float>(sum), part) * a.inv_width;
     }
-    float q = 0.0f;
+    double q = 0.0;
     for (int64_t c = first; c < a.width; c += step) {
       f[0].load(a, row, grp, static_cast<int>(c));
       f[0].get(a, u, gz);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float d = u[e] - mean;
-        q = fmaf(d, d, q);
+        q += static_cast<double>(d) * d;
       }
     }
-    const float rs = 1.0f / sqrtf(reduce_wg<THREADS>(q, part) * a.inv_width + a.eps);
+    const float rs = 1.0f / sqrtf(reduce_wg<THREADS>(static_cast<float>(q), part) * a.inv_width + a.eps);
     // In place a thread overwrites only what it alone reads in this pass; the passes before it
     // ended at the barriers of the sums.
     for (int64_t c = first; c < a.width; c += step) {
