@@ -345,7 +345,10 @@ axon_status axon_clear_behind_sequences(int64_t sequences, int64_t total_tokens,
  * 64 tokens on the matrix cores: with g the inclusive sum of dt A inside the chunk and S0 the
  * entering state, D = T (v - e^g S0 k^), T = (I + M)^-1 diag(beta), M[t,s] = beta_t e^(g_t - g_s)
  * k^_t.k^_s for s < t, are the chunk's corrected writes. axon_gated_delta_step is the recurrence
- * itself for one token a row. All sums, decays and states are fp32.
+ * itself for one token a row. All sums, decays and states are fp32. The scan's products are off by
+ * about 2^-23 of the largest entry of their row or column in a chunk, so that errors are relative to
+ * the largest entries of a state's row (and of v's column) in a chunk, not to each. Squares of a row
+ * of q or k must not sum beyond the range of fp32.
  *
  * Layouts: q, k (tokens, key_heads, K); v (tokens, value_heads, V); dt_raw, beta_raw
  * (tokens, value_heads); y (tokens, value_heads, V); activation dtype. The rows of q, k and v may

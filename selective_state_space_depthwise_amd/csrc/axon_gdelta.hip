@@ -35,9 +35,11 @@
 //                without leaving their lanes.
 //
 // Precision. fp32 products would run at a sixteenth of the fp16 matrix rate, so the walk splits
-// each fp32 operand into two fp16 pieces, x = hi + lo: 22 bits of x, and 2^-25 of one at least. A
-// product of pieces (hi hi + hi lo + lo hi) is then as exact as an fp32 one if the operands lie near
-// one: T and A are at most 1; rows of k and q are scaled by a power of two that takes their largest
+// each fp32 operand into two fp16 pieces, x = hi + lo: off by 2^-23 of x at most, or by 2^-25 where x
+// is below a quarter; of a product of pieces lo lo is left out (hi hi + hi lo + lo hi). If the largest
+// operands of a sum lie near one, that is nearly what fp32 gives (2 x 2048 tokens against 64 bits: 4.2e-7
+// in the mean, the plain form in fp32 2.7e-7), relative to the largest and not to each: T and A are at
+// most 1; rows of k and q are scaled by a power of two that takes their largest
 // entry to [1, 2) (bf16 entries are then exact in one piece); each column of S, with what the chunk
 // makes of its v (X, E and the writes), is kept in a unit of its own, a power of two that takes the
 // larger of S and v to about 2^5. By the contraction of the delta rule (0 <= beta <= 1) no entry of
@@ -45,7 +47,8 @@
 // nothing leaves the range of fp16. The states, every accumulator and every factor are fp32. This
 // holds for bf16 activations too, the operands that only y sees among them: y is what fp32 gives,
 // rounded once. (With S, A and E of y's products in one piece, 2^-11, a value in twenty of y came out
-// as another bf16 number; 16384 tokens took 406 us and 32768 packed ones 487 us.)
+// as another bf16 number; 16384 tokens took 406 us instead of 438 us, 32768 packed ones 487 us instead
+// of 537 us.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -325,9 +328,9 @@ __device__ __forceinline__ float max4(float m, f4 x) {
 // are inverted by one wave, block g by lane group g, a column a lane. From T (I + M) = I the blocks
 // below follow row by row: T_IJ = (sum_{J < S <= I} T_IS (-M)_SJ) D_J with D_J the inverse of
 // diagonal block J; one wave takes row block 3 of a head (9 products), another its rows 2 and 1 (7).
-// 32768 tokens x 16 key and 32 value heads, bf16: 155 us for 0.56 GB read and written (3.6 TB/s); the
+// 32768 tokens x 16 key and 32 value heads, bf16: 167 us for 0.53 GB read and written (3.2 TB/s); the
 // phases of a workgroup wait for each other, four workgroups a CU fill most of that. (Five spill
-// registers: the scan takes 3% longer. Records stored past the caches: no change.)
+// registers: the scan takes 5% longer. Records stored past the caches: no change.)
 constexpr int kHeads = 2;      // value heads at a time
 constexpr int kBlockRow = 20;  // floats between the rows of a block in LDS
 
@@ -599,8 +602,8 @@ __global__ __launch_bounds__(kThreads, sizeof(Act) == 2 ? 4 : 3) void prep_kerne
 
 // ---- the walk over the chunks -------------------------------------------------------------------
 // Bound by a chunk's chain of dependent products and the LDS reads and conversions that feed them:
-// 32768 packed tokens x 32 heads, bf16, K = V = 128: 333 us, of a CU's about 9800 clocks a chunk the
-// matrix cores are busy for a third, the vector units for half.
+// 32768 packed tokens x 32 heads, bf16, K = V = 128: 371 us, of a CU's about 11700 clocks a chunk the
+// matrix cores are busy for 4200, the vector units for 5400.
 // W waves a workgroup, each with NC tiles of 16 columns of V of one head (two in the first walk over
 // segments of bf16, which has no outputs to sum). Per chunk the workgroup brings k and q, converted to
 // fp16 pieces on the way, as rows of K fp16 (read as left operand of S k^ and S q^, and k by
@@ -930,8 +933,8 @@ __global__ __launch_bounds__(64 * W, W == 4 && !LOCAL ? 1 : 2) void walk_kernel(
     // k and q have the whole chunk's time to arrive, where their registers fit.
     if (NC == 1 && P == 1) load(next);
     // A SIMD's waves serve a chunk together; the one that is behind goes first (its priority falls
-    // from phase to phase), so that they reach the barrier together: 346 -> 333 us for 32768 packed
-    // tokens.
+    // from phase to phase), so that they reach the barrier together: 32768 packed tokens 535 -> 529 us,
+    // 16384 of one sequence 455 -> 439 us.
     __builtin_amdgcn_s_setprio(3);
     f4 X[NC][4], O[NC][4];
 #pragma unroll
@@ -1171,7 +1174,7 @@ __global__ __launch_bounds__(64 * W, W == 4 && !LOCAL ? 1 : 2) void walk_kernel(
 // after segment S <- S M + N, transposed as in the walk, with M^T in LDS in operand order (the next
 // segment's on its way meanwhile). N's place takes the state before the segment: the second walk
 // reads no other, so that the last segment may write the state in place. Bound by the latency of a
-// step (about 6 us: M and N arrive, 192 products a wave and its LDS reads); 44 us for 8 segments.
+// step (about 7 us: M and N arrive, 192 products a wave and its LDS reads); 48 us for 8 segments.
 template <int K>
 __global__ __launch_bounds__(kThreads) void join_kernel(DeltaArgs a) {
   constexpr int NB = K / 16, KB = K / 32, NC = 2;
@@ -1325,8 +1328,9 @@ __global__ __launch_bounds__(kThreads) void join_kernel(DeltaArgs a) {
 // ---- one token a row ----------------------------------------------------------------------------
 // Bound by reading and writing the states. K / 16 lanes hold a row of the state (16 values each, as
 // four float4 spaced so that a load's lanes read whole 64 or 128 byte pieces); a wave passes over R
-// times its 64 / lanes rows, all loaded before the first is used. 64 rows x 32 heads x 128 x 128:
-// 43 us, 6.2 TB/s; 512 rows: 326 us, 6.6 TB/s.
+// times its 64 / lanes rows, all loaded before the first is used. 56 rows x 32 heads x 128 x 128 (and 8
+// idle ones, which read and write nothing): 43 us, 5.5 TB/s; 448 rows (and 64): 326 us, 5.8 TB/s. A
+// scaling of 512 MB in place reaches 6.1 TB/s.
 struct StepArgs {
   const void *q, *k, *v, *dt_raw, *beta_raw;
   const float *A_log, *dt_bias;
@@ -1489,7 +1493,8 @@ struct ScanPlan {
 
 // Workspace and segments from the shape alone. Sequences are split where their heads leave most of
 // the 256 CUs idle (a workgroup a head) and they are long enough for it to pay: at 32 heads 16384
-// tokens take 0.42 ms in 8 segments and 0.98 ms in one.
+// tokens take 0.44 ms in 8 segments and 1.10 ms in one. Only the mean length is known here, so that a
+// long sequence packed with short ones may be walked whole.
 ScanPlan plan_scan(const axon_gated_delta_shape* s) {
   ScanPlan p;
   if (!s->tokens) return p;
@@ -1548,7 +1553,8 @@ void launch_scan(DeltaArgs a, bool any, hipStream_t st) {
     hipLaunchKernelGGL(kernel, dim3(unsigned(wgs)), dim3(64 * waves), 0, st, b);
   };
   if (split) {
-    // (bf16 with eight waves of one tile: 217 us against 187 us at 32 heads and 16384 tokens.)
+    // (bf16 with eight waves of one tile: the scan takes 470 us against 439 us at 32 heads and 16384
+    // tokens.)
     if constexpr (kPieces<Act> == 1)
       go(walk_kernel<Act, K, 4, 2, true>, 4, 2, a.value_dim + K);
     else
@@ -1575,7 +1581,7 @@ void launch_step(StepArgs a, hipStream_t st) {
   const bool wide = heads * w4 >= 2048;
   a.waves_per_head = wide ? w4 : (a.value_dim + RW - 1) / RW;
   const unsigned wgs = static_cast<unsigned>((heads * a.waves_per_head + 3) / 4);
-  // A layer's states stream where those of a model's layers together pass the 256 MB cache (512 rows
+  // A layer's states stream where those of a model's layers together pass the 256 MB cache (448 rows
   // x 32 heads: 327 us against 355 us; 56 rows, states of three calls in turn: 45 us against 48 us,
   // of one call again and again 43 us against 38 us).
   const bool stream = heads * a.value_dim * K * 4 > (int64_t(16) << 20);
