@@ -72,7 +72,8 @@ template <typename Act>
 constexpr int kPieces = sizeof(Act) == 2 ? 1 : 2;
 
 // What prep leaves for each (chunk, value head): T and A in two pieces, each as ten 16 x 16 blocks
-// on and below the diagonal (at block_at), a block as 64 lanes x 4 fp16 in left-operand order (lane (g, i): row i, columns 4 g .. 4 g + 3); then the row
+// on and below the diagonal (at block_at), a block as 64 lanes x 4 fp16 in left-operand order (lane
+// (g, i): row i, columns 4 g .. 4 g + 3); then the row
 // factors of the 64 tokens, fp32, and e^{g_last} with its base-2 logarithm. What the walk keeps in
 // LDS comes first.
 constexpr int kBlocks = 10;

@@ -223,9 +223,9 @@ def gated_delta_scan(q, k, v, dt_raw, beta_raw, A_log, dt_bias, *, dt_min=1e-4, 
         if tables.block != DELTA_CHUNK or tables.total_tokens != lead[0]:
             raise ValueError(f"tables are for {tables.total_tokens} tokens in blocks of "
                              f"{tables.block}, expected {lead[0]} in blocks of {DELTA_CHUNK}")
-        if tables.buffer.device != device:
-            raise ValueError(f"tables are on {tables.buffer.device}, expected {device}")
         n = tables.sequences
+        _dense(tables.buffer, "tables.buffer", (2 * (2 * n + 1 + lead[0] // DELTA_CHUNK),), torch.int32,
+               device)
     elif lengths is not None:
         if not isinstance(lengths, torch.Tensor) or lengths.device != device:
             raise ValueError(f"lengths must be a tensor on {device}")

@@ -97,3 +97,20 @@ def test_clear(total, row, end):
     first = min(max(end, 0), total) * row
     assert bool((x[:first] == 5).all()) and bool((x[first:total * row] == 0).all())
     assert bool((x[total * row:] == 5).all())
+
+
+@pytest.mark.parametrize("what", ["short", "long", "type", "host", "spread", "more sequences"])
+def test_refused_tables(what):
+    """Tables whose buffer is not what the kernels read from are refused before any launch."""
+    axon = _axon()
+    d = make((100,), 1, 2, 64, 48, "f32", seed=1)
+    good = axon.sequence_tables(torch.tensor([60, 40], dtype=torch.int32).cuda(), 100)
+    torch.cuda.synchronize()
+    b, n = good.buffer, 2
+    if what == "more sequences":
+        n = 3
+    else:
+        b = {"short": b[:-1], "long": torch.cat([b, b[:1]]), "type": b.long(), "host": b.cpu(),
+             "spread": b.repeat_interleave(2)[::2]}[what]
+    with pytest.raises((TypeError, ValueError)):
+        axon.gated_delta_scan(**d, tables=axon.SequenceTables(b, n, 100, 64))
