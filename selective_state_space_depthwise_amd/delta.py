@@ -238,7 +238,8 @@ def gated_delta_scan(q, k, v, dt_raw, beta_raw, A_log, dt_bias, *, dt_min=1e-4, 
     if state_in is not None:
         shape.state_slots = _pool(state_in, "state_in", (hv, V, K), device)
     with _on(device):
-        mine = []
+        # The tables' buffer is the binding's too, on whatever stream they were built.
+        mine = [] if tables is None else [tables.buffer]
         own_y = y is None
         if own_y:
             y = torch.empty(v.shape, dtype=v.dtype, device=device)

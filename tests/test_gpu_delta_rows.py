@@ -114,3 +114,26 @@ def test_refused_tables(what):
              "spread": b.repeat_interleave(2)[::2]}[what]
     with pytest.raises((TypeError, ValueError)):
         axon.gated_delta_scan(**d, tables=axon.SequenceTables(b, n, 100, 64))
+
+
+def test_tables_dropped_while_in_use():
+    """Tables built on one stream, used on another that is behind, and dropped: their memory is not
+    handed out again before the scan has read it."""
+    axon = _axon()
+    total, lengths = 6400, [3000, 0, 3400]
+    d = make((total,), 1, 2, 64, 48, "bf16", seed=3)
+    n = torch.tensor(lengths, dtype=torch.int32).cuda()
+    y0, s0 = axon.gated_delta_scan(**d, lengths=n)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    tables = axon.sequence_tables(n, total)
+    size = tables.buffer.numel()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    y, s = axon.gated_delta_scan(**d, tables=tables, stream=side)
+    del tables
+    others = [torch.full((size,), -1, dtype=torch.int32, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(y, y0) and torch.equal(s, s0)
+    assert all(bool((t == -1).all()) for t in others)
