@@ -459,6 +459,207 @@ typedef struct {
 axon_status axon_group_norm(const axon_group_norm_desc* desc, const void* x, const void* z,
                             const float* weight, const float* bias, void* y, void* stream);
 
+/* ---- Gated linear recurrence -------------------------------------------------------------------
+ * One state a channel, with a decay and an input that are gated by the token. For every sequence and
+ * channel e, per token:
+ *
+ *   dt    = sigmoid(dt_raw + dt_bias[e])   (AXON_LINEAR_SIGMOID), or softplus(..) (AXON_LINEAR_SOFTPLUS)
+ *   log a = -exp(A_log[e]) dt
+ *   u     = x sigmoid(in_raw + in_bias[e]), or x where in_raw is NULL
+ *   h    <- a h + m u,  m = 1 (AXON_INPUT_PLAIN), 1 - a (AXON_INPUT_COMPLEMENT),
+ *                           sqrt(1 - a^2) (AXON_INPUT_SQRT)
+ *   y     = h
+ *
+ * (With softplus, A_log = 0 and the complement, a = 1 - z and m = z for the gate z = sigmoid(dt_raw
+ * + dt_bias).) Gates, decays and states are fp32, y is rounded once; h is advanced by expm1(log a)
+ * where a >= 1/2, so that slow decays lose nothing to the rounding of a.
+ *
+ * Layouts: x, dt_raw, in_raw, y (tokens, channels), activation dtype; the rows of x, dt_raw, in_raw
+ * and dy may lie x_stride, dt_stride, in_stride, dy_stride elements apart (0 = dense, else at least
+ * `channels`); y and the gradients are dense. A_log, dt_bias, in_bias (channels) fp32; the biases
+ * may be NULL (zeros). Pools of states (slots, channels) fp32. Sequences (a uniform batch, or packed
+ * with tables of block 64) and slots as for axon_gated_delta_scan. Activations need the alignment of an element only, fp32
+ * and integer arrays 4-byte.
+ * Limits: sequences in [1, 65535]; channels in [1, 2^22]; tokens < 2^29; strides up to 2^22; tokens *
+ * stride and slots * channels <= 2^40; (tokens / 64 + sequences) * channels < 2^37.
+ *
+ * A value that is not finite in a token's x, dt_raw or in_raw makes its channel's state not finite
+ * from there on, unless a gate has an infinity, where it is the gate's limit. No other channel or
+ * sequence sees it. */
+enum { AXON_LINEAR_SIGMOID = 0, AXON_LINEAR_SOFTPLUS = 1 };
+enum { AXON_INPUT_PLAIN = 0, AXON_INPUT_COMPLEMENT = 1, AXON_INPUT_SQRT = 2 };
+
+typedef struct {
+  int64_t sequences;    /* batch rows, or packed sequences; the step's rows */
+  int64_t tokens;       /* rows of x: sequences * seqlen, or the packed buffer's rows */
+  int64_t channels;     /* E */
+  int64_t x_stride;     /* elements between rows; 0 = dense */
+  int64_t dt_stride;
+  int64_t in_stride;
+  int64_t dy_stride;    /* read by the backward pass only */
+  int64_t state_slots;  /* states of the pool state_in (of the step's pool); not read by the backward pass */
+  int64_t out_slots;    /* states of the pool state_out; not read by the step and the backward pass */
+  int32_t act_dtype;    /* an axon_dtype value */
+  int32_t gate;         /* AXON_LINEAR_* */
+  int32_t input_scale;  /* AXON_INPUT_* */
+  int32_t clear_behind; /* 1: rows of y behind the last sequence get zeros; 0: they are left as they
+                           were. Read by the scan only */
+} axon_linear_shape;
+
+typedef struct {
+  const float* A_log;    /* (channels) */
+  const float* dt_bias;  /* (channels) or NULL */
+  const float* in_bias;  /* (channels) or NULL; not read where in_raw is NULL */
+} axon_linear_params;
+
+/* Rows of `checkpoints`: blocks of 64 tokens that sequences of these tokens can have, packed
+ * (tokens / 64 + sequences) or uniform. 0 for invalid arguments. */
+size_t axon_linear_checkpoint_rows(int64_t sequences, int64_t tokens, int32_t packed);
+
+/* Bytes of device workspace axon_linear_scan needs (0 for an invalid shape; 0 is possible). */
+size_t axon_linear_scan_workspace_bytes(const axon_linear_shape* shape);
+
+/* Runs every sequence. tables, state_in, in_slots, state_out, out_slots and workspace as for
+ * axon_gated_delta_scan, with the same rules of aliasing. checkpoints: NULL, or
+ * (axon_linear_checkpoint_rows, channels) fp32, which receives the state that enters each block of
+ * 64 tokens, for the backward pass (rows of blocks that no sequence has are left as they were). */
+axon_status axon_linear_scan(const axon_linear_shape* shape, const axon_linear_params* params,
+                             const void* x, const void* dt_raw, const void* in_raw,
+                             const int32_t* tables, const float* state_in, const int32_t* in_slots,
+                             void* y, float* state_out, const int32_t* out_slots,
+                             float* checkpoints, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Bytes of device workspace axon_linear_scan_backward needs (0 for an invalid shape). */
+size_t axon_linear_scan_backward_workspace_bytes(const axon_linear_shape* shape);
+
+/* Gradients of axon_linear_scan: from dy (tokens, channels) and dstate_out (sequences, channels; the
+ * gradient of each sequence's final state, NULL = zeros), with the inputs, tables and checkpoints of
+ * the forward call, to
+ *   dx, ddt_raw, din_raw (tokens, channels) activation dtype; zeros behind the last sequence
+ *   dA_log, ddt_bias, din_bias (channels) fp32, summed over all tokens in an order of their own that
+ *       does not change from call to call
+ *   dstate_in (sequences, channels) fp32; NULL = not stored
+ * din_raw and din_bias belong to in_raw: all three or none. Where m = sqrt(1 - a^2) is 0 the gradient
+ * of its input term is taken as 0 (its limit for the gate). Outputs overlap nothing. */
+axon_status axon_linear_scan_backward(const axon_linear_shape* shape,
+                                      const axon_linear_params* params, const void* dy,
+                                      const void* x, const void* dt_raw, const void* in_raw,
+                                      const int32_t* tables, const float* checkpoints,
+                                      const float* dstate_out, void* dx, void* ddt_raw,
+                                      void* din_raw, float* dA_log, float* ddt_bias,
+                                      float* din_bias, float* dstate_in, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* One token for each of `sequences` rows (tokens == sequences), states updated in place. A row whose
+ * slot lies outside the pool is idle: its y stays as it was and no state is touched. */
+axon_status axon_linear_step(const axon_linear_shape* shape, const axon_linear_params* params,
+                             const void* x, const void* dt_raw, const void* in_raw, float* state,
+                             const int32_t* slots, void* y, void* stream);
+
+/* ---- Causal depthwise convolution --------------------------------------------------------------
+ * The convolution in front of a scan, by itself: for every sequence and channel e
+ *
+ *   p_t = conv_b[e] + sum_k conv_w[e,k] xx[t - 3 + k],  k = 0 .. 3
+ *   y_t = p_t, or SiLU(p_t) (AXON_CONV_SILU)
+ *
+ * xx[s] is x for s >= 0 and the sequence's cache (its last three inputs, oldest first) for s < 0, as in
+ * axon_ssm_prefill. Layouts: x, y (tokens, channels), activation dtype, the rows of x and dy x_stride,
+ * dy_stride elements apart (0 = dense); conv_w (channels, 4), conv_b (channels, or NULL = zeros)
+ * fp32; pools of caches (slots, 3, channels) fp32. Sums are fp32 and rounded once. Sequences, tables
+ * (block 64), slots, alignment and limits as for axon_linear_scan (slots * 3 * channels <= 2^40). */
+typedef struct {
+  int64_t sequences;
+  int64_t tokens;
+  int64_t channels;
+  int64_t x_stride;
+  int64_t dy_stride;    /* read by the backward pass only */
+  int64_t cache_slots;  /* caches of the pool cache_in (of the step's pool); not read by the backward pass */
+  int64_t out_slots;    /* caches of the pool cache_out; read by the forward pass only */
+  int32_t act_dtype;
+  int32_t activation;   /* AXON_CONV_NONE or AXON_CONV_SILU */
+  int32_t clear_behind; /* as in axon_linear_shape */
+} axon_conv_shape;
+
+/* cache_in NULL: zeros. cache_out NULL: not stored. cache_out may equal cache_in (then with as many
+ * slots) but must not overlap it otherwise; outputs overlap nothing else. A sequence without tokens
+ * copies its cache. The cache holds exact copies of the inputs. */
+axon_status axon_causal_conv(const axon_conv_shape* shape, const void* x, const float* conv_w,
+                             const float* conv_b, const int32_t* tables, const float* cache_in,
+                             const int32_t* in_slots, void* y, float* cache_out,
+                             const int32_t* out_slots, void* stream);
+
+/* Bytes of device workspace axon_causal_conv_backward needs (0 for an invalid shape). */
+size_t axon_causal_conv_backward_workspace_bytes(const axon_conv_shape* shape);
+
+/* Gradients of axon_causal_conv from dy (tokens, channels) and dcache_out (sequences, 3, channels, or
+ * NULL = zeros), with the inputs of the forward call; cache_in is (sequences, 3, channels) or NULL.
+ * dx (tokens, channels), zeros behind the last sequence; dconv_w (channels, 4), dconv_b (channels)
+ * fp32, summed in an order that does not change from call to call; dcache_in (sequences, 3,
+ * channels) or NULL. Outputs overlap nothing. */
+axon_status axon_causal_conv_backward(const axon_conv_shape* shape, const void* dy, const void* x,
+                                      const float* conv_w, const float* conv_b,
+                                      const int32_t* tables, const float* cache_in,
+                                      const float* dcache_out, void* dx, float* dconv_w,
+                                      float* dconv_b, float* dcache_in, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* One token for each of `sequences` rows (tokens == sequences), caches updated in place; idle rows as
+ * in axon_linear_step. */
+axon_status axon_causal_conv_step(const axon_conv_shape* shape, const void* x, const float* conv_w,
+                                  const float* conv_b, float* cache, const int32_t* slots, void* y,
+                                  void* stream);
+
+/* ---- Head norm with position rotation ----------------------------------------------------------
+ * Queries and keys before attention or before axon_gated_delta_scan: every head of head_dim D
+ * channels is normalised and its first rotary_dim R channels are turned by the token's position, in
+ * one pass over both tensors. Per row (token) with position p and head:
+ *
+ *   n = x / sqrt(mean(x^2) + eps) w
+ *   (n_i, n_j) <- (n_i cos - n_j sin, n_j cos + n_i sin) of the angle p freqs[c],  c = 0 .. R / 2 - 1
+ *
+ * where pair c is (c, c + R / 2), or (2 c, 2 c + 1) with `interleaved`. Angles are reduced in 64 bits,
+ * so that far positions lose nothing; sums and products are fp32 and rounded once.
+ *
+ * q (rows, q_heads, D), k (rows, k_heads, D; k_heads = 0: none), activation dtype, rows q_stride /
+ * k_stride elements apart (0 = dense, else at least heads * D); outputs dense. positions (rows) int32,
+ * any sign; freqs (R / 2) fp64, radians a token; weights (D) fp32 or NULL (ones). q_out may equal q
+ * (and k_out k) where that is dense, else outputs overlap nothing.
+ * Limits: D even, in [2, 256]; R even, in [2, D]; q_heads in [1, 65535], k_heads in [0, 65535]; rows
+ * < 2^31; strides up to 2^31; rows * stride <= 2^40. Activations need the alignment of an element
+ * only, fp32 and int32 arrays 4-byte, freqs 8-byte. Squares of a head must not sum beyond fp32. */
+typedef struct {
+  int64_t rows;
+  int64_t q_heads;
+  int64_t k_heads;
+  int64_t head_dim;     /* D */
+  int64_t rotary_dim;   /* R */
+  int64_t q_stride;     /* elements between the rows of q; 0 = dense */
+  int64_t k_stride;
+  int64_t dq_stride;    /* of the output gradients; read by the backward pass only */
+  int64_t dk_stride;
+  float eps;            /* finite, >= 0 */
+  int32_t act_dtype;
+  int32_t interleaved;  /* 0 or 1 */
+} axon_norm_rotate_desc;
+
+axon_status axon_norm_rotate(const axon_norm_rotate_desc* desc, const void* q, const void* k,
+                             const int32_t* positions, const double* freqs, const float* q_weight,
+                             const float* k_weight, void* q_out, void* k_out, void* stream);
+
+/* Bytes of device workspace axon_norm_rotate_backward needs (0 for an invalid desc or no rows). */
+size_t axon_norm_rotate_backward_workspace_bytes(const axon_norm_rotate_desc* desc);
+
+/* Gradients from dq_out, dk_out (rows, heads, D) with the inputs of the forward call: dq, dk dense,
+ * activation dtype; dq_weight, dk_weight (D) fp32, each NULL = not wanted, summed in an order that does
+ * not change from call to call. dq may equal a dense dq_out (dk dk_out); else outputs overlap nothing. */
+axon_status axon_norm_rotate_backward(const axon_norm_rotate_desc* desc, const void* dq_out,
+                                      const void* dk_out, const void* q, const void* k,
+                                      const int32_t* positions, const double* freqs,
+                                      const float* q_weight, const float* k_weight, void* dq,
+                                      void* dk, float* dq_weight, float* dk_weight,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

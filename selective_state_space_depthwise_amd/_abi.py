@@ -87,6 +87,33 @@ class GroupNormDesc(ctypes.Structure):
                 ("gate", ctypes.c_int32), ("shared_weights", ctypes.c_int32)]
 
 
+class LinearShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "sequences", "tokens", "channels", "x_stride", "dt_stride", "in_stride", "dy_stride",
+        "state_slots", "out_slots")] + [(n, ctypes.c_int32) for n in (
+            "act_dtype", "gate", "input_scale", "clear_behind")]
+
+
+class LinearParams(ctypes.Structure):
+    _fields_ = [("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+                ("in_bias", ctypes.c_void_p)]
+
+
+class ConvShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "sequences", "tokens", "channels", "x_stride", "dy_stride", "cache_slots",
+        "out_slots")] + [(n, ctypes.c_int32) for n in ("act_dtype", "activation", "clear_behind")]
+
+
+class NormRotateDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "rows", "q_heads", "k_heads", "head_dim", "rotary_dim", "q_stride", "k_stride",
+        "dq_stride", "dk_stride")] + [("eps", ctypes.c_float), ("act_dtype", ctypes.c_int32),
+                                      ("interleaved", ctypes.c_int32)]
+
+
+LINEAR_GATES = {"sigmoid": 0, "softplus": 1}
+LINEAR_INPUT_SCALES = {"none": 0, "complement": 1, "sqrt": 2}
 NORM_ACTIVATIONS = {"none": 0, "silu": 1}
 NORM_GATES = {"none": 0, "before": 1, "after": 2}
 CONV_ACTIVATIONS = {"none": 0, "silu": 1}
@@ -163,6 +190,36 @@ def load():
             P, P, P, P, P, P, P, P, P]
         lib.axon_group_norm.restype = ctypes.c_int
         lib.axon_group_norm.argtypes = [ctypes.POINTER(GroupNormDesc), P, P, P, P, P, P]
+        Z = ctypes.c_size_t
+        linear = [ctypes.POINTER(LinearShape), ctypes.POINTER(LinearParams)]
+        lib.axon_linear_checkpoint_rows.restype = Z
+        lib.axon_linear_checkpoint_rows.argtypes = [I, I, ctypes.c_int32]
+        lib.axon_linear_scan_workspace_bytes.restype = Z
+        lib.axon_linear_scan_workspace_bytes.argtypes = linear[:1]
+        lib.axon_linear_scan.restype = ctypes.c_int
+        lib.axon_linear_scan.argtypes = linear + [P] * 11 + [Z, P]
+        lib.axon_linear_scan_backward_workspace_bytes.restype = Z
+        lib.axon_linear_scan_backward_workspace_bytes.argtypes = linear[:1]
+        lib.axon_linear_scan_backward.restype = ctypes.c_int
+        lib.axon_linear_scan_backward.argtypes = linear + [P] * 15 + [Z, P]
+        lib.axon_linear_step.restype = ctypes.c_int
+        lib.axon_linear_step.argtypes = linear + [P] * 7
+        conv = [ctypes.POINTER(ConvShape)]
+        lib.axon_causal_conv.restype = ctypes.c_int
+        lib.axon_causal_conv.argtypes = conv + [P] * 10
+        lib.axon_causal_conv_backward_workspace_bytes.restype = Z
+        lib.axon_causal_conv_backward_workspace_bytes.argtypes = conv
+        lib.axon_causal_conv_backward.restype = ctypes.c_int
+        lib.axon_causal_conv_backward.argtypes = conv + [P] * 12 + [Z, P]
+        lib.axon_causal_conv_step.restype = ctypes.c_int
+        lib.axon_causal_conv_step.argtypes = conv + [P] * 7
+        rotate = [ctypes.POINTER(NormRotateDesc)]
+        lib.axon_norm_rotate.restype = ctypes.c_int
+        lib.axon_norm_rotate.argtypes = rotate + [P] * 9
+        lib.axon_norm_rotate_backward_workspace_bytes.restype = Z
+        lib.axon_norm_rotate_backward_workspace_bytes.argtypes = rotate
+        lib.axon_norm_rotate_backward.restype = ctypes.c_int
+        lib.axon_norm_rotate_backward.argtypes = rotate + [P] * 13 + [Z, P]
         _lib = lib
         return lib
 

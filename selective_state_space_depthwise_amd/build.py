@@ -23,7 +23,7 @@ MICRO_LIB = os.path.join(PKG, "libaxonmicro.so")
 
 HIP_SOURCES = ["axon_kernels.hip", "axon_rowscan.hip", "axon_chanscan.hip", "axon_layer.hip",
                "axon_ssd.hip", "axon_noalloc.hip", "axon_seqtables.hip", "axon_gdelta.hip",
-               "axon_groupnorm.hip"]
+               "axon_groupnorm.hip", "axon_linear.hip", "axon_conv.hip", "axon_rotate.hip"]
 CXX_SOURCES = ["axonscan_api.cpp"]
 ARCH = "gfx950"
 ROCM_LIB = "/opt/rocm/lib"  # hipBLASLt (the layer's projection GEMMs)
