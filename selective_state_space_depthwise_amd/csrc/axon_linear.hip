@@ -19,12 +19,15 @@
 namespace axon {
 namespace {
 
+constexpr int kPer = 16;  // tokens of a wave
+
 struct LinearArgs {
   const void *x, *dt_raw, *in_raw, *dy;
   const float *A_log, *dt_bias, *in_bias;
   Packed p;
   int64_t x_stride, dt_stride, in_stride, dy_stride;
   int channels, gate, input_scale, clear_behind;
+  int tiles, groups;  // tiles of blocks, groups of 64 channels
   // scan, step
   const float* state_in;
   const int32_t *in_slots, *out_slots;
@@ -35,18 +38,15 @@ struct LinearArgs {
   const float *points, *dstate_out;
   void *dx, *ddt_raw, *din_raw;
   float *dA_log, *ddt_bias, *din_bias, *dstate_in;
-  float* partial;  // (sequences, 3, channels)
+  float* partial;  // (tiles, 3, channels)
+  // What tiles tell each other (tiles, 64 groups): all bits set where nothing is told yet.
+  uint32_t* ticket;  // null: one tile
+  uint64_t* sums;    // decay and own part of a tile
+  uint32_t* carry;   // what leaves it
 };
 
-// expm1(v) for v <= 0 (and NaN). Below -1/4 exp(v) - 1 cancels two bits at most; above it the series
-// up to v^6 / 720 leaves a relative 5e-8.
-__device__ __forceinline__ float expm1_neg(float v, float e) {
-  float p = fmaf(v, 1.0f / 720.0f, 1.0f / 120.0f);
-  p = fmaf(v, p, 1.0f / 24.0f);
-  p = fmaf(v, p, 1.0f / 6.0f);
-  p = fmaf(v, p, 0.5f);
-  p = fmaf(v * v, p, v);
-  return v > -0.25f ? p : e - 1.0f;
+__device__ __forceinline__ float sigmoid_f32(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
 }
 
 // sigmoid(v) and 1 - sigmoid(v), each with a relative error of a few 2^-24.
@@ -60,137 +60,486 @@ struct Sigmoid {
   }
 };
 
-// What a token's gate makes of its channel: log a, a, expm1(log a), m.
+// How a token advances its state, in one number: a itself where a < 1/2, else expm1(log a) with the sign
+// bit set (also where it is zero). For a >= 1/2 the rounding of a would be a systematic error of the
+// decay, 2^-25 against 1 - a; below, h + expm1(log a) h would lose b beside a larger h.
+__device__ __forceinline__ float advance(float c, float h, float b) {
+  return fmaf(c, h, b) + (__float_as_int(c) < 0 ? h : 0.0f);
+}
+constexpr uint32_t kKeep = 0x80000000u;  // a = 1
+
+// softplus, NaN kept.
+__device__ __forceinline__ float softplus_nan(float v) { return v != v ? v : softplus_f32(v); }
+
+// a token's decay from its log a in base 2 (<= 0): expm1(log a) and the number that advance takes.
+// Below log2 a = -0.36, a - 1 cancels two bits at most; above it the series up to (log a)^6 / 720 leaves
+// a relative 5e-8.
 struct Decay {
-  float L, a, em1, m;
-  __device__ __forceinline__ Decay(float v, float rate, int gate, int input_scale) {
-    L = -rate * (gate == AXON_LINEAR_SIGMOID ? Sigmoid(v).on : softplus_f32(v));
-    if (v != v) L = v;
-    a = __builtin_amdgcn_exp2f(L * kLog2e);
-    em1 = expm1_neg(L, a);
-    m = input_scale == AXON_INPUT_PLAIN ? 1.0f
-        : input_scale == AXON_INPUT_COMPLEMENT
-            ? -em1
-            : __builtin_amdgcn_sqrtf(-em1 * (2.0f + em1));
-  }
-  // a h + b. For a >= 1/2 the rounding of a would be a systematic error of the decay, 2^-25 against
-  // 1 - a; below, h + expm1(log a) h would lose b beside a larger h.
-  __device__ __forceinline__ float advance(float h, float b) const {
-    return a < 0.5f ? fmaf(a, h, b) : h + fmaf(em1, h, b);
+  float em1, c;
+  __device__ __forceinline__ explicit Decay(float l2) {
+    const float a = __builtin_amdgcn_exp2f(l2);
+    float p = fmaf(l2, 1.54035304e-4f, 1.33335581e-3f);
+    p = fmaf(l2, p, 9.61812911e-3f);
+    p = fmaf(l2, p, 5.55041087e-2f);
+    p = fmaf(l2, p, 2.40226507e-1f);
+    p = fmaf(l2, p, 6.93147181e-1f) * l2;
+    em1 = l2 > -0.36f ? p : a - 1.0f;
+    c = l2 < -1.0f ? a : __uint_as_float(__float_as_uint(em1) | kKeep);
   }
 };
 
-// The simple form: a lane walks one channel of one sequence.
+__device__ __forceinline__ float input_factor(float em1, int input_scale) {
+  if (input_scale == AXON_INPUT_PLAIN) return 1.0f;
+  if (input_scale == AXON_INPUT_COMPLEMENT) return -em1;
+  return __builtin_amdgcn_sqrtf(-em1 * (2.0f + em1));
+}
+
+// A wave's share of a tile: kPer tokens of one block, one channel a lane.
+struct Share {
+  int seq, first, count;   // count 0: none; rows first .. first + count - 1
+  int row;                 // of the block tables
+  bool begins, ends;       // holds the sequence's first / last token
+  bool opens;              // holds the block's first token
+};
+
+__device__ __forceinline__ Share share_of(const Packed& p, int tile, int wave, int waves) {
+  const int at = (tile * waves + wave) * kPer;  // tokens in front, were all blocks full
+  Share s{};
+  s.row = at / kBlock;
+  const int sub = at - s.row * kBlock;
+  const BlockAt b = block_at(p, s.row);
+  s.seq = b.seq;
+  s.first = b.first + sub;
+  s.count = b.seq < 0 ? 0 : min(max(b.count - sub, 0), kPer);
+  s.opens = s.count > 0 && sub == 0;
+  s.begins = s.opens && b.begins;
+  s.ends = s.count > 0 && b.ends && sub + s.count == b.count;
+  return s;
+}
+
+// kPer rows of a wave as loaded; rows behind the last repeat it, channels behind the last likewise.
 template <typename Act>
-__global__ __launch_bounds__(64) void linear_walk_kernel(LinearArgs g) {
-  const int e = blockIdx.x * 64 + threadIdx.x, n = blockIdx.y;
-  if (e >= g.channels) return;
-  const Act* x = static_cast<const Act*>(g.x);
-  const Act* raw = static_cast<const Act*>(g.dt_raw);
-  const Act* in = static_cast<const Act*>(g.in_raw);
-  const float rate = expf(g.A_log[e]);
-  const float bias = g.dt_bias ? g.dt_bias[e] : 0.0f, ib = in && g.in_bias ? g.in_bias[e] : 0.0f;
-  const int s0 = packed_start(g.p, n), s1 = packed_start(g.p, n + 1);
-  float h = 0.0f;
-  if (g.state_in) {
-    const int64_t slot = g.in_slots ? g.in_slots[n] : n;
-    if (slot >= 0 && slot < g.in_count) h = g.state_in[slot * g.channels + e];
+struct Rows {
+  typename RawOf<Act>::type v[kPer];
+  __device__ __forceinline__ void load(const void* base, int64_t stride, const Share& s, int e) {
+    const rsrc_t r = make_rsrc(static_cast<const Act*>(base) + s.first * stride);
+    const uint32_t step = static_cast<uint32_t>(stride) * sizeof(Act), off = e * sizeof(Act);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint32_t row = static_cast<uint32_t>(min(j, s.count - 1)) * step;
+      if constexpr (sizeof(Act) == 4) v[j] = __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
+      else v[j] = __builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
+    }
   }
-  const int64_t row0 = g.p.starts ? max(g.p.block_starts[n], 0) : int64_t(n) * g.p.blocks_per_seq;
-  for (int t = s0; t < s1; ++t) {
-    const int64_t row = row0 + (t - s0) / kBlock;
-    if (g.checkpoints && (t - s0) % kBlock == 0 && row < g.p.rows)
-      g.checkpoints[row * g.channels + e] = h;
-    const Decay d(load_act(raw, t * g.dt_stride + e) + bias, rate, g.gate, g.input_scale);
-    float u = load_act(x, t * g.x_stride + e);
-    if (in) u *= Sigmoid(load_act(in, t * g.in_stride + e) + ib).on;
-    h = d.advance(h, d.m * u);
-    store_act(static_cast<Act*>(g.y), int64_t(t) * g.channels + e, h);
+  __device__ __forceinline__ float operator[](int j) const { return widen(v[j]); }
+};
+
+// What the tiles in front (behind, in the backward pass) hand on. A tile first publishes its own part
+// (decay A, h from zero), then, once it knows what enters it, what leaves it. A reader takes the
+// nearest tile that has published the latter and applies the parts between in the order in which
+// those tiles do it themselves, so that the result does not depend on who was first. Both are one
+// atomic of the value itself: a NaN with all bits set stands for nothing, and stored NaNs are others.
+__device__ __forceinline__ uint32_t told(float v) {
+  return v != v ? 0x7FC00000u : __float_as_uint(v);
+}
+__device__ __forceinline__ void tell_sums(uint64_t* p, float A, float h) {
+  __hip_atomic_store(p, static_cast<uint64_t>(told(h)) << 32 | told(A), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void tell_carry(uint32_t* p, float h) {
+  __hip_atomic_store(p, told(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+constexpr int kWindow = 8;  // tiles looked at
+
+// Waits for what tile `from` hands on; tiles go down from it (DIR -1) or up (DIR 1), `left` of them.
+// Every tile's workgroup has started once a later ticket is out, and none of them waits for a later
+// one, so that the wait ends.
+template <int DIR>
+__device__ __forceinline__ float hear(const LinearArgs& g, int from, int left, int64_t column) {
+  const int64_t width = int64_t(g.groups) * 64;
+  const int n = min(left, kWindow);
+  for (;;) {
+    uint32_t c[kWindow];
+    uint64_t s[kWindow];
+#pragma unroll
+    for (int k = 0; k < kWindow; ++k) {
+      const int64_t at = int64_t(from + DIR * min(k, n - 1)) * width + column;
+      c[k] = __hip_atomic_load(g.carry + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      s[k] = __hip_atomic_load(g.sums + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    int found = -1;
+    bool between = true;  // all sums up to here are told
+#pragma unroll
+    for (int k = 0; k < kWindow; ++k) {
+      if (found < 0 && k < n && between) {
+        if (__all(c[k] != ~0u)) found = k;
+        else between = __all(s[k] != ~uint64_t(0));
+      }
+    }
+    if (found >= 0) {
+      float h = 0.0f;
+#pragma unroll
+      for (int k = kWindow - 1; k >= 0; --k) {
+        if (k == found) h = __uint_as_float(c[k]);
+        else if (k < found)
+          h = fmaf(__uint_as_float(static_cast<uint32_t>(s[k])), h,
+                   __uint_as_float(static_cast<uint32_t>(s[k] >> 32)));
+      }
+      return h;
+    }
+    __builtin_amdgcn_s_sleep(2);
   }
-  if (g.state_out) {
-    const int64_t slot = g.out_slots ? g.out_slots[n] : n;
-    if (slot >= 0 && slot < g.out_count) g.state_out[slot * g.channels + e] = h;
+}
+
+// The tile and channel group of this workgroup: in the order in which workgroups start.
+__device__ __forceinline__ uint32_t take_ticket(const LinearArgs& g, uint32_t* shared) {
+  if (!g.ticket) return blockIdx.x;
+  if (threadIdx.x == 0)
+    *shared = 1 + __hip_atomic_fetch_add(g.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(*shared);
+}
+
+__global__ __launch_bounds__(256) void linear_clear_kernel(uint4* p, int64_t count) {
+  const int64_t step = int64_t(gridDim.x) * 256;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < count; i += step)
+    p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+}
+
+template <typename Act, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void linear_tile_kernel(LinearArgs g) {
+  __shared__ uint32_t ticket;
+  __shared__ float decay[WAVES][64], part[WAVES][64], enter[64];
+  __shared__ int fresh[WAVES];  // the wave begins a sequence
+  const uint32_t t = take_ticket(g, &ticket);
+  const int tile = t / g.groups, grp = t - tile * g.groups;
+  if (tile >= g.tiles) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const bool in_range = grp * 64 + lane < g.channels;
+  const int e = min(grp * 64 + lane, g.channels - 1);
+  const Share s = share_of(g.p, tile, wave, WAVES);
+  float c[kPer], b[kPer];
+  float h0 = 0.0f;  // what enters the wave, where it begins a sequence
+  float L = 0.0f, h = 0.0f;
+  if (s.count > 0) {
+    Rows<Act> x, raw, in;
+    raw.load(g.dt_raw, g.dt_stride, s, e);
+    x.load(g.x, g.x_stride, s, e);
+    if (g.in_raw) in.load(g.in_raw, g.in_stride, s, e);
+    if (s.begins && g.state_in) {
+      const int64_t slot = g.in_slots ? g.in_slots[s.seq] : s.seq;
+      if (slot >= 0 && slot < g.in_count) h0 = g.state_in[slot * g.channels + e];
+    }
+    const float rate = -expf(g.A_log[e]) * kLog2e;
+    const float bias = g.dt_bias ? g.dt_bias[e] : 0.0f;
+    if (g.gate == AXON_LINEAR_SIGMOID) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) c[j] = rate * sigmoid_f32(raw[j] + bias);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) c[j] = rate * softplus_nan(raw[j] + bias);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      L += j < s.count ? c[j] : 0.0f;
+      const Decay d(c[j]);
+      c[j] = d.c;
+      b[j] = d.em1;
+    }
+    if (g.input_scale == AXON_INPUT_SQRT) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) b[j] = x[j] * input_factor(b[j], AXON_INPUT_SQRT);
+    } else if (g.input_scale == AXON_INPUT_COMPLEMENT) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) b[j] = x[j] * -b[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) b[j] = x[j];
+    }
+    if (g.in_raw) {
+      const float ib = g.in_bias ? g.in_bias[e] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) b[j] *= sigmoid_f32(in[j] + ib);
+    }
+    if (s.count < kPer) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (j >= s.count) c[j] = __uint_as_float(kKeep), b[j] = 0.0f;
+    }
+    h = h0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) h = advance(c[j], h, b[j]);
+  }
+  decay[wave][lane] = __builtin_amdgcn_exp2f(L);
+  part[wave][lane] = h;
+  if (lane == 0) fresh[wave] = s.begins;
+  __syncthreads();
+  if (wave == 0) {
+    // The tile's own part, then what enters it.
+    float A = 1.0f, own = 0.0f;
+    bool closed = false;  // a sequence begins in the tile: nothing from in front leaves it
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const bool f = fresh[w];
+      own = f ? part[w][lane] : fmaf(decay[w][lane], own, part[w][lane]);
+      A *= decay[w][lane];
+      closed |= f;
+    }
+    float before = 0.0f;
+    if (g.ticket) {
+      const int64_t at = int64_t(t) * 64 + lane;
+      const bool alone = s.begins || tile == 0;
+      if (closed || alone) tell_carry(g.carry + at, own);
+      else tell_sums(g.sums + at, A, own);
+      if (!alone) {
+        before = hear<-1>(g, tile - 1, tile, grp * 64 + lane);
+        if (!closed) tell_carry(g.carry + at, fmaf(A, before, own));
+      }
+    }
+    enter[lane] = before;
+  }
+  __syncthreads();
+  if (s.count > 0) {
+    h = enter[lane];
+    for (int w = 0; w < wave; ++w)
+      h = fresh[w] ? part[w][lane] : fmaf(decay[w][lane], h, part[w][lane]);
+    if (s.begins) h = h0;
+    if (in_range) {
+      if (s.opens && g.checkpoints) g.checkpoints[int64_t(s.row) * g.channels + e] = h;
+      Act* y = static_cast<Act*>(g.y) + int64_t(s.first) * g.channels + e;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        h = advance(c[j], h, b[j]);
+        if (j < s.count) store_act(y, int64_t(j) * g.channels, h);
+      }
+      if (s.ends && g.state_out) {
+        const int64_t slot = g.out_slots ? g.out_slots[s.seq] : s.seq;
+        if (slot >= 0 && slot < g.out_count) g.state_out[slot * g.channels + e] = h;
+      }
+    }
+  }
+  if (!in_range) return;
+  // Sequences without tokens, and rows behind the last one: shared out to the tiles' waves.
+  for (int n = tile * WAVES + wave; n < g.p.sequences; n += g.tiles * WAVES) {
+    if (!g.state_out || packed_start(g.p, n) < packed_start(g.p, n + 1)) continue;
+    const int64_t from = g.in_slots ? g.in_slots[n] : n, to = g.out_slots ? g.out_slots[n] : n;
+    if (to >= 0 && to < g.out_count)
+      g.state_out[to * g.channels + e] =
+          g.state_in && from >= 0 && from < g.in_count ? g.state_in[from * g.channels + e] : 0.0f;
   }
   if (g.clear_behind)
-    for (int t = packed_start(g.p, g.p.sequences) + n; t < g.p.tokens; t += g.p.sequences)
-      store_act(static_cast<Act*>(g.y), int64_t(t) * g.channels + e, 0.0f);
+    for (int64_t r = int64_t(packed_start(g.p, g.p.sequences)) + tile * WAVES + wave;
+         r < g.p.tokens; r += int64_t(g.tiles) * WAVES)
+      store_act(static_cast<Act*>(g.y), r * g.channels + e, 0.0f);
 }
 
-// The same backwards, a block at a time: the block's states are found again from its checkpoint.
-template <typename Act>
-__global__ __launch_bounds__(64) void linear_walk_back_kernel(LinearArgs g) {
-  const int e = blockIdx.x * 64 + threadIdx.x, n = blockIdx.y;
-  if (e >= g.channels) return;
-  const Act* x = static_cast<const Act*>(g.x);
-  const Act* raw = static_cast<const Act*>(g.dt_raw);
-  const Act* in = static_cast<const Act*>(g.in_raw);
-  const float rate = expf(g.A_log[e]);
-  const float bias = g.dt_bias ? g.dt_bias[e] : 0.0f, ib = in && g.in_bias ? g.in_bias[e] : 0.0f;
-  const int s0 = packed_start(g.p, n), s1 = packed_start(g.p, n + 1);
-  const int64_t row0 = g.p.starts ? max(g.p.block_starts[n], 0) : int64_t(n) * g.p.blocks_per_seq;
-  float k = g.dstate_out ? g.dstate_out[int64_t(n) * g.channels + e] : 0.0f;
-  double sA = 0.0, sdt = 0.0, sin = 0.0;
-  float before[kBlock];
-  for (int first = s0 + (s1 - s0 - 1) / kBlock * kBlock; s1 > s0 && first >= s0; first -= kBlock) {
-    const int count = min(kBlock, s1 - first);
-    const int64_t row = row0 + (first - s0) / kBlock;
-    float h = row < g.p.rows ? g.points[row * g.channels + e] : 0.0f;
-    for (int j = 0; j < count; ++j) {
-      const int64_t t = first + j;
-      before[j] = h;
-      const Decay d(load_act(raw, t * g.dt_stride + e) + bias, rate, g.gate, g.input_scale);
-      float u = load_act(x, t * g.x_stride + e);
-      if (in) u *= Sigmoid(load_act(in, t * g.in_stride + e) + ib).on;
-      h = d.advance(h, d.m * u);
+// The same from the last tile to the first. A wave finds its block's states again from the block's
+// checkpoint and the parts of the waves in front of it.
+template <typename Act, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void linear_tile_back_kernel(LinearArgs g) {
+  static_assert(WAVES * kPer % kBlock == 0, "a tile holds whole blocks");
+  constexpr int kBlockWaves = kBlock / kPer;
+  __shared__ uint32_t ticket;
+  __shared__ float decay[WAVES][64], part[WAVES][64], back[WAVES][64], enter[64];
+  __shared__ int fresh[WAVES];  // the wave ends a sequence
+  const uint32_t t = take_ticket(g, &ticket);
+  const int turn = t / g.groups, grp = t - turn * g.groups;
+  if (turn >= g.tiles) return;
+  const int tile = g.tiles - 1 - turn;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const bool in_range = grp * 64 + lane < g.channels;
+  const int e = min(grp * 64 + lane, g.channels - 1);
+  const Share s = share_of(g.p, tile, wave, WAVES);
+  float c[kPer], v[kPer], vi[kPer], xs[kPer], dy[kPer], hb[kPer];
+  float L = 0.0f, h = 0.0f, k = 0.0f, k0 = 0.0f, rate = 0.0f;
+  if (s.count > 0) {
+    Rows<Act> x, raw, in, d;
+    raw.load(g.dt_raw, g.dt_stride, s, e);
+    x.load(g.x, g.x_stride, s, e);
+    if (g.in_raw) in.load(g.in_raw, g.in_stride, s, e);
+    d.load(g.dy, g.dy_stride, s, e);
+    if (s.opens) h = g.points[int64_t(s.row) * g.channels + e];
+    if (s.ends && g.dstate_out) k0 = g.dstate_out[int64_t(s.seq) * g.channels + e];
+    rate = -expf(g.A_log[e]);
+    const float bias = g.dt_bias ? g.dt_bias[e] : 0.0f;
+    const float ib = g.in_raw && g.in_bias ? g.in_bias[e] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      v[j] = raw[j] + bias;
+      xs[j] = x[j];
+      dy[j] = d[j];
+      vi[j] = g.in_raw ? in[j] + ib : 0.0f;
     }
-    for (int j = count - 1; j >= 0; --j) {
-      const int64_t t = first + j;
-      const float v = load_act(raw, t * g.dt_stride + e) + bias;
-      const Decay d(v, rate, g.gate, g.input_scale);
-      const float xv = load_act(x, t * g.x_stride + e);
-      const Sigmoid i(in ? load_act(in, t * g.in_stride + e) + ib : 0.0f);
-      const float u = in ? xv * i.on : xv;
-      const float gt = load_act(static_cast<const Act*>(g.dy), t * g.dy_stride + e) + k;
-      const float aL = d.a == 0.0f ? 0.0f : d.a * d.L;
-      float G = aL * before[j];
-      if (g.input_scale == AXON_INPUT_COMPLEMENT) G -= aL * u;
-      if (g.input_scale == AXON_INPUT_SQRT && d.m != 0.0f) G -= d.a * (aL * u) / d.m;
-      G *= gt;
-      const Sigmoid s(v);
-      const float slope = g.gate == AXON_LINEAR_SIGMOID ? s.off : (v < -20.0f ? 1.0f : s.on / softplus_f32(v));
-      const float draw = G * slope, du = gt * d.m;
-      sA += G, sdt += draw;
-      const int64_t at = t * g.channels + e;
-      store_act(static_cast<Act*>(g.ddt_raw), at, draw);
-      store_act(static_cast<Act*>(g.dx), at, in ? du * i.on : du);
-      if (in) {
-        const float di = du * xv * i.on * i.off;
-        sin += di;
-        store_act(static_cast<Act*>(g.din_raw), at, di);
-      }
-      k = d.advance(gt, 0.0f);
+    const float rate2 = rate * kLog2e;
+    if (g.gate == AXON_LINEAR_SIGMOID) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) c[j] = rate2 * sigmoid_f32(v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) c[j] = rate2 * softplus_nan(v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      L += j < s.count ? c[j] : 0.0f;
+      const Decay t2(c[j]);
+      c[j] = t2.c;
+      float u = xs[j] * input_factor(t2.em1, g.input_scale);
+      if (g.in_raw) u *= sigmoid_f32(vi[j]);
+      hb[j] = u;
+    }
+    if (s.count < kPer) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (j >= s.count) c[j] = __uint_as_float(kKeep), hb[j] = 0.0f, dy[j] = 0.0f;
+    }
+    // hb holds the inputs still: the wave's own part of its last state
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) h = advance(c[j], h, hb[j]);
+    k = k0;
+#pragma unroll
+    for (int j = kPer - 1; j >= 0; --j) {
+      k += dy[j];
+      k = advance(c[j], k, 0.0f);
     }
   }
-  if (g.dstate_in) g.dstate_in[int64_t(n) * g.channels + e] = k;
-  float* part = g.partial + int64_t(n) * 3 * g.channels + e;
-  part[0] = static_cast<float>(sA);
-  part[g.channels] = static_cast<float>(sdt);
-  part[2 * int64_t(g.channels)] = static_cast<float>(sin);
-  for (int t = packed_start(g.p, g.p.sequences) + n; t < g.p.tokens; t += g.p.sequences) {
-    const int64_t at = int64_t(t) * g.channels + e;
+  decay[wave][lane] = __builtin_amdgcn_exp2f(L);
+  part[wave][lane] = h;
+  back[wave][lane] = k;
+  if (lane == 0) fresh[wave] = s.ends;
+  __syncthreads();
+  if (wave == WAVES - 1) {
+    float A = 1.0f, own = 0.0f;
+    bool closed = false;
+#pragma unroll
+    for (int w = WAVES - 1; w >= 0; --w) {
+      const bool f = fresh[w];
+      own = f ? back[w][lane] : fmaf(decay[w][lane], own, back[w][lane]);
+      A *= decay[w][lane];
+      closed |= f;
+    }
+    float behind = 0.0f;
+    if (g.ticket) {
+      const int64_t at = (int64_t(tile) * g.groups + grp) * 64 + lane;
+      const bool alone = s.ends || turn == 0;
+      if (closed || alone) tell_carry(g.carry + at, own);
+      else tell_sums(g.sums + at, A, own);
+      if (!alone) {
+        behind = hear<1>(g, tile + 1, turn, grp * 64 + lane);
+        if (!closed) tell_carry(g.carry + at, fmaf(A, behind, own));
+      }
+    }
+    enter[lane] = behind;
+  }
+  float sA = 0.0f, sdt = 0.0f, sin = 0.0f;
+  // The states in front of the wave's tokens.
+  if (s.count > 0) {
+    const int w0 = wave / kBlockWaves * kBlockWaves;
+    h = s.opens ? g.points[int64_t(s.row) * g.channels + e] : part[w0][lane];
+    for (int w = w0 + 1; w < wave; ++w) h = fmaf(decay[w][lane], h, part[w][lane]);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const float u = hb[j];
+      hb[j] = h;
+      h = advance(c[j], h, u);
+    }
+  }
+  __syncthreads();
+  if (s.count > 0) {
+    k = enter[lane];
+    for (int w = WAVES - 1; w > wave; --w)
+      k = fresh[w] ? back[w][lane] : fmaf(decay[w][lane], k, back[w][lane]);
+    if (s.ends) k = k0;
+    const int64_t first = int64_t(s.first) * g.channels + e;
+    Act* dx = static_cast<Act*>(g.dx) + first;
+    Act* ddt = static_cast<Act*>(g.ddt_raw) + first;
+    Act* din = static_cast<Act*>(g.din_raw) + first;
+#pragma unroll
+    for (int j = kPer - 1; j >= 0; --j) {
+      if (j >= s.count) continue;
+      const bool slow = __float_as_int(c[j]) < 0;
+      const float a = slow ? 1.0f + c[j] : c[j], em1 = slow ? c[j] : c[j] - 1.0f;
+      const float gt = dy[j] + k;
+      k = advance(c[j], gt, 0.0f);
+      float Lj, slope;
+      if (g.gate == AXON_LINEAR_SIGMOID) {
+        const Sigmoid sg(v[j]);
+        Lj = rate * sg.on;
+        slope = sg.off;
+      } else {
+        const float sp = softplus_nan(v[j]);
+        Lj = rate * sp;
+        slope = v[j] < -20.0f ? 1.0f : sigmoid_f32(v[j]) / sp;
+      }
+      const Sigmoid i(vi[j]);
+      const float u = g.in_raw ? xs[j] * i.on : xs[j];
+      const float aL = a == 0.0f ? 0.0f : a * Lj;
+      float G = aL * hb[j], m = 1.0f;
+      if (g.input_scale == AXON_INPUT_COMPLEMENT) {
+        m = -em1;
+        G -= aL * u;
+      } else if (g.input_scale == AXON_INPUT_SQRT) {
+        m = input_factor(em1, AXON_INPUT_SQRT);
+        if (m != 0.0f) G -= a * (aL * u) * __builtin_amdgcn_rcpf(m);
+      }
+      G *= gt;
+      const float draw = G * slope, du = gt * m;
+      sA += G;
+      sdt += draw;
+      if (in_range) {
+        const int64_t at = int64_t(j) * g.channels;
+        store_act(ddt, at, draw);
+        store_act(dx, at, g.in_raw ? du * i.on : du);
+        if (g.in_raw) {
+          const float di = du * xs[j] * i.on * i.off;
+          sin += di;
+          store_act(din, at, di);
+        }
+      }
+    }
+    if (s.begins && g.dstate_in && in_range) g.dstate_in[int64_t(s.seq) * g.channels + e] = k;
+  }
+  __syncthreads();
+  decay[wave][lane] = sA;
+  part[wave][lane] = sdt;
+  back[wave][lane] = sin;
+  __syncthreads();
+  if (wave < 3 && in_range) {
+    const float* from = wave == 0 ? &decay[0][lane] : wave == 1 ? &part[0][lane] : &back[0][lane];
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) sum += from[w * 64];
+    g.partial[(int64_t(tile) * 3 + wave) * g.channels + e] = sum;
+  }
+  if (!in_range) return;
+  if (g.dstate_in)
+    for (int n = tile * WAVES + wave; n < g.p.sequences; n += g.tiles * WAVES) {
+      if (packed_start(g.p, n) < packed_start(g.p, n + 1)) continue;
+      const int64_t at = int64_t(n) * g.channels + e;
+      g.dstate_in[at] = g.dstate_out ? g.dstate_out[at] : 0.0f;
+    }
+  for (int64_t r = int64_t(packed_start(g.p, g.p.sequences)) + tile * WAVES + wave; r < g.p.tokens;
+       r += int64_t(g.tiles) * WAVES) {
+    const int64_t at = r * g.channels + e;
     store_act(static_cast<Act*>(g.dx), at, 0.0f);
     store_act(static_cast<Act*>(g.ddt_raw), at, 0.0f);
-    if (in) store_act(static_cast<Act*>(g.din_raw), at, 0.0f);
+    if (g.in_raw) store_act(static_cast<Act*>(g.din_raw), at, 0.0f);
   }
 }
 
-__global__ __launch_bounds__(64) void linear_sum_kernel(LinearArgs g, int parts) {
-  const int e = blockIdx.x * 64 + threadIdx.x, which = blockIdx.y;
-  if (e >= g.channels) return;
+// Sums of the tiles' parts in 64 bits: four waves take every fourth tile.
+__global__ __launch_bounds__(256) void linear_sum_kernel(LinearArgs g, int parts) {
+  __shared__ double sums[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.x * 64 + lane, which = blockIdx.y;
   double s = 0.0;
-  for (int j = 0; j < parts; ++j) s += g.partial[(int64_t(j) * 3 + which) * g.channels + e];
+  if (e < g.channels)
+    for (int j = wave; j < parts; j += 4)
+      s += g.partial[(int64_t(j) * 3 + which) * g.channels + e];
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave || e >= g.channels) return;
   float* out = which == 0 ? g.dA_log : which == 1 ? g.ddt_bias : g.din_bias;
-  out[e] = static_cast<float>(s);
+  out[e] = static_cast<float>(sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane]);
 }
 
 template <typename Act>
@@ -200,12 +549,14 @@ __global__ __launch_bounds__(256) void linear_step_kernel(LinearArgs g) {
   const int64_t slot = g.in_slots ? g.in_slots[n] : n;
   if (slot < 0 || slot >= g.in_count) return;
   const Act* in = static_cast<const Act*>(g.in_raw);
-  const float v = load_act(static_cast<const Act*>(g.dt_raw), n * g.dt_stride + e);
+  const float v =
+      load_act(static_cast<const Act*>(g.dt_raw), n * g.dt_stride + e) + (g.dt_bias ? g.dt_bias[e] : 0.0f);
   float u = load_act(static_cast<const Act*>(g.x), n * g.x_stride + e);
-  const Decay d(v + (g.dt_bias ? g.dt_bias[e] : 0.0f), expf(g.A_log[e]), g.gate, g.input_scale);
-  if (in) u *= Sigmoid(load_act(in, n * g.in_stride + e) + (g.in_bias ? g.in_bias[e] : 0.0f)).on;
+  const float dt = g.gate == AXON_LINEAR_SIGMOID ? sigmoid_f32(v) : softplus_nan(v);
+  const Decay d(-expf(g.A_log[e]) * kLog2e * dt);
+  if (in) u *= sigmoid_f32(load_act(in, n * g.in_stride + e) + (g.in_bias ? g.in_bias[e] : 0.0f));
   float* state = g.state_out + slot * g.channels + e;
-  const float h = d.advance(*state, d.m * u);
+  const float h = advance(d.c, *state, input_factor(d.em1, g.input_scale) * u);
   *state = h;
   store_act(static_cast<Act*>(g.y), int64_t(n) * g.channels + e, h);
 }
@@ -264,6 +615,63 @@ size_t tables_bytes(const Packed& p) {
   return p.starts ? 4 * (2 * (size_t(p.sequences) + 1) + 2 * size_t(p.rows)) : 0;
 }
 
+constexpr int kWaves = 8;
+constexpr int kBackWaves = 8;
+
+// Tiles, and what of the workspace they use.
+struct Plan {
+  int64_t tiles, groups;
+  size_t sums, carry, ticket, chain;  // offsets and bytes of what tiles tell each other; chain 0: nothing
+  size_t bytes;
+};
+
+Plan plan_linear(const axon_linear_shape& s, bool packed, int waves, bool backward) {
+  Plan p{};
+  // rows of the tables, or sequences without tokens, at least one tile
+  const int64_t rows = std::max<int64_t>(packed_rows(s.sequences, s.tokens, packed), 1);
+  const int64_t blocks = waves * kPer / kBlock;
+  p.tiles = (rows + blocks - 1) / blocks;
+  p.groups = (s.channels + 63) / 64;
+  const size_t cells = size_t(p.tiles) * size_t(p.groups) * 64;
+  if (p.tiles > 1) {
+    p.sums = 0;
+    p.carry = 8 * cells;
+    p.ticket = 12 * cells;
+    p.chain = p.ticket + 16;
+  }
+  p.bytes = p.chain + (backward ? 4 * 3 * size_t(p.tiles) * size_t(s.channels) : 0);
+  return p;
+}
+
+// The workspace holds for either kind of batch: a uniform one has no more blocks than a packed one can.
+size_t workspace_of(const axon_linear_shape& s, int waves, bool backward) {
+  return plan_linear(s, true, waves, backward).bytes;
+}
+
+void use_plan(LinearArgs* a, const Plan& p, void* workspace) {
+  a->tiles = static_cast<int>(p.tiles), a->groups = static_cast<int>(p.groups);
+  char* w = static_cast<char*>(workspace);
+  if (p.chain) {
+    a->sums = reinterpret_cast<uint64_t*>(w + p.sums);
+    a->carry = reinterpret_cast<uint32_t*>(w + p.carry);
+    a->ticket = reinterpret_cast<uint32_t*>(w + p.ticket);
+  }
+  a->partial = reinterpret_cast<float*>(w + p.chain);
+}
+
+void clear_chain(const Plan& p, void* workspace, hipStream_t st) {
+  if (!p.chain) return;
+  const int64_t count = static_cast<int64_t>(p.chain / 16), wgs = (count + 1023) / 1024;
+  hipLaunchKernelGGL(linear_clear_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(wgs, 2048))), dim3(256),
+                     0, st, static_cast<uint4*>(workspace), count);
+}
+
+// Workgroups along x, beyond 2^20 of them (a launch holds fewer than 2^32 threads along x) along y.
+dim3 tile_grid(const Plan& p) {
+  const int64_t n = p.tiles * p.groups, x = std::min<int64_t>(n, 1 << 20);
+  return dim3(static_cast<unsigned>(x), static_cast<unsigned>((n + x - 1) / x));
+}
+
 unsigned channel_groups(int channels, int width) {
   return static_cast<unsigned>((channels + width - 1) / width);
 }
@@ -280,7 +688,10 @@ size_t axon_linear_checkpoint_rows(int64_t sequences, int64_t tokens, int32_t pa
   return size_t(axon::packed_rows(sequences, tokens, packed != 0));
 }
 
-size_t axon_linear_scan_workspace_bytes(const axon_linear_shape*) { return 0; }
+size_t axon_linear_scan_workspace_bytes(const axon_linear_shape* shape) {
+  if (axon::check_shape(shape, false) != AXON_OK) return 0;
+  return axon::workspace_of(*shape, axon::kWaves, false);
+}
 
 axon_status axon_linear_scan(const axon_linear_shape* shape, const axon_linear_params* params,
                              const void* x, const void* dt_raw, const void* in_raw,
@@ -332,18 +743,20 @@ axon_status axon_linear_scan(const axon_linear_shape* shape, const axon_linear_p
   a.state_in = state_in, a.in_slots = in_slots, a.in_count = s.state_slots;
   a.state_out = state_out, a.out_slots = out_slots, a.out_count = s.out_slots;
   a.y = y, a.checkpoints = checkpoints;
-  const dim3 grid(channel_groups(a.channels, 64), a.p.sequences);
+  const Plan plan = plan_linear(s, tables != nullptr, kWaves, false);
+  use_plan(&a, plan, workspace);
   hipStream_t st = static_cast<hipStream_t>(stream);
+  clear_chain(plan, workspace, st);
   if (bf)
-    hipLaunchKernelGGL(linear_walk_kernel<bf16_bits>, grid, dim3(64), 0, st, a);
+    hipLaunchKernelGGL((linear_tile_kernel<bf16_bits, kWaves>), tile_grid(plan), dim3(64 * kWaves), 0, st, a);
   else
-    hipLaunchKernelGGL(linear_walk_kernel<float>, grid, dim3(64), 0, st, a);
+    hipLaunchKernelGGL((linear_tile_kernel<float, kWaves>), tile_grid(plan), dim3(64 * kWaves), 0, st, a);
   return hipGetLastError() == hipSuccess ? AXON_OK : AXON_ERR_HIP;
 }
 
 size_t axon_linear_scan_backward_workspace_bytes(const axon_linear_shape* shape) {
   if (axon::check_shape(shape, true) != AXON_OK) return 0;
-  return 4 * 3 * size_t(shape->sequences) * size_t(shape->channels);
+  return axon::workspace_of(*shape, axon::kBackWaves, true);
 }
 
 axon_status axon_linear_scan_backward(const axon_linear_shape* shape,
@@ -397,15 +810,17 @@ axon_status axon_linear_scan_backward(const axon_linear_shape* shape,
   a.dy = dy, a.points = checkpoints, a.dstate_out = dstate_out;
   a.dx = dx, a.ddt_raw = ddt_raw, a.din_raw = din_raw;
   a.dA_log = dA_log, a.ddt_bias = ddt_bias, a.din_bias = din_bias, a.dstate_in = dstate_in;
-  a.partial = static_cast<float*>(workspace);
-  const dim3 grid(channel_groups(a.channels, 64), a.p.sequences);
+  const Plan plan = plan_linear(s, tables != nullptr, kBackWaves, true);
+  use_plan(&a, plan, workspace);
   hipStream_t st = static_cast<hipStream_t>(stream);
+  clear_chain(plan, workspace, st);
+  const dim3 grid = tile_grid(plan), threads(64 * kBackWaves);
   if (bf)
-    hipLaunchKernelGGL(linear_walk_back_kernel<bf16_bits>, grid, dim3(64), 0, st, a);
+    hipLaunchKernelGGL((linear_tile_back_kernel<bf16_bits, kBackWaves>), grid, threads, 0, st, a);
   else
-    hipLaunchKernelGGL(linear_walk_back_kernel<float>, grid, dim3(64), 0, st, a);
+    hipLaunchKernelGGL((linear_tile_back_kernel<float, kBackWaves>), grid, threads, 0, st, a);
   hipLaunchKernelGGL(linear_sum_kernel, dim3(channel_groups(a.channels, 64), din_bias ? 3 : 2),
-                     dim3(64), 0, st, a, a.p.sequences);
+                     dim3(256), 0, st, a, a.tiles);
   return hipGetLastError() == hipSuccess ? AXON_OK : AXON_ERR_HIP;
 }
 
