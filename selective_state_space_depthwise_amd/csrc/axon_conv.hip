@@ -37,167 +37,331 @@ struct ConvArgs {
   float* partial;  // (rows, kSums, channels)
 };
 
-// The cache of sequence n at channel e, zeros where there is none.
-__device__ __forceinline__ void load_cache(const ConvArgs& g, int n, int e, float* c) {
-  c[0] = c[1] = c[2] = 0.0f;
+// V channels as loaded, and as fp32.
+template <typename Act, int V>
+struct Raw {
+  Act v;
+  __device__ __forceinline__ void load(const Act* p) { v = *p; }
+  __device__ __forceinline__ void get(float* o) const { o[0] = load_act(&v, 0); }
+  static __device__ __forceinline__ void store(Act* p, const float* o) { store_act(p, 0, o[0]); }
+};
+template <>
+struct Raw<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float* o) const { o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w; }
+  static __device__ __forceinline__ void store(float* p, const float* o) {
+    *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+  }
+};
+__device__ __forceinline__ void widen2(uint32_t w, float* o) {
+  o[0] = __uint_as_float(w << 16), o[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t narrow2(const float* o) {
+  return static_cast<uint32_t>(f32_to_bf16(o[0])) | static_cast<uint32_t>(f32_to_bf16(o[1])) << 16;
+}
+template <>
+struct Raw<bf16_bits, 2> {
+  uint32_t v;
+  __device__ __forceinline__ void load(const bf16_bits* p) { v = *reinterpret_cast<const uint32_t*>(p); }
+  __device__ __forceinline__ void get(float* o) const { widen2(v, o); }
+  static __device__ __forceinline__ void store(bf16_bits* p, const float* o) {
+    *reinterpret_cast<uint32_t*>(p) = narrow2(o);
+  }
+};
+template <>
+struct Raw<bf16_bits, 4> {
+  uint2 v;
+  __device__ __forceinline__ void load(const bf16_bits* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void get(float* o) const { widen2(v.x, o), widen2(v.y, o + 2); }
+  static __device__ __forceinline__ void store(bf16_bits* p, const float* o) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(narrow2(o), narrow2(o + 2));
+  }
+};
+
+// The cache of sequence n at V channels from e on, zeros where there is none.
+template <int V>
+__device__ __forceinline__ void load_cache(const ConvArgs& g, int n, int e, float (*c)[V]) {
+#pragma unroll
+  for (int j = 0; j < kHalo; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[j][i] = 0.0f;
   if (!g.cache_in) return;
   const int64_t slot = g.in_slots ? g.in_slots[n] : n;
   if (slot < 0 || slot >= g.in_count) return;
 #pragma unroll
-  for (int j = 0; j < kHalo; ++j) c[j] = g.cache_in[(slot * kHalo + j) * g.channels + e];
+  for (int j = 0; j < kHalo; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[j][i] = g.cache_in[(slot * kHalo + j) * g.channels + e + i];
 }
-__device__ __forceinline__ void store_cache(const ConvArgs& g, int n, int e, const float* c) {
+template <int V>
+__device__ __forceinline__ void store_cache(const ConvArgs& g, int n, int e, const float (*c)[V]) {
   if (!g.cache_out) return;
   const int64_t slot = g.out_slots ? g.out_slots[n] : n;
   if (slot < 0 || slot >= g.out_count) return;
 #pragma unroll
-  for (int j = 0; j < kHalo; ++j) g.cache_out[(slot * kHalo + j) * g.channels + e] = c[j];
+  for (int j = 0; j < kHalo; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) g.cache_out[(slot * kHalo + j) * g.channels + e + i] = c[j][i];
 }
 
-__device__ __forceinline__ float convolve(const float* w, float b, float x0, float x1, float x2,
-                                          float x3) {
-  return fmaf(w[3], x3, fmaf(w[2], x2, fmaf(w[1], x1, fmaf(w[0], x0, b))));
+template <int V>
+struct Taps {
+  float w[kConv][V], b[V];
+  __device__ __forceinline__ void load(const ConvArgs& g, int e) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+      for (int k = 0; k < kConv; ++k) w[k][i] = g.w[int64_t(e + i) * kConv + k];
+      b[i] = g.b ? g.b[e + i] : 0.0f;
+    }
+  }
+  __device__ __forceinline__ float at(int i, float x0, float x1, float x2, float x3) const {
+    return fmaf(w[3][i], x3, fmaf(w[2][i], x2, fmaf(w[1][i], x1, fmaf(w[0][i], x0, b[i]))));
+  }
+};
+
+// Block rows go along y and z; with several waves a workgroup, each takes one.
+__device__ __forceinline__ int block_row() {
+  return __builtin_amdgcn_readfirstlane(
+      static_cast<int>((blockIdx.y + blockIdx.z * gridDim.y) * (blockDim.x >> 6) + (threadIdx.x >> 6)));
+}
+__device__ __forceinline__ int block_rows() {
+  return static_cast<int>(gridDim.y * gridDim.z * (blockDim.x >> 6));
 }
 
-template <typename Act>
+// A wave: 64 V channels of one block. The next kAhead rows are on their way while kAhead are computed.
+template <typename Act, int V>
 __global__ __launch_bounds__(64) void conv_kernel(ConvArgs g) {
-  const int e = blockIdx.x * 64 + threadIdx.x, row = blockIdx.y + blockIdx.z * gridDim.y;
-  const int rows = gridDim.y * gridDim.z;
+  constexpr int kAhead = 8;
+  const int e = (blockIdx.x * 64 + threadIdx.x) * V;
+  const int row = block_row(), rows = block_rows();
   if (e >= g.channels) return;
   const Act* x = static_cast<const Act*>(g.x) + e;
   Act* y = static_cast<Act*>(g.y) + e;
   const BlockAt b = block_at(g.p, row);
   if (b.seq >= 0) {
-    float w[kConv], h[kHalo];
+    const Act* xb = x + b.first * g.x_stride;
+    Act* yb = y + int64_t(b.first) * g.channels;
+    Raw<Act, V> next[kAhead];
 #pragma unroll
-    for (int k = 0; k < kConv; ++k) w[k] = g.w[int64_t(e) * kConv + k];
-    const float bias = g.b ? g.b[e] : 0.0f;
+    for (int j = 0; j < kAhead; ++j) next[j].load(xb + min(j, b.count - 1) * g.x_stride);
+    Taps<V> taps;
+    taps.load(g, e);
+    float h[kHalo][V];
     if (b.begins) {
-      load_cache(g, b.seq, e, h);
+      load_cache<V>(g, b.seq, e, h);
       const int len = packed_start(g.p, b.seq + 1) - b.first;
-      float c[kHalo];
+      float c[kHalo][V];
 #pragma unroll
       for (int j = 0; j < kHalo; ++j) {
         const int at = len - kHalo + j;  // -2 .. of the sequence
-        c[j] = at >= 0 ? load_act(x, (b.first + at) * g.x_stride) : at == -2 ? h[1] : h[2];
+        if (at >= 0) {
+          Raw<Act, V> last;
+          last.load(xb + at * g.x_stride);
+          last.get(c[j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) c[j][i] = at == -2 ? h[1][i] : h[2][i];
+        }
       }
-      store_cache(g, b.seq, e, c);
+      store_cache<V>(g, b.seq, e, c);
     } else {
 #pragma unroll
-      for (int j = 0; j < kHalo; ++j) h[j] = load_act(x, (b.first - kHalo + j) * g.x_stride);
+      for (int j = 0; j < kHalo; ++j) {
+        Raw<Act, V> r;
+        r.load(xb + (j - kHalo) * g.x_stride);
+        r.get(h[j]);
+      }
     }
-    for (int j = 0; j < b.count; ++j) {
-      const float v = load_act(x, (int64_t(b.first) + j) * g.x_stride);
-      float p = convolve(w, bias, h[0], h[1], h[2], v);
-      if (g.silu) p = silu(p);
-      store_act(y, (int64_t(b.first) + j) * g.channels, p);
-      h[0] = h[1], h[1] = h[2], h[2] = v;
+    for (int j0 = 0; j0 < b.count; j0 += kAhead) {
+      Raw<Act, V> now[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) now[j] = next[j];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        next[j].load(xb + min(j0 + kAhead + j, b.count - 1) * g.x_stride);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        float v[V], p[V];
+        now[j].get(v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          p[i] = taps.at(i, h[0][i], h[1][i], h[2][i], v[i]);
+          if (g.silu) p[i] = silu(p[i]);
+          h[0][i] = h[1][i], h[1][i] = h[2][i], h[2][i] = v[i];
+        }
+        if (j0 + j < b.count) Raw<Act, V>::store(yb + int64_t(j0 + j) * g.channels, p);
+      }
     }
   }
   for (int n = row; n < g.p.sequences; n += rows)
     if (packed_start(g.p, n) >= packed_start(g.p, n + 1)) {
-      float c[kHalo];
-      load_cache(g, n, e, c);
-      store_cache(g, n, e, c);
+      float c[kHalo][V];
+      load_cache<V>(g, n, e, c);
+      store_cache<V>(g, n, e, c);
     }
-  if (g.clear_behind)
+  if (g.clear_behind) {
+    const float zero[V] = {};
     for (int64_t t = int64_t(packed_start(g.p, g.p.sequences)) + row; t < g.p.tokens; t += rows)
-      store_act(y, t * g.channels, 0.0f);
+      Raw<Act, V>::store(y + t * g.channels, zero);
+  }
 }
 
-template <typename Act>
-__global__ __launch_bounds__(64) void conv_back_kernel(ConvArgs g) {
-  const int e = blockIdx.x * 64 + threadIdx.x, row = blockIdx.y + blockIdx.z * gridDim.y;
-  const int rows = gridDim.y * gridDim.z;
-  if (e >= g.channels) return;
-  const Act* x = static_cast<const Act*>(g.x) + e;
-  const Act* dy = static_cast<const Act*>(g.dy) + e;
-  Act* dx = static_cast<Act*>(g.dx) + e;
+constexpr int kBackWaves = 4;  // blocks of a workgroup, whose sums are joined
+
+template <typename Act, int V>
+__global__ __launch_bounds__(64 * kBackWaves) void conv_back_kernel(ConvArgs g) {
+  constexpr int kAhead = 4;
+  __shared__ float joined[kBackWaves][kSums * V][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = (blockIdx.x * 64 + lane) * V;
+  const int row = block_row(), rows = block_rows();
+  const bool live = e < g.channels;
   const BlockAt b = block_at(g.p, row);
-  float sum[kSums] = {};
-  if (b.seq >= 0) {
-    float w[kConv], h[kHalo];
+  float sum[kSums][V] = {};
+  if (live && b.seq >= 0) {
+    const Act* xb = static_cast<const Act*>(g.x) + e + b.first * g.x_stride;
+    const Act* dyb = static_cast<const Act*>(g.dy) + e + b.first * g.dy_stride;
+    Act* dxb = static_cast<Act*>(g.dx) + e + int64_t(b.first) * g.channels;
+    const int s0 = packed_start(g.p, b.seq), s1 = packed_start(g.p, b.seq + 1);
+    const int have = min(b.count + kHalo, s1 - b.first);  // tokens of the block and behind it
+    Raw<Act, V> nx[kAhead], nd[kAhead];
 #pragma unroll
-    for (int k = 0; k < kConv; ++k) w[k] = g.w[int64_t(e) * kConv + k];
-    const float bias = g.b ? g.b[e] : 0.0f;
+    for (int j = 0; j < kAhead; ++j) {
+      nx[j].load(xb + min(j, have - 1) * g.x_stride);
+      nd[j].load(dyb + min(j, have - 1) * g.dy_stride);
+    }
+    Taps<V> taps;
+    taps.load(g, e);
+    float h[kHalo][V];
     if (b.begins) {
-      load_cache(g, b.seq, e, h);
+      load_cache<V>(g, b.seq, e, h);
     } else {
 #pragma unroll
-      for (int j = 0; j < kHalo; ++j) h[j] = load_act(x, (b.first - kHalo + j) * g.x_stride);
+      for (int j = 0; j < kHalo; ++j) {
+        Raw<Act, V> r;
+        r.load(xb + (j - kHalo) * g.x_stride);
+        r.get(h[j]);
+      }
     }
-    const int64_t s1 = packed_start(g.p, b.seq + 1), len = s1 - packed_start(g.p, b.seq);
     const float* dco = g.dcache_out ? g.dcache_out + int64_t(b.seq) * kHalo * g.channels + e : nullptr;
-    float s1d = 0.0f, s2d = 0.0f, s3d = 0.0f;  // s one, two and three tokens earlier
-    float begin[kHalo] = {};                   // s of the sequence's first tokens
-    for (int j = 0; j < b.count + kHalo; ++j) {
-      const int64_t t = int64_t(b.first) + j;
-      float s = 0.0f;
-      if (t < s1) {
-        const float v = load_act(x, t * g.x_stride);
-        s = load_act(dy, t * g.dy_stride);
-        if (g.silu) {
-          const float p = convolve(w, bias, h[0], h[1], h[2], v);
-          const float e2 = __builtin_amdgcn_exp2f(-fabsf(p) * kLog2e);
-          const float big = __builtin_amdgcn_rcpf(1.0f + e2), small = e2 * big;
-          const float on = p < 0.0f ? small : big, off = p < 0.0f ? big : small;
-          s *= on * fmaf(p, off, 1.0f);
-        }
-        if (j < b.count) {
-          sum[0] = fmaf(s, h[0], sum[0]);
-          sum[1] = fmaf(s, h[1], sum[1]);
-          sum[2] = fmaf(s, h[2], sum[2]);
-          sum[3] = fmaf(s, v, sum[3]);
-          sum[4] += s;
-        }
-        h[0] = h[1], h[1] = h[2], h[2] = v;
+    float s1d[V] = {}, s2d[V] = {}, s3d[V] = {};  // s one, two and three tokens earlier
+    float begin[kHalo][V] = {};                   // s of the sequence's first tokens
+    for (int j0 = 0; j0 < b.count + kHalo; j0 += kAhead) {
+      Raw<Act, V> cx[kAhead], cd[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) cx[j] = nx[j], cd[j] = nd[j];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        nx[j].load(xb + min(j0 + kAhead + j, have - 1) * g.x_stride);
+        nd[j].load(dyb + min(j0 + kAhead + j, have - 1) * g.dy_stride);
       }
-      if (j == 0) begin[0] = s;
-      if (j == 1) begin[1] = s;
-      if (j == 2) begin[2] = s;
-      if (j >= kHalo) {
-        float d = fmaf(w[3], s3d, fmaf(w[2], s2d, fmaf(w[1], s1d, w[0] * s)));
-        const int64_t at = t - kHalo, kept = at - (s1 - kHalo);  // which row of the final cache
-        if (dco && kept >= 0) d += dco[kept * g.channels];
-        store_act(dx, at * g.channels, d);
+#pragma unroll
+      for (int jj = 0; jj < kAhead; ++jj) {
+        const int j = j0 + jj;
+        float s[V] = {};
+        if (j < have) {
+          float v[V];
+          cx[jj].get(v);
+          cd[jj].get(s);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            if (g.silu) {
+              const float p = taps.at(i, h[0][i], h[1][i], h[2][i], v[i]);
+              // sigmoid(p) and 1 - sigmoid(p), neither from the other by a subtraction
+              const float x2 = __builtin_amdgcn_exp2f(-fabsf(p) * kLog2e);
+              const float big = __builtin_amdgcn_rcpf(1.0f + x2), small = x2 * big;
+              const float on = p < 0.0f ? small : big, off = p < 0.0f ? big : small;
+              s[i] *= on * fmaf(p, off, 1.0f);
+            }
+            if (j < b.count) {
+              sum[0][i] = fmaf(s[i], h[0][i], sum[0][i]);
+              sum[1][i] = fmaf(s[i], h[1][i], sum[1][i]);
+              sum[2][i] = fmaf(s[i], h[2][i], sum[2][i]);
+              sum[3][i] = fmaf(s[i], v[i], sum[3][i]);
+              sum[4][i] += s[i];
+            }
+            h[0][i] = h[1][i], h[1][i] = h[2][i], h[2][i] = v[i];
+          }
+        }
+        if (j0 == 0 && jj < kHalo)
+#pragma unroll
+          for (int i = 0; i < V; ++i) begin[jj][i] = s[i];
+        if (j >= kHalo && j < b.count + kHalo) {
+          const int kept = b.first + j - s1;  // which row of the final cache this token is
+          float d[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            d[i] = fmaf(taps.w[3][i], s3d[i],
+                        fmaf(taps.w[2][i], s2d[i], fmaf(taps.w[1][i], s1d[i], taps.w[0][i] * s[i])));
+            if (dco && kept >= 0) d[i] += dco[int64_t(kept) * g.channels + i];
+          }
+          Raw<Act, V>::store(dxb + int64_t(j - kHalo) * g.channels, d);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) s3d[i] = s2d[i], s2d[i] = s1d[i], s1d[i] = s[i];
       }
-      s3d = s2d, s2d = s1d, s1d = s;
     }
     if (b.begins && g.dcache_in) {
+      const int len = s1 - s0;
       float* out = g.dcache_in + int64_t(b.seq) * kHalo * g.channels + e;
 #pragma unroll
-      for (int c = 0; c < kHalo; ++c) {
-        float d = 0.0f;
+      for (int c = 0; c < kHalo; ++c)
 #pragma unroll
-        for (int k = 0; k <= c; ++k) d = fmaf(w[k], begin[c - k], d);
-        if (dco && c >= len) d += dco[(c - len) * g.channels];
-        out[int64_t(c) * g.channels] = d;
-      }
+        for (int i = 0; i < V; ++i) {
+          float d = 0.0f;
+#pragma unroll
+          for (int k = 0; k <= c; ++k) d = fmaf(taps.w[k][i], begin[c - k][i], d);
+          if (dco && c >= len) d += dco[int64_t(c - len) * g.channels + i];
+          out[int64_t(c) * g.channels + i] = d;
+        }
     }
   }
-  if (row < g.p.rows)
 #pragma unroll
-    for (int k = 0; k < kSums; ++k) g.partial[(int64_t(row) * kSums + k) * g.channels + e] = sum[k];
+  for (int k = 0; k < kSums; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) joined[wave][k * V + i][lane] = sum[k][i];
+  __syncthreads();
+  const int64_t part = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
+  for (int t = wave; t < kSums * V; t += kBackWaves) {
+    float a = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kBackWaves; ++w) a += joined[w][t][lane];
+    if (live) g.partial[(part * kSums + t / V) * g.channels + e + t % V] = a;
+  }
+  if (!live) return;
   if (g.dcache_in)
     for (int n = row; n < g.p.sequences; n += rows)
       if (packed_start(g.p, n) >= packed_start(g.p, n + 1))
-        for (int c = 0; c < kHalo; ++c) {
-          const int64_t at = (int64_t(n) * kHalo + c) * g.channels + e;
+        for (int c = 0; c < kHalo * V; ++c) {
+          const int64_t at = (int64_t(n) * kHalo + c / V) * g.channels + e + c % V;
           g.dcache_in[at] = g.dcache_out ? g.dcache_out[at] : 0.0f;
         }
+  const float zero[V] = {};
   for (int64_t t = int64_t(packed_start(g.p, g.p.sequences)) + row; t < g.p.tokens; t += rows)
-    store_act(dx, t * g.channels, 0.0f);
+    Raw<Act, V>::store(static_cast<Act*>(g.dx) + e + t * g.channels, zero);
 }
 
-__global__ __launch_bounds__(64) void conv_sum_kernel(ConvArgs g, int parts) {
-  const int e = blockIdx.x * 64 + threadIdx.x, k = blockIdx.y;
-  if (e >= g.channels) return;
+// Sums of the workgroups' parts in 64 bits: a lane a sum, four waves take every fourth part.
+__global__ __launch_bounds__(256) void conv_sum_kernel(ConvArgs g, int parts) {
+  __shared__ double sums[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.x * 64 + lane, k = blockIdx.y;
   double s = 0.0;
-  for (int j = 0; j < parts; ++j) s += g.partial[(int64_t(j) * kSums + k) * g.channels + e];
+  if (e < g.channels) {
+    const float* from = g.partial + int64_t(k) * g.channels + e;
+#pragma unroll 8
+    for (int j = wave; j < parts; j += 4) s += from[int64_t(j) * kSums * g.channels];
+  }
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave || e >= g.channels) return;
+  const float all = static_cast<float>(sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane]);
   if (k < kConv)
-    g.dw[int64_t(e) * kConv + k] = static_cast<float>(s);
+    g.dw[int64_t(e) * kConv + k] = all;
   else
-    g.db[e] = static_cast<float>(s);
+    g.db[e] = all;
 }
 
 template <typename Act>
@@ -212,7 +376,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs g) {
   float w[kConv];
 #pragma unroll
   for (int k = 0; k < kConv; ++k) w[k] = g.w[int64_t(e) * kConv + k];
-  float p = convolve(w, g.b ? g.b[e] : 0.0f, h0, h1, h2, v);
+  float p = fmaf(w[3], v, fmaf(w[2], h2, fmaf(w[1], h1, fmaf(w[0], h0, g.b ? g.b[e] : 0.0f))));
   if (g.silu) p = silu(p);
   store_act(static_cast<Act*>(g.y), int64_t(n) * g.channels + e, p);
   c[0] = h1, c[g.channels] = h2, c[2 * int64_t(g.channels)] = v;
@@ -256,6 +420,29 @@ dim3 block_grid(int channels, int width, int rows) {
   return dim3(static_cast<unsigned>((channels + width - 1) / width), (r + z - 1) / z, z);
 }
 
+// Parts that conv_back_kernel leaves: its workgroups of one channel group.
+int64_t back_parts(int64_t rows) {
+  const int64_t r = std::max<int64_t>((rows + kBackWaves - 1) / kBackWaves, 1), z = (r + 32767) / 32768;
+  return (r + z - 1) / z * z;
+}
+
+// Channels a lane takes at once: as many as width, rows and pointers keep aligned.
+bool vectors_ok(const ConvArgs& a, int v, size_t es, bool backward) {
+  return a.channels % v == 0 && a.x_stride % v == 0 && aligned_to(a.x, v * es) &&
+         (backward ? a.dy_stride % v == 0 && aligned_to(a.dy, v * es) && aligned_to(a.dx, v * es)
+                   : aligned_to(a.y, v * es));
+}
+
+template <typename Act, int V>
+void launch_conv(const ConvArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((conv_kernel<Act, V>), block_grid(a.channels, 64 * V, a.p.rows), dim3(64), 0, st, a);
+}
+template <typename Act, int V>
+void launch_back(const ConvArgs& a, hipStream_t st) {
+  const dim3 grid = block_grid(a.channels, 64 * V, (a.p.rows + kBackWaves - 1) / kBackWaves);
+  hipLaunchKernelGGL((conv_back_kernel<Act, V>), grid, dim3(64 * kBackWaves), 0, st, a);
+}
+
 }  // namespace
 }  // namespace axon
 
@@ -295,19 +482,21 @@ axon_status axon_causal_conv(const axon_conv_shape* shape, const void* x, const 
     return AXON_ERR_INVALID_ARGUMENT;
   a.cache_in = cache_in, a.in_slots = in_slots, a.in_count = s.cache_slots;
   a.cache_out = cache_out, a.out_slots = out_slots, a.out_count = s.out_slots, a.y = y;
-  const dim3 grid = block_grid(a.channels, 64, a.p.rows);
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (bf)
-    hipLaunchKernelGGL(conv_kernel<bf16_bits>, grid, dim3(64), 0, st, a);
+  if (!bf)
+    vectors_ok(a, 4, es, false) ? launch_conv<float, 4>(a, st) : launch_conv<float, 1>(a, st);
+  else if (vectors_ok(a, 4, es, false))
+    launch_conv<bf16_bits, 4>(a, st);
   else
-    hipLaunchKernelGGL(conv_kernel<float>, grid, dim3(64), 0, st, a);
+    vectors_ok(a, 2, es, false) ? launch_conv<bf16_bits, 2>(a, st) : launch_conv<bf16_bits, 1>(a, st);
   return hipGetLastError() == hipSuccess ? AXON_OK : AXON_ERR_HIP;
 }
 
 size_t axon_causal_conv_backward_workspace_bytes(const axon_conv_shape* shape) {
   if (axon::check_shape(shape, true) != AXON_OK) return 0;
   // as many block rows as packed sequences can have
-  return 4 * axon::kSums * size_t(shape->tokens / axon::kBlock + shape->sequences) *
+  return 4 * axon::kSums *
+         size_t(axon::back_parts(axon::packed_rows(shape->sequences, shape->tokens, true))) *
          size_t(shape->channels);
 }
 
@@ -350,14 +539,15 @@ axon_status axon_causal_conv_backward(const axon_conv_shape* shape, const void* 
   a.dy = dy, a.cache_in = cache_in, a.in_count = s.sequences;
   a.dcache_out = dcache_out, a.dx = dx, a.dw = dconv_w, a.db = dconv_b, a.dcache_in = dcache_in;
   a.partial = static_cast<float*>(workspace);
-  const dim3 grid = block_grid(a.channels, 64, a.p.rows);
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (bf)
-    hipLaunchKernelGGL(conv_back_kernel<bf16_bits>, grid, dim3(64), 0, st, a);
+  if (!bf)
+    vectors_ok(a, 4, es, true) ? launch_back<float, 4>(a, st) : launch_back<float, 1>(a, st);
+  else if (vectors_ok(a, 4, es, true))
+    launch_back<bf16_bits, 4>(a, st);
   else
-    hipLaunchKernelGGL(conv_back_kernel<float>, grid, dim3(64), 0, st, a);
-  hipLaunchKernelGGL(conv_sum_kernel, dim3((a.channels + 63) / 64, kSums), dim3(64), 0, st, a,
-                     a.p.rows);
+    vectors_ok(a, 2, es, true) ? launch_back<bf16_bits, 2>(a, st) : launch_back<bf16_bits, 1>(a, st);
+  hipLaunchKernelGGL(conv_sum_kernel, dim3((a.channels + 63) / 64, kSums), dim3(256), 0, st, a,
+                     static_cast<int>(back_parts(a.p.rows)));
   return hipGetLastError() == hipSuccess ? AXON_OK : AXON_ERR_HIP;
 }
 
