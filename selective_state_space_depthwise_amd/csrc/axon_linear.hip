@@ -19,8 +19,6 @@
 namespace axon {
 namespace {
 
-constexpr int kPer = 16;  // tokens of a wave
-
 struct LinearArgs {
   const void *x, *dt_raw, *in_raw, *dy;
   const float *A_log, *dt_bias, *in_bias;
@@ -41,60 +39,71 @@ struct LinearArgs {
   float* partial;  // (tiles, 3, channels)
   // What tiles tell each other (tiles, 64 groups): all bits set where nothing is told yet.
   uint32_t* ticket;  // null: one tile
-  uint64_t* sums;    // decay and own part of a tile
+  uint64_t* sums;    // log2 of the decay over a tile, and its own part
   uint32_t* carry;   // what leaves it
 };
 
-__device__ __forceinline__ float sigmoid_f32(float v) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
+// sigmoid(raw + bias), with the bias scaled: scaled_bias(bias).
+__device__ __forceinline__ float scaled_bias(float bias) { return -kLog2e * bias; }
+__device__ __forceinline__ float sigmoid_f32(float raw, float scaled) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(fmaf(raw, -kLog2e, scaled)));
 }
 
-// sigmoid(v) and 1 - sigmoid(v), each with a relative error of a few 2^-24.
-struct Sigmoid {
+// sigmoid(raw + bias) and 1 - sigmoid(raw + bias), each with a relative error of a few 2^-24; the first is
+// no less than 2^-126.
+struct Gate {
   float on, off;
-  __device__ __forceinline__ explicit Sigmoid(float v) {
-    const float e = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e);
-    const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
-    on = v < 0.0f ? small : big;
-    off = v < 0.0f ? big : small;
+  __device__ __forceinline__ Gate(float raw, float bias) {
+    const float x = __builtin_amdgcn_exp2f(fmaf(raw, -kLog2e, scaled_bias(bias)));
+    const float e = x > 8.5e37f ? 8.5e37f : x;
+    on = __builtin_amdgcn_rcpf(1.0f + e);
+    off = e * on;
   }
 };
-
-// How a token advances its state, in one number: a itself where a < 1/2, else expm1(log a) with the sign
-// bit set (also where it is zero). For a >= 1/2 the rounding of a would be a systematic error of the
-// decay, 2^-25 against 1 - a; below, h + expm1(log a) h would lose b beside a larger h.
-__device__ __forceinline__ float advance(float c, float h, float b) {
-  return fmaf(c, h, b) + (__float_as_int(c) < 0 ? h : 0.0f);
-}
-constexpr uint32_t kKeep = 0x80000000u;  // a = 1
-
 // softplus, NaN kept.
 __device__ __forceinline__ float softplus_nan(float v) { return v != v ? v : softplus_f32(v); }
 
-// a token's decay from its log a in base 2 (<= 0): expm1(log a) and the number that advance takes.
-// Below log2 a = -0.36, a - 1 cancels two bits at most; above it the series up to (log a)^6 / 720 leaves
-// a relative 5e-8.
-struct Decay {
-  float em1, c;
-  __device__ __forceinline__ explicit Decay(float l2) {
-    const float a = __builtin_amdgcn_exp2f(l2);
-    float p = fmaf(l2, 1.54035304e-4f, 1.33335581e-3f);
-    p = fmaf(l2, p, 9.61812911e-3f);
-    p = fmaf(l2, p, 5.55041087e-2f);
-    p = fmaf(l2, p, 2.40226507e-1f);
-    p = fmaf(l2, p, 6.93147181e-1f) * l2;
-    em1 = l2 > -0.36f ? p : a - 1.0f;
-    c = l2 < -1.0f ? a : __uint_as_float(__float_as_uint(em1) | kKeep);
-  }
-};
+// expm1(log a) from log2 a (<= 0) and a. Below log2 a = -0.36, a - 1 cancels two bits at most; above it
+// the series up to (log a)^6 / 720 leaves a relative 5e-8.
+__device__ __forceinline__ float expm1_of(float l2, float a) {
+  float p = fmaf(l2, 1.54035304e-4f, 1.33335581e-3f);
+  p = fmaf(l2, p, 9.61812911e-3f);
+  p = fmaf(l2, p, 5.55041087e-2f);
+  p = fmaf(l2, p, 2.40226507e-1f);
+  p = fmaf(l2, p, 6.93147181e-1f) * l2;
+  return l2 > -0.36f ? p : a - 1.0f;
+}
 
-__device__ __forceinline__ float input_factor(float em1, int input_scale) {
-  if (input_scale == AXON_INPUT_PLAIN) return 1.0f;
-  if (input_scale == AXON_INPUT_COMPLEMENT) return -em1;
+// A state over several tokens, from the sum of their log2 a and their own part: a h + part. Rounding a
+// close to 1 would be the same error for every block of a slow channel, 2^-25 against 1 - a, so that for
+// a >= 1/2 it is h + expm1(log a) h; below, that would lose the part beside a larger h. (Within a
+// block of 16 tokens the roundings of a are 16 2^-25 of h at most, and end with the block.) `carry` holds
+// a, or expm1(log a) with the sign bit set.
+__device__ __forceinline__ float carry_of(float l2) {
+  const float a = __builtin_amdgcn_exp2f(l2);
+  return l2 < -1.0f ? a : __uint_as_float(__float_as_uint(expm1_of(l2, a)) | 0x80000000u);
+}
+__device__ __forceinline__ float advance(float carry, float h, float part) {
+  return fmaf(carry, h, part) + (__float_as_int(carry) < 0 ? h : 0.0f);
+}
+
+// m from log2 a and a.
+template <int SCALE>
+__device__ __forceinline__ float input_factor(float l2, float a) {
+  if constexpr (SCALE == AXON_INPUT_PLAIN) return 1.0f;
+  const float em1 = expm1_of(l2, a);
+  if constexpr (SCALE == AXON_INPUT_COMPLEMENT) return -em1;
   return __builtin_amdgcn_sqrtf(-em1 * (2.0f + em1));
 }
 
-// A wave's share of a tile: kPer tokens of one block, one channel a lane.
+// log2 a; rate: -exp(A_log) log2 e.
+template <int GATE>
+__device__ __forceinline__ float log2_decay(float rate, float raw, float bias) {
+  if constexpr (GATE == AXON_LINEAR_SIGMOID) return rate * sigmoid_f32(raw, scaled_bias(bias));
+  return rate * softplus_nan(raw + bias);
+}
+
+// A wave's share of a tile: P tokens of one block, V channels a lane.
 struct Share {
   int seq, first, count;   // count 0: none; rows first .. first + count - 1
   int row;                 // of the block tables
@@ -102,68 +111,111 @@ struct Share {
   bool opens;              // holds the block's first token
 };
 
-__device__ __forceinline__ Share share_of(const Packed& p, int tile, int wave, int waves) {
-  const int at = (tile * waves + wave) * kPer;  // tokens in front, were all blocks full
+template <int P, int WAVES>
+__device__ __forceinline__ Share share_of(const Packed& p, int tile, int wave) {
+  const int at = (tile * WAVES + wave) * P;  // tokens in front, were all blocks full
   Share s{};
   s.row = at / kBlock;
   const int sub = at - s.row * kBlock;
   const BlockAt b = block_at(p, s.row);
   s.seq = b.seq;
   s.first = b.first + sub;
-  s.count = b.seq < 0 ? 0 : min(max(b.count - sub, 0), kPer);
+  s.count = b.seq < 0 ? 0 : min(max(b.count - sub, 0), P);
   s.opens = s.count > 0 && sub == 0;
   s.begins = s.opens && b.begins;
   s.ends = s.count > 0 && b.ends && sub + s.count == b.count;
   return s;
 }
 
-// kPer rows of a wave as loaded; rows behind the last repeat it, channels behind the last likewise.
-template <typename Act>
-struct Rows {
-  typename RawOf<Act>::type v[kPer];
-  __device__ __forceinline__ void load(const void* base, int64_t stride, const Share& s, int e) {
-    const rsrc_t r = make_rsrc(static_cast<const Act*>(base) + s.first * stride);
-    const uint32_t step = static_cast<uint32_t>(stride) * sizeof(Act), off = e * sizeof(Act);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const uint32_t row = static_cast<uint32_t>(min(j, s.count - 1)) * step;
-      if constexpr (sizeof(Act) == 4) v[j] = __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
-      else v[j] = __builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
-    }
+// P rows of a wave as loaded, V channels a lane; rows behind the last repeat it.
+template <typename Act, int V, int P>
+struct Rows;
+template <int P>
+struct Rows<float, 1, P> {
+  uint32_t v[P];
+  __device__ __forceinline__ void load1(int j, rsrc_t r, uint32_t off, uint32_t row) {
+    v[j] = __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
   }
-  __device__ __forceinline__ float operator[](int j) const { return widen(v[j]); }
+  __device__ __forceinline__ float at(int j, int) const { return __uint_as_float(v[j]); }
 };
+template <int P>
+struct Rows<bf16_bits, 1, P> {
+  uint16_t v[P];
+  __device__ __forceinline__ void load1(int j, rsrc_t r, uint32_t off, uint32_t row) {
+    v[j] = __builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
+  }
+  __device__ __forceinline__ float at(int j, int) const { return raw16_to_f32(v[j]); }
+};
+template <int P>
+struct Rows<bf16_bits, 2, P> {
+  uint32_t v[P];
+  __device__ __forceinline__ void load1(int j, rsrc_t r, uint32_t off, uint32_t row) {
+    v[j] = __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
+  }
+  __device__ __forceinline__ float at(int j, int i) const {
+    return __uint_as_float(i ? v[j] & 0xFFFF0000u : v[j] << 16);
+  }
+};
+template <typename Act, int V, int P>
+__device__ __forceinline__ void load_rows(Rows<Act, V, P>& to, const void* base, int64_t stride,
+                                          const Share& s, int e) {
+  const rsrc_t r = make_rsrc(static_cast<const Act*>(base) + s.first * stride);
+  const uint32_t step = static_cast<uint32_t>(stride) * sizeof(Act), off = e * sizeof(Act);
+#pragma unroll
+  for (int j = 0; j < P; ++j) to.load1(j, r, off, static_cast<uint32_t>(min(j, s.count - 1)) * step);
+}
+template <int V>
+__device__ __forceinline__ void store_vals(float* p, const float* v) {
+  p[0] = v[0];
+}
+template <int V>
+__device__ __forceinline__ void store_vals(bf16_bits* p, const float* v) {
+  if constexpr (V == 2)
+    *reinterpret_cast<uint32_t*>(p) =
+        static_cast<uint32_t>(f32_to_bf16(v[0])) | static_cast<uint32_t>(f32_to_bf16(v[1])) << 16;
+  else
+    p[0] = f32_to_bf16(v[0]);
+}
+
+template <typename Act, int V>
+__device__ __forceinline__ void store_row(rsrc_t r, uint32_t off, uint32_t row, const float* v) {
+  if constexpr (V == 2)
+    __builtin_amdgcn_raw_buffer_store_b32(
+        static_cast<uint32_t>(f32_to_bf16(v[0])) | static_cast<uint32_t>(f32_to_bf16(v[1])) << 16, r, off, row, 0);
+  else
+    store_buf_s<Act>(r, off, row, v[0]);
+}
 
 // What the tiles in front (behind, in the backward pass) hand on. A tile first publishes its own part
-// (decay A, h from zero), then, once it knows what enters it, what leaves it. A reader takes the
-// nearest tile that has published the latter and applies the parts between in the order in which
-// those tiles do it themselves, so that the result does not depend on who was first. Both are one
+// (the sum of its log2 a, and h from zero), then, once it knows what enters it, what leaves it. A reader
+// takes the nearest tile that has published the latter and applies the parts between in the order in
+// which those tiles do it themselves, so that the result does not depend on who was first. Both are one
 // atomic of the value itself: a NaN with all bits set stands for nothing, and stored NaNs are others.
 __device__ __forceinline__ uint32_t told(float v) {
   return v != v ? 0x7FC00000u : __float_as_uint(v);
 }
-__device__ __forceinline__ void tell_sums(uint64_t* p, float A, float h) {
-  __hip_atomic_store(p, static_cast<uint64_t>(told(h)) << 32 | told(A), __ATOMIC_RELAXED,
+__device__ __forceinline__ void tell_sums(uint64_t* p, float log, float h) {
+  __hip_atomic_store(p, static_cast<uint64_t>(told(h)) << 32 | told(log), __ATOMIC_RELAXED,
                      __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ void tell_carry(uint32_t* p, float h) {
   __hip_atomic_store(p, told(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-constexpr int kWindow = 8;  // tiles looked at
+constexpr int kWindow = 2;  // tiles looked at
 
 // Waits for what tile `from` hands on; tiles go down from it (DIR -1) or up (DIR 1), `left` of them.
-// Every tile's workgroup has started once a later ticket is out, and none of them waits for a later
-// one, so that the wait ends.
+// `column`: of the lane, among the `columns` of a tile. Every tile's workgroup has started once a later
+// ticket is out, and none of them waits for a later one, so that the wait ends.
 template <int DIR>
-__device__ __forceinline__ float hear(const LinearArgs& g, int from, int left, int64_t column) {
-  const int64_t width = int64_t(g.groups) * 64;
+__device__ __forceinline__ float hear(const LinearArgs& g, int from, int left, int64_t columns,
+                                      int64_t column) {
   const int n = min(left, kWindow);
   for (;;) {
     uint32_t c[kWindow];
     uint64_t s[kWindow];
 #pragma unroll
     for (int k = 0; k < kWindow; ++k) {
-      const int64_t at = int64_t(from + DIR * min(k, n - 1)) * width + column;
+      const int64_t at = (from + DIR * min(k, n - 1)) * columns + column;
       c[k] = __hip_atomic_load(g.carry + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       s[k] = __hip_atomic_load(g.sums + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
@@ -182,8 +234,8 @@ __device__ __forceinline__ float hear(const LinearArgs& g, int from, int left, i
       for (int k = kWindow - 1; k >= 0; --k) {
         if (k == found) h = __uint_as_float(c[k]);
         else if (k < found)
-          h = fmaf(__uint_as_float(static_cast<uint32_t>(s[k])), h,
-                   __uint_as_float(static_cast<uint32_t>(s[k] >> 32)));
+          h = advance(carry_of(__uint_as_float(static_cast<uint32_t>(s[k]))), h,
+                      __uint_as_float(static_cast<uint32_t>(s[k] >> 32)));
       }
       return h;
     }
@@ -206,116 +258,153 @@ __global__ __launch_bounds__(256) void linear_clear_kernel(uint4* p, int64_t cou
     p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
 }
 
-template <typename Act, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void linear_tile_kernel(LinearArgs g) {
+// What a tile's waves leave for each other: column (i, lane) is channel V lane + i of the group.
+template <int V, int WAVES>
+struct Parts {
+  float logs[WAVES][V][64], decay[WAVES][V][64], part[WAVES][V][64], enter[V][64];
+  int fresh[WAVES];  // nothing from in front (behind, backwards) reaches the wave's end
+};
+
+// One wave for each of V columns: the tile's own part is told, and what enters the tile is found.
+// alone: nothing enters; DIR as for hear.
+template <int DIR, int V, int WAVES>
+__device__ __forceinline__ void exchange(const LinearArgs& g, Parts<V, WAVES>& sh, int i, int lane,
+                                         int tile, int grp, bool alone, int left) {
+  float sum = 0.0f, own = 0.0f;
+  bool closed = false;  // a sequence begins (ends) in the tile: nothing passes through it
+#pragma unroll
+  for (int n = 0; n < WAVES; ++n) {
+    const int w = DIR < 0 ? n : WAVES - 1 - n;
+    const bool f = sh.fresh[w];
+    own = f ? sh.part[w][i][lane] : advance(sh.decay[w][i][lane], own, sh.part[w][i][lane]);
+    sum += sh.logs[w][i][lane];
+    closed |= f;
+  }
+  float before = 0.0f;
+  if (g.ticket) {
+    const int64_t columns = int64_t(g.groups) * V * 64, column = (int64_t(grp) * V + i) * 64 + lane;
+    const int64_t at = tile * columns + column;
+    if (closed || alone) tell_carry(g.carry + at, own);
+    else tell_sums(g.sums + at, sum, own);
+    if (!alone) {
+      before = hear<DIR>(g, tile + DIR, left, columns, column);
+      if (!closed) tell_carry(g.carry + at, advance(carry_of(sum), before, own));
+    }
+  }
+  sh.enter[i][lane] = before;
+}
+
+template <typename Act, int V, int P, int WAVES, int GATE, int SCALE>
+__global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g) {
+  static_assert(V <= WAVES, "a wave a column");
   __shared__ uint32_t ticket;
-  __shared__ float decay[WAVES][64], part[WAVES][64], enter[64];
-  __shared__ int fresh[WAVES];  // the wave begins a sequence
+  __shared__ Parts<V, WAVES> sh;
   const uint32_t t = take_ticket(g, &ticket);
   const int tile = t / g.groups, grp = t - tile * g.groups;
   if (tile >= g.tiles) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const bool in_range = grp * 64 + lane < g.channels;
-  const int e = min(grp * 64 + lane, g.channels - 1);
-  const Share s = share_of(g.p, tile, wave, WAVES);
-  float c[kPer], b[kPer];
-  float h0 = 0.0f;  // what enters the wave, where it begins a sequence
-  float L = 0.0f, h = 0.0f;
+  const bool in_range = (grp * 64 + lane) * V < g.channels;
+  const int e = min((grp * 64 + lane) * V, g.channels - V);
+  const Share s = share_of<P, WAVES>(g.p, tile, wave);
+  float a[P][V], b[P][V];
+  float h0[V] = {};  // what enters the wave, where it begins a sequence
+  float L[V] = {}, h[V] = {};
   if (s.count > 0) {
-    Rows<Act> x, raw, in;
-    raw.load(g.dt_raw, g.dt_stride, s, e);
-    x.load(g.x, g.x_stride, s, e);
-    if (g.in_raw) in.load(g.in_raw, g.in_stride, s, e);
+    Rows<Act, V, P> x, raw, in;
+    load_rows(raw, g.dt_raw, g.dt_stride, s, e);
+    load_rows(x, g.x, g.x_stride, s, e);
+    if (g.in_raw) load_rows(in, g.in_raw, g.in_stride, s, e);
     if (s.begins && g.state_in) {
-      const int64_t slot = g.in_slots ? g.in_slots[s.seq] : s.seq;
-      if (slot >= 0 && slot < g.in_count) h0 = g.state_in[slot * g.channels + e];
+      const int64_t slot = g.in_slots ? table_at(g.in_slots, s.seq) : s.seq;
+      if (slot >= 0 && slot < g.in_count)
+#pragma unroll
+        for (int i = 0; i < V; ++i) h0[i] = g.state_in[slot * g.channels + e + i];
     }
-    const float rate = -expf(g.A_log[e]) * kLog2e;
-    const float bias = g.dt_bias ? g.dt_bias[e] : 0.0f;
-    if (g.gate == AXON_LINEAR_SIGMOID) {
+    float rate[V], bias[V], ib[V];
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) c[j] = rate * sigmoid_f32(raw[j] + bias);
-    } else {
+    for (int i = 0; i < V; ++i) {
+      rate[i] = -expf(g.A_log[e + i]) * kLog2e;
+      bias[i] = g.dt_bias ? g.dt_bias[e + i] : 0.0f;
+      ib[i] = scaled_bias(g.in_raw && g.in_bias ? g.in_bias[e + i] : 0.0f);
+    }
+    // a: log2 a first
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) c[j] = rate * softplus_nan(raw[j] + bias);
+    for (int j = 0; j < P; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) a[j][i] = log2_decay<GATE>(rate[i], raw.at(j, i), bias[i]);
+    if (s.count < P) {
+#pragma unroll
+      for (int j = 0; j < P; ++j)
+        if (j >= s.count)
+#pragma unroll
+          for (int i = 0; i < V; ++i) a[j][i] = 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      L += j < s.count ? c[j] : 0.0f;
-      const Decay d(c[j]);
-      c[j] = d.c;
-      b[j] = d.em1;
-    }
-    if (g.input_scale == AXON_INPUT_SQRT) {
+    for (int j = 0; j < P; ++j)
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) b[j] = x[j] * input_factor(b[j], AXON_INPUT_SQRT);
-    } else if (g.input_scale == AXON_INPUT_COMPLEMENT) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) b[j] = x[j] * -b[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) b[j] = x[j];
-    }
+      for (int i = 0; i < V; ++i) {
+        L[i] += a[j][i];
+        const float l2 = a[j][i];
+        a[j][i] = __builtin_amdgcn_exp2f(l2);
+        b[j][i] = x.at(j, i) * input_factor<SCALE>(l2, a[j][i]);
+      }
     if (g.in_raw) {
-      const float ib = g.in_bias ? g.in_bias[e] : 0.0f;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) b[j] *= sigmoid_f32(in[j] + ib);
+      for (int j = 0; j < P; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          b[j][i] *= sigmoid_f32(in.at(j, i), ib[i]);
+        }
     }
-    if (s.count < kPer) {
+    if (s.count < P) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (j >= s.count) c[j] = __uint_as_float(kKeep), b[j] = 0.0f;
+      for (int j = 0; j < P; ++j)
+        if (j >= s.count)
+#pragma unroll
+          for (int i = 0; i < V; ++i) b[j][i] = 0.0f;
     }
-    h = h0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) h = advance(c[j], h, b[j]);
+    for (int i = 0; i < V; ++i) h[i] = h0[i];
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[i] = fmaf(a[j][i], h[i], b[j][i]);
   }
-  decay[wave][lane] = __builtin_amdgcn_exp2f(L);
-  part[wave][lane] = h;
-  if (lane == 0) fresh[wave] = s.begins;
-  __syncthreads();
-  if (wave == 0) {
-    // The tile's own part, then what enters it.
-    float A = 1.0f, own = 0.0f;
-    bool closed = false;  // a sequence begins in the tile: nothing from in front leaves it
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      const bool f = fresh[w];
-      own = f ? part[w][lane] : fmaf(decay[w][lane], own, part[w][lane]);
-      A *= decay[w][lane];
-      closed |= f;
-    }
-    float before = 0.0f;
-    if (g.ticket) {
-      const int64_t at = int64_t(t) * 64 + lane;
-      const bool alone = s.begins || tile == 0;
-      if (closed || alone) tell_carry(g.carry + at, own);
-      else tell_sums(g.sums + at, A, own);
-      if (!alone) {
-        before = hear<-1>(g, tile - 1, tile, grp * 64 + lane);
-        if (!closed) tell_carry(g.carry + at, fmaf(A, before, own));
-      }
-    }
-    enter[lane] = before;
+  for (int i = 0; i < V; ++i) {
+    sh.logs[wave][i][lane] = L[i];
+    sh.decay[wave][i][lane] = carry_of(L[i]);
+    sh.part[wave][i][lane] = h[i];
+  }
+  if (lane == 0) sh.fresh[wave] = s.begins;
+  __syncthreads();
+  if (wave < V) {
+    const bool alone = tile == 0 || share_of<P, WAVES>(g.p, tile, 0).begins;
+    exchange<-1, V, WAVES>(g, sh, wave, lane, tile, grp, alone, tile);
   }
   __syncthreads();
-  if (s.count > 0) {
-    h = enter[lane];
-    for (int w = 0; w < wave; ++w)
-      h = fresh[w] ? part[w][lane] : fmaf(decay[w][lane], h, part[w][lane]);
-    if (s.begins) h = h0;
-    if (in_range) {
-      if (s.opens && g.checkpoints) g.checkpoints[int64_t(s.row) * g.channels + e] = h;
-      Act* y = static_cast<Act*>(g.y) + int64_t(s.first) * g.channels + e;
+  if (s.count > 0 && in_range) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        h = advance(c[j], h, b[j]);
-        if (j < s.count) store_act(y, int64_t(j) * g.channels, h);
-      }
-      if (s.ends && g.state_out) {
-        const int64_t slot = g.out_slots ? g.out_slots[s.seq] : s.seq;
-        if (slot >= 0 && slot < g.out_count) g.state_out[slot * g.channels + e] = h;
-      }
+    for (int i = 0; i < V; ++i) {
+      h[i] = sh.enter[i][lane];
+      for (int w = 0; w < wave; ++w)
+        h[i] = sh.fresh[w] ? sh.part[w][i][lane] : advance(sh.decay[w][i][lane], h[i], sh.part[w][i][lane]);
+      if (s.begins) h[i] = h0[i];
+      if (s.opens && g.checkpoints) g.checkpoints[int64_t(s.row) * g.channels + e + i] = h[i];
+    }
+    const rsrc_t y = make_rsrc(static_cast<Act*>(g.y) + int64_t(s.first) * g.channels);
+    const uint32_t step = static_cast<uint32_t>(g.channels) * sizeof(Act), off = e * sizeof(Act);
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[i] = fmaf(a[j][i], h[i], b[j][i]);
+      if (j < s.count) store_row<Act, V>(y, off, j * step, h);
+    }
+    if (s.ends && g.state_out) {
+      const int64_t slot = g.out_slots ? table_at(g.out_slots, s.seq) : s.seq;
+      if (slot >= 0 && slot < g.out_count)
+#pragma unroll
+        for (int i = 0; i < V; ++i) g.state_out[slot * g.channels + e + i] = h[i];
     }
   }
   if (!in_range) return;
@@ -324,205 +413,216 @@ __global__ __launch_bounds__(64 * WAVES) void linear_tile_kernel(LinearArgs g) {
     if (!g.state_out || packed_start(g.p, n) < packed_start(g.p, n + 1)) continue;
     const int64_t from = g.in_slots ? g.in_slots[n] : n, to = g.out_slots ? g.out_slots[n] : n;
     if (to >= 0 && to < g.out_count)
-      g.state_out[to * g.channels + e] =
-          g.state_in && from >= 0 && from < g.in_count ? g.state_in[from * g.channels + e] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        g.state_out[to * g.channels + e + i] =
+            g.state_in && from >= 0 && from < g.in_count ? g.state_in[from * g.channels + e + i] : 0.0f;
   }
-  if (g.clear_behind)
+  if (g.clear_behind) {
+    const float zero[V] = {};
     for (int64_t r = int64_t(packed_start(g.p, g.p.sequences)) + tile * WAVES + wave;
          r < g.p.tokens; r += int64_t(g.tiles) * WAVES)
-      store_act(static_cast<Act*>(g.y), r * g.channels + e, 0.0f);
+      store_vals<V>(static_cast<Act*>(g.y) + r * g.channels + e, zero);
+  }
 }
 
 // The same from the last tile to the first. A wave finds its block's states again from the block's
 // checkpoint and the parts of the waves in front of it.
-template <typename Act, int WAVES>
+template <typename Act, int V, int P, int WAVES, int GATE, int SCALE>
 __global__ __launch_bounds__(64 * WAVES) void linear_tile_back_kernel(LinearArgs g) {
-  static_assert(WAVES * kPer % kBlock == 0, "a tile holds whole blocks");
-  constexpr int kBlockWaves = kBlock / kPer;
+  static_assert(WAVES * P % kBlock == 0 && V <= WAVES, "a tile holds whole blocks");
+  constexpr int kBlockWaves = kBlock / P;
   __shared__ uint32_t ticket;
-  __shared__ float decay[WAVES][64], part[WAVES][64], back[WAVES][64], enter[64];
-  __shared__ int fresh[WAVES];  // the wave ends a sequence
+  __shared__ Parts<V, WAVES> sh;
+  __shared__ float states[WAVES][V][64], totals[WAVES][3][V][64];
   const uint32_t t = take_ticket(g, &ticket);
   const int turn = t / g.groups, grp = t - turn * g.groups;
   if (turn >= g.tiles) return;
   const int tile = g.tiles - 1 - turn;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const bool in_range = grp * 64 + lane < g.channels;
-  const int e = min(grp * 64 + lane, g.channels - 1);
-  const Share s = share_of(g.p, tile, wave, WAVES);
-  float c[kPer], v[kPer], vi[kPer], xs[kPer], dy[kPer], hb[kPer];
-  float L = 0.0f, h = 0.0f, k = 0.0f, k0 = 0.0f, rate = 0.0f;
+  const bool in_range = (grp * 64 + lane) * V < g.channels;
+  const int e = min((grp * 64 + lane) * V, g.channels - V);
+  const Share s = share_of<P, WAVES>(g.p, tile, wave);
+  // Per token: a L, a, what the gate's slope makes of G, the input's gate, u (1 - gate), m, the second term
+  // of G; hb holds the inputs m u first and the states in front of the tokens then.
+  Rows<Act, V, P> d;
+  float aL[P][V], av[P][V], slope[P][V], on[P][V], z[P][V], m[P][V], w2[P][V], hb[P][V];
+  float L[V] = {}, h[V] = {}, k[V] = {}, k0[V] = {}, point[V] = {};
   if (s.count > 0) {
-    Rows<Act> x, raw, in, d;
-    raw.load(g.dt_raw, g.dt_stride, s, e);
-    x.load(g.x, g.x_stride, s, e);
-    if (g.in_raw) in.load(g.in_raw, g.in_stride, s, e);
-    d.load(g.dy, g.dy_stride, s, e);
-    if (s.opens) h = g.points[int64_t(s.row) * g.channels + e];
-    if (s.ends && g.dstate_out) k0 = g.dstate_out[int64_t(s.seq) * g.channels + e];
-    rate = -expf(g.A_log[e]);
-    const float bias = g.dt_bias ? g.dt_bias[e] : 0.0f;
-    const float ib = g.in_raw && g.in_bias ? g.in_bias[e] : 0.0f;
+    Rows<Act, V, P> x, raw, in;
+    load_rows(raw, g.dt_raw, g.dt_stride, s, e);
+    load_rows(x, g.x, g.x_stride, s, e);
+    if (g.in_raw) load_rows(in, g.in_raw, g.in_stride, s, e);
+    load_rows(d, g.dy, g.dy_stride, s, e);
+    float rate[V], bias[V], ib[V];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      v[j] = raw[j] + bias;
-      xs[j] = x[j];
-      dy[j] = d[j];
-      vi[j] = g.in_raw ? in[j] + ib : 0.0f;
+    for (int i = 0; i < V; ++i) {
+      if (s.opens) point[i] = g.points[int64_t(s.row) * g.channels + e + i];
+      if (s.ends && g.dstate_out) k0[i] = g.dstate_out[int64_t(s.seq) * g.channels + e + i];
+      rate[i] = -expf(g.A_log[e + i]) * kLog2e;
+      bias[i] = g.dt_bias ? g.dt_bias[e + i] : 0.0f;
+      ib[i] = g.in_raw && g.in_bias ? g.in_bias[e + i] : 0.0f;
     }
-    const float rate2 = rate * kLog2e;
-    if (g.gate == AXON_LINEAR_SIGMOID) {
+    if (g.in_raw) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) c[j] = rate2 * sigmoid_f32(v[j]);
+      for (int j = 0; j < P; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const Gate q(in.at(j, i), ib[i]);
+          on[j][i] = q.on;
+          z[j][i] = x.at(j, i) * q.on * q.off;
+        }
     } else {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) c[j] = rate2 * softplus_nan(v[j]);
+      for (int j = 0; j < P; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) on[j][i] = 1.0f, z[j][i] = 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      L += j < s.count ? c[j] : 0.0f;
-      const Decay t2(c[j]);
-      c[j] = t2.c;
-      float u = xs[j] * input_factor(t2.em1, g.input_scale);
-      if (g.in_raw) u *= sigmoid_f32(vi[j]);
-      hb[j] = u;
-    }
-    if (s.count < kPer) {
+    for (int i = 0; i < V; ++i) h[i] = point[i];
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (j >= s.count) c[j] = __uint_as_float(kKeep), hb[j] = 0.0f, dy[j] = 0.0f;
-    }
-    // hb holds the inputs still: the wave's own part of its last state
+    for (int j = 0; j < P; ++j)
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) h = advance(c[j], h, hb[j]);
-    k = k0;
-#pragma unroll
-    for (int j = kPer - 1; j >= 0; --j) {
-      k += dy[j];
-      k = advance(c[j], k, 0.0f);
-    }
-  }
-  decay[wave][lane] = __builtin_amdgcn_exp2f(L);
-  part[wave][lane] = h;
-  back[wave][lane] = k;
-  if (lane == 0) fresh[wave] = s.ends;
-  __syncthreads();
-  if (wave == WAVES - 1) {
-    float A = 1.0f, own = 0.0f;
-    bool closed = false;
-#pragma unroll
-    for (int w = WAVES - 1; w >= 0; --w) {
-      const bool f = fresh[w];
-      own = f ? back[w][lane] : fmaf(decay[w][lane], own, back[w][lane]);
-      A *= decay[w][lane];
-      closed |= f;
-    }
-    float behind = 0.0f;
-    if (g.ticket) {
-      const int64_t at = (int64_t(tile) * g.groups + grp) * 64 + lane;
-      const bool alone = s.ends || turn == 0;
-      if (closed || alone) tell_carry(g.carry + at, own);
-      else tell_sums(g.sums + at, A, own);
-      if (!alone) {
-        behind = hear<1>(g, tile + 1, turn, grp * 64 + lane);
-        if (!closed) tell_carry(g.carry + at, fmaf(A, behind, own));
+      for (int i = 0; i < V; ++i) {
+        const bool held = j < s.count;
+        float l2;
+        if constexpr (GATE == AXON_LINEAR_SIGMOID) {
+          const Gate q(raw.at(j, i), bias[i]);
+          l2 = rate[i] * q.on;
+          slope[j][i] = q.off;
+        } else {
+          const float v = raw.at(j, i) + bias[i], sp = softplus_nan(v);
+          l2 = rate[i] * sp;
+          slope[j][i] = v < -20.0f ? 1.0f : sigmoid_f32(v, 0.0f) * __builtin_amdgcn_rcpf(sp);
+        }
+        l2 = held ? l2 : 0.0f;
+        L[i] += l2;
+        const float a = __builtin_amdgcn_exp2f(l2), u = held ? x.at(j, i) * on[j][i] : 0.0f;
+        av[j][i] = a;
+        aL[j][i] = a * (fmaxf(l2, -200.0f) * kLn2);  // 0 for log a = -inf
+        if constexpr (SCALE == AXON_INPUT_SQRT) {
+          const float em1 = expm1_of(l2, a), q = -em1 * (2.0f + em1);
+          const float rs = q == 0.0f ? 0.0f : __builtin_amdgcn_rsqf(q);
+          m[j][i] = q * rs;
+          w2[j][i] = a * u * rs;
+        } else if constexpr (SCALE == AXON_INPUT_COMPLEMENT) {
+          m[j][i] = -expm1_of(l2, a);
+          w2[j][i] = u;
+        } else {
+          m[j][i] = 1.0f;
+          w2[j][i] = 0.0f;
+        }
+        hb[j][i] = m[j][i] * u;
+        h[i] = fmaf(a, h[i], hb[j][i]);
       }
-    }
-    enter[lane] = behind;
+#pragma unroll
+    for (int i = 0; i < V; ++i) k[i] = k0[i];
+#pragma unroll
+    for (int j = P - 1; j >= 0; --j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) k[i] = av[j][i] * (k[i] + (j < s.count ? d.at(j, i) : 0.0f));
   }
-  float sA = 0.0f, sdt = 0.0f, sin = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    sh.logs[wave][i][lane] = L[i];
+    sh.decay[wave][i][lane] = carry_of(L[i]);
+    sh.part[wave][i][lane] = k[i];
+    states[wave][i][lane] = h[i];
+  }
+  if (lane == 0) sh.fresh[wave] = s.ends;
+  __syncthreads();
+  if (wave < V) {
+    const bool alone = turn == 0 || share_of<P, WAVES>(g.p, tile, WAVES - 1).ends;
+    exchange<1, V, WAVES>(g, sh, wave, lane, tile, grp, alone, turn);
+  }
   // The states in front of the wave's tokens.
   if (s.count > 0) {
     const int w0 = wave / kBlockWaves * kBlockWaves;
-    h = s.opens ? g.points[int64_t(s.row) * g.channels + e] : part[w0][lane];
-    for (int w = w0 + 1; w < wave; ++w) h = fmaf(decay[w][lane], h, part[w][lane]);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const float u = hb[j];
-      hb[j] = h;
-      h = advance(c[j], h, u);
+    for (int i = 0; i < V; ++i) {
+      h[i] = s.opens ? point[i] : states[w0][i][lane];
+      for (int w = w0 + 1; w < wave; ++w) h[i] = advance(sh.decay[w][i][lane], h[i], states[w][i][lane]);
     }
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float u = hb[j][i];
+        hb[j][i] = h[i];
+        h[i] = fmaf(av[j][i], h[i], u);
+      }
   }
   __syncthreads();
+  float sA[V] = {}, sdt[V] = {}, sin[V] = {};
   if (s.count > 0) {
-    k = enter[lane];
-    for (int w = WAVES - 1; w > wave; --w)
-      k = fresh[w] ? back[w][lane] : fmaf(decay[w][lane], k, back[w][lane]);
-    if (s.ends) k = k0;
-    const int64_t first = int64_t(s.first) * g.channels + e;
-    Act* dx = static_cast<Act*>(g.dx) + first;
-    Act* ddt = static_cast<Act*>(g.ddt_raw) + first;
-    Act* din = static_cast<Act*>(g.din_raw) + first;
 #pragma unroll
-    for (int j = kPer - 1; j >= 0; --j) {
+    for (int i = 0; i < V; ++i) {
+      k[i] = sh.enter[i][lane];
+      for (int w = WAVES - 1; w > wave; --w)
+        k[i] = sh.fresh[w] ? sh.part[w][i][lane] : advance(sh.decay[w][i][lane], k[i], sh.part[w][i][lane]);
+      if (s.ends) k[i] = k0[i];
+    }
+    const int64_t first = int64_t(s.first) * g.channels;
+    const rsrc_t dx = make_rsrc(static_cast<Act*>(g.dx) + first), ddt = make_rsrc(static_cast<Act*>(g.ddt_raw) + first);
+    const rsrc_t din = make_rsrc(static_cast<Act*>(g.din_raw) + (g.in_raw ? first : 0));
+    const uint32_t step = static_cast<uint32_t>(g.channels) * sizeof(Act), off = e * sizeof(Act);
+#pragma unroll
+    for (int j = P - 1; j >= 0; --j) {
       if (j >= s.count) continue;
-      const bool slow = __float_as_int(c[j]) < 0;
-      const float a = slow ? 1.0f + c[j] : c[j], em1 = slow ? c[j] : c[j] - 1.0f;
-      const float gt = dy[j] + k;
-      k = advance(c[j], gt, 0.0f);
-      float Lj, slope;
-      if (g.gate == AXON_LINEAR_SIGMOID) {
-        const Sigmoid sg(v[j]);
-        Lj = rate * sg.on;
-        slope = sg.off;
-      } else {
-        const float sp = softplus_nan(v[j]);
-        Lj = rate * sp;
-        slope = v[j] < -20.0f ? 1.0f : sigmoid_f32(v[j]) / sp;
+      float odt[V], ox[V], oin[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float gt = d.at(j, i) + k[i];
+        k[i] = av[j][i] * gt;
+        const float G = gt * aL[j][i] * (hb[j][i] - w2[j][i]), du = gt * m[j][i];
+        odt[i] = G * slope[j][i];
+        ox[i] = du * on[j][i];
+        oin[i] = du * z[j][i];
+        sA[i] += G;
+        sdt[i] += odt[i];
+        sin[i] += oin[i];
       }
-      const Sigmoid i(vi[j]);
-      const float u = g.in_raw ? xs[j] * i.on : xs[j];
-      const float aL = a == 0.0f ? 0.0f : a * Lj;
-      float G = aL * hb[j], m = 1.0f;
-      if (g.input_scale == AXON_INPUT_COMPLEMENT) {
-        m = -em1;
-        G -= aL * u;
-      } else if (g.input_scale == AXON_INPUT_SQRT) {
-        m = input_factor(em1, AXON_INPUT_SQRT);
-        if (m != 0.0f) G -= a * (aL * u) * __builtin_amdgcn_rcpf(m);
-      }
-      G *= gt;
-      const float draw = G * slope, du = gt * m;
-      sA += G;
-      sdt += draw;
       if (in_range) {
-        const int64_t at = int64_t(j) * g.channels;
-        store_act(ddt, at, draw);
-        store_act(dx, at, g.in_raw ? du * i.on : du);
-        if (g.in_raw) {
-          const float di = du * xs[j] * i.on * i.off;
-          sin += di;
-          store_act(din, at, di);
-        }
+        store_row<Act, V>(ddt, off, j * step, odt);
+        store_row<Act, V>(dx, off, j * step, ox);
+        if (g.in_raw) store_row<Act, V>(din, off, j * step, oin);
       }
     }
-    if (s.begins && g.dstate_in && in_range) g.dstate_in[int64_t(s.seq) * g.channels + e] = k;
+    if (s.begins && g.dstate_in && in_range)
+#pragma unroll
+      for (int i = 0; i < V; ++i) g.dstate_in[int64_t(s.seq) * g.channels + e + i] = k[i];
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    totals[wave][0][i][lane] = sA[i];
+    totals[wave][1][i][lane] = sdt[i];
+    totals[wave][2][i][lane] = sin[i];
   }
   __syncthreads();
-  decay[wave][lane] = sA;
-  part[wave][lane] = sdt;
-  back[wave][lane] = sin;
-  __syncthreads();
-  if (wave < 3 && in_range) {
-    const float* from = wave == 0 ? &decay[0][lane] : wave == 1 ? &part[0][lane] : &back[0][lane];
+  for (int q = wave; q < 3 * V; q += WAVES) {
+    const int which = q / V, i = q - which * V;
     float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) sum += from[w * 64];
-    g.partial[(int64_t(tile) * 3 + wave) * g.channels + e] = sum;
+    for (int w = 0; w < WAVES; ++w) sum += totals[w][which][i][lane];
+    if (in_range) g.partial[(int64_t(tile) * 3 + which) * g.channels + e + i] = sum;
   }
   if (!in_range) return;
   if (g.dstate_in)
     for (int n = tile * WAVES + wave; n < g.p.sequences; n += g.tiles * WAVES) {
       if (packed_start(g.p, n) < packed_start(g.p, n + 1)) continue;
-      const int64_t at = int64_t(n) * g.channels + e;
-      g.dstate_in[at] = g.dstate_out ? g.dstate_out[at] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int64_t at = int64_t(n) * g.channels + e + i;
+        g.dstate_in[at] = g.dstate_out ? g.dstate_out[at] : 0.0f;
+      }
     }
+  const float zero[V] = {};
   for (int64_t r = int64_t(packed_start(g.p, g.p.sequences)) + tile * WAVES + wave; r < g.p.tokens;
        r += int64_t(g.tiles) * WAVES) {
     const int64_t at = r * g.channels + e;
-    store_act(static_cast<Act*>(g.dx), at, 0.0f);
-    store_act(static_cast<Act*>(g.ddt_raw), at, 0.0f);
-    if (g.in_raw) store_act(static_cast<Act*>(g.din_raw), at, 0.0f);
+    store_vals<V>(static_cast<Act*>(g.dx) + at, zero);
+    store_vals<V>(static_cast<Act*>(g.ddt_raw) + at, zero);
+    if (g.in_raw) store_vals<V>(static_cast<Act*>(g.din_raw) + at, zero);
   }
 }
 
@@ -533,6 +633,7 @@ __global__ __launch_bounds__(256) void linear_sum_kernel(LinearArgs g, int parts
   const int e = blockIdx.x * 64 + lane, which = blockIdx.y;
   double s = 0.0;
   if (e < g.channels)
+#pragma unroll 8
     for (int j = wave; j < parts; j += 4)
       s += g.partial[(int64_t(j) * 3 + which) * g.channels + e];
   sums[wave][lane] = s;
@@ -552,11 +653,15 @@ __global__ __launch_bounds__(256) void linear_step_kernel(LinearArgs g) {
   const float v =
       load_act(static_cast<const Act*>(g.dt_raw), n * g.dt_stride + e) + (g.dt_bias ? g.dt_bias[e] : 0.0f);
   float u = load_act(static_cast<const Act*>(g.x), n * g.x_stride + e);
-  const float dt = g.gate == AXON_LINEAR_SIGMOID ? sigmoid_f32(v) : softplus_nan(v);
-  const Decay d(-expf(g.A_log[e]) * kLog2e * dt);
-  if (in) u *= sigmoid_f32(load_act(in, n * g.in_stride + e) + (g.in_bias ? g.in_bias[e] : 0.0f));
+  const float rate = -expf(g.A_log[e]) * kLog2e;
+  const float l2 = g.gate == AXON_LINEAR_SIGMOID ? log2_decay<AXON_LINEAR_SIGMOID>(rate, v, 0.0f)
+                                                 : log2_decay<AXON_LINEAR_SOFTPLUS>(rate, v, 0.0f);
+  const float a = __builtin_amdgcn_exp2f(l2);
+  if (g.input_scale == AXON_INPUT_COMPLEMENT) u *= input_factor<AXON_INPUT_COMPLEMENT>(l2, a);
+  if (g.input_scale == AXON_INPUT_SQRT) u *= input_factor<AXON_INPUT_SQRT>(l2, a);
+  if (in) u *= sigmoid_f32(load_act(in, n * g.in_stride + e) + (g.in_bias ? g.in_bias[e] : 0.0f), 0.0f);
   float* state = g.state_out + slot * g.channels + e;
-  const float h = advance(d.c, *state, input_factor(d.em1, g.input_scale) * u);
+  const float h = advance(carry_of(l2), *state, u);
   *state = h;
   store_act(static_cast<Act*>(g.y), int64_t(n) * g.channels + e, h);
 }
@@ -615,24 +720,30 @@ size_t tables_bytes(const Packed& p) {
   return p.starts ? 4 * (2 * (size_t(p.sequences) + 1) + 2 * size_t(p.rows)) : 0;
 }
 
-constexpr int kWaves = 8;
-constexpr int kBackWaves = 8;
+// Tokens a wave and waves a tile, by channels a lane.
+constexpr int kTokens = 16, kWaves = 8;          // one channel
+constexpr int kTokens2 = 8, kWaves2 = 16;        // two
+constexpr int kBackTokens = 16, kBackWaves = 4;  // one, backwards
+constexpr int kBackTokens2 = 8, kBackWaves2 = 8;
 
 // Tiles, and what of the workspace they use.
 struct Plan {
+  int vec;  // channels a lane
   int64_t tiles, groups;
   size_t sums, carry, ticket, chain;  // offsets and bytes of what tiles tell each other; chain 0: nothing
   size_t bytes;
 };
 
-Plan plan_linear(const axon_linear_shape& s, bool packed, int waves, bool backward) {
+Plan plan_linear(const axon_linear_shape& s, bool packed, int vec, bool backward) {
   Plan p{};
+  p.vec = vec;
   // rows of the tables, or sequences without tokens, at least one tile
   const int64_t rows = std::max<int64_t>(packed_rows(s.sequences, s.tokens, packed), 1);
-  const int64_t blocks = waves * kPer / kBlock;
+  const int64_t blocks = (backward ? vec == 2 ? kBackTokens2 * kBackWaves2 : kBackTokens * kBackWaves
+                                   : vec == 2 ? kTokens2 * kWaves2 : kTokens * kWaves) / kBlock;
   p.tiles = (rows + blocks - 1) / blocks;
-  p.groups = (s.channels + 63) / 64;
-  const size_t cells = size_t(p.tiles) * size_t(p.groups) * 64;
+  p.groups = (s.channels + 64 * vec - 1) / (64 * vec);
+  const size_t cells = size_t(p.tiles) * size_t(p.groups) * 64 * size_t(vec);
   if (p.tiles > 1) {
     p.sums = 0;
     p.carry = 8 * cells;
@@ -643,9 +754,19 @@ Plan plan_linear(const axon_linear_shape& s, bool packed, int waves, bool backwa
   return p;
 }
 
-// The workspace holds for either kind of batch: a uniform one has no more blocks than a packed one can.
-size_t workspace_of(const axon_linear_shape& s, int waves, bool backward) {
-  return plan_linear(s, true, waves, backward).bytes;
+// The workspace holds for either kind of batch (a uniform one has no more blocks than a packed one can)
+// and any alignment.
+size_t workspace_of(const axon_linear_shape& s, bool backward) {
+  return std::max(plan_linear(s, true, 1, backward).bytes, plan_linear(s, true, 2, backward).bytes);
+}
+
+// Two channels a lane where a pair never straddles: bf16, even width and rows, pointers of four bytes.
+int vec_of(const LinearArgs& a, bool bf, bool backward) {
+  if (!bf || a.channels % 2 || a.x_stride % 2 || a.dt_stride % 2 || a.in_stride % 2) return 1;
+  const void* ps[] = {a.x, a.dt_raw, a.in_raw, a.y, a.dx, a.ddt_raw, a.din_raw, a.dy};
+  for (const void* p : ps)
+    if (!aligned_to(p, 4)) return 1;
+  return backward ? (a.dy_stride % 2 ? 1 : 2) : 1;
 }
 
 void use_plan(LinearArgs* a, const Plan& p, void* workspace) {
@@ -672,6 +793,42 @@ dim3 tile_grid(const Plan& p) {
   return dim3(static_cast<unsigned>(x), static_cast<unsigned>((n + x - 1) / x));
 }
 
+template <bool BACK, typename Act, int V, int P, int WAVES, int GATE>
+void launch_scale(const LinearArgs& a, dim3 grid, hipStream_t st) {
+#define AXON_LAUNCH(SCALE)                                                                            \
+  if constexpr (BACK)                                                                                 \
+    hipLaunchKernelGGL((linear_tile_back_kernel<Act, V, P, WAVES, GATE, SCALE>), grid, dim3(64 * WAVES), 0, st, a); \
+  else                                                                                                \
+    hipLaunchKernelGGL((linear_tile_kernel<Act, V, P, WAVES, GATE, SCALE>), grid, dim3(64 * WAVES), 0, st, a)
+  if (a.input_scale == AXON_INPUT_SQRT) {
+    AXON_LAUNCH(AXON_INPUT_SQRT);
+  } else if (a.input_scale == AXON_INPUT_COMPLEMENT) {
+    AXON_LAUNCH(AXON_INPUT_COMPLEMENT);
+  } else {
+    AXON_LAUNCH(AXON_INPUT_PLAIN);
+  }
+#undef AXON_LAUNCH
+}
+
+template <bool BACK, typename Act, int V, int P, int WAVES>
+void launch_gate(const LinearArgs& a, dim3 grid, hipStream_t st) {
+  if (a.gate == AXON_LINEAR_SIGMOID)
+    launch_scale<BACK, Act, V, P, WAVES, AXON_LINEAR_SIGMOID>(a, grid, st);
+  else
+    launch_scale<BACK, Act, V, P, WAVES, AXON_LINEAR_SOFTPLUS>(a, grid, st);
+}
+
+template <bool BACK>
+void launch_tiles(const LinearArgs& a, const Plan& plan, bool bf, hipStream_t st) {
+  const dim3 grid = tile_grid(plan);
+  if (plan.vec == 2)
+    launch_gate<BACK, bf16_bits, 2, BACK ? kBackTokens2 : kTokens2, BACK ? kBackWaves2 : kWaves2>(a, grid, st);
+  else if (bf)
+    launch_gate<BACK, bf16_bits, 1, BACK ? kBackTokens : kTokens, BACK ? kBackWaves : kWaves>(a, grid, st);
+  else
+    launch_gate<BACK, float, 1, BACK ? kBackTokens : kTokens, BACK ? kBackWaves : kWaves>(a, grid, st);
+}
+
 unsigned channel_groups(int channels, int width) {
   return static_cast<unsigned>((channels + width - 1) / width);
 }
@@ -690,7 +847,7 @@ size_t axon_linear_checkpoint_rows(int64_t sequences, int64_t tokens, int32_t pa
 
 size_t axon_linear_scan_workspace_bytes(const axon_linear_shape* shape) {
   if (axon::check_shape(shape, false) != AXON_OK) return 0;
-  return axon::workspace_of(*shape, axon::kWaves, false);
+  return axon::workspace_of(*shape, false);
 }
 
 axon_status axon_linear_scan(const axon_linear_shape* shape, const axon_linear_params* params,
@@ -743,20 +900,17 @@ axon_status axon_linear_scan(const axon_linear_shape* shape, const axon_linear_p
   a.state_in = state_in, a.in_slots = in_slots, a.in_count = s.state_slots;
   a.state_out = state_out, a.out_slots = out_slots, a.out_count = s.out_slots;
   a.y = y, a.checkpoints = checkpoints;
-  const Plan plan = plan_linear(s, tables != nullptr, kWaves, false);
+  const Plan plan = plan_linear(s, tables != nullptr, vec_of(a, bf, false), false);
   use_plan(&a, plan, workspace);
   hipStream_t st = static_cast<hipStream_t>(stream);
   clear_chain(plan, workspace, st);
-  if (bf)
-    hipLaunchKernelGGL((linear_tile_kernel<bf16_bits, kWaves>), tile_grid(plan), dim3(64 * kWaves), 0, st, a);
-  else
-    hipLaunchKernelGGL((linear_tile_kernel<float, kWaves>), tile_grid(plan), dim3(64 * kWaves), 0, st, a);
+  launch_tiles<false>(a, plan, bf, st);
   return hipGetLastError() == hipSuccess ? AXON_OK : AXON_ERR_HIP;
 }
 
 size_t axon_linear_scan_backward_workspace_bytes(const axon_linear_shape* shape) {
   if (axon::check_shape(shape, true) != AXON_OK) return 0;
-  return axon::workspace_of(*shape, axon::kBackWaves, true);
+  return axon::workspace_of(*shape, true);
 }
 
 axon_status axon_linear_scan_backward(const axon_linear_shape* shape,
@@ -810,15 +964,11 @@ axon_status axon_linear_scan_backward(const axon_linear_shape* shape,
   a.dy = dy, a.points = checkpoints, a.dstate_out = dstate_out;
   a.dx = dx, a.ddt_raw = ddt_raw, a.din_raw = din_raw;
   a.dA_log = dA_log, a.ddt_bias = ddt_bias, a.din_bias = din_bias, a.dstate_in = dstate_in;
-  const Plan plan = plan_linear(s, tables != nullptr, kBackWaves, true);
+  const Plan plan = plan_linear(s, tables != nullptr, vec_of(a, bf, true), true);
   use_plan(&a, plan, workspace);
   hipStream_t st = static_cast<hipStream_t>(stream);
   clear_chain(plan, workspace, st);
-  const dim3 grid = tile_grid(plan), threads(64 * kBackWaves);
-  if (bf)
-    hipLaunchKernelGGL((linear_tile_back_kernel<bf16_bits, kBackWaves>), grid, threads, 0, st, a);
-  else
-    hipLaunchKernelGGL((linear_tile_back_kernel<float, kBackWaves>), grid, threads, 0, st, a);
+  launch_tiles<true>(a, plan, bf, st);
   hipLaunchKernelGGL(linear_sum_kernel, dim3(channel_groups(a.channels, 64), din_bias ? 3 : 2),
                      dim3(256), 0, st, a, a.tiles);
   return hipGetLastError() == hipSuccess ? AXON_OK : AXON_ERR_HIP;

@@ -42,10 +42,16 @@ inline Packed make_packed(int64_t sequences, int64_t tokens, const int32_t* tabl
   return p;
 }
 
+// A table's entry at a wave-uniform place: through the constant address space, so that it comes by a
+// scalar load, which waits for no vector load (no kernel that reads tables writes them).
+__device__ __forceinline__ int table_at(const int32_t* p, int64_t i) {
+  return ((const __attribute__((address_space(4))) int32_t*)p)[i];
+}
+
 // Where sequence n begins (n = sequences: where the last one ends). Entries are cut to the buffer, so
 // that no contents of the tables lead outside it.
 __device__ __forceinline__ int packed_start(const Packed& p, int n) {
-  return p.starts ? min(max(p.starts[n], 0), p.tokens) : n * p.seqlen;
+  return p.starts ? min(max(table_at(p.starts, n), 0), p.tokens) : n * p.seqlen;
 }
 
 struct BlockAt {
@@ -61,10 +67,10 @@ __device__ __forceinline__ BlockAt block_at(const Packed& p, int row) {
   if (row >= p.rows) return b;
   int s0, s1;
   if (p.starts) {
-    const int seq = p.block_seq[row];
+    const int seq = table_at(p.block_seq, row);
     if (seq < 0 || seq >= p.sequences) return b;
     s0 = packed_start(p, seq), s1 = packed_start(p, seq + 1);
-    b.first = p.block_first[row];
+    b.first = table_at(p.block_first, row);
     if (b.first < s0 || b.first >= s1 || (b.first - s0) % kBlock) return b;
     b.seq = seq;
   } else {
