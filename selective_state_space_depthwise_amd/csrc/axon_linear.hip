@@ -103,7 +103,7 @@ __device__ __forceinline__ float log2_decay(float rate, float raw, float bias) {
   return rate * softplus_nan(raw + bias);
 }
 
-// A wave's share of a tile: P tokens of one block, V channels a lane.
+// A wave's share of a tile: P tokens of one block, a channel a lane.
 struct Share {
   int seq, first, count;   // count 0: none; rows first .. first + count - 1
   int row;                 // of the block tables
@@ -127,70 +127,29 @@ __device__ __forceinline__ Share share_of(const Packed& p, int tile, int wave) {
   return s;
 }
 
-// P rows of a wave as loaded, V channels a lane; rows behind the last repeat it.
-template <typename Act, int V, int P>
-struct Rows;
-template <int P>
-struct Rows<float, 1, P> {
-  uint32_t v[P];
-  __device__ __forceinline__ void load1(int j, rsrc_t r, uint32_t off, uint32_t row) {
-    v[j] = __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
-  }
-  __device__ __forceinline__ float at(int j, int) const { return __uint_as_float(v[j]); }
-};
-template <int P>
-struct Rows<bf16_bits, 1, P> {
-  uint16_t v[P];
-  __device__ __forceinline__ void load1(int j, rsrc_t r, uint32_t off, uint32_t row) {
-    v[j] = __builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
-  }
-  __device__ __forceinline__ float at(int j, int) const { return raw16_to_f32(v[j]); }
-};
-template <int P>
-struct Rows<bf16_bits, 2, P> {
-  uint32_t v[P];
-  __device__ __forceinline__ void load1(int j, rsrc_t r, uint32_t off, uint32_t row) {
-    v[j] = __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
-  }
-  __device__ __forceinline__ float at(int j, int i) const {
-    return __uint_as_float(i ? v[j] & 0xFFFF0000u : v[j] << 16);
-  }
-};
-template <typename Act, int V, int P>
-__device__ __forceinline__ void load_rows(Rows<Act, V, P>& to, const void* base, int64_t stride,
-                                          const Share& s, int e) {
-  const rsrc_t r = make_rsrc(static_cast<const Act*>(base) + s.first * stride);
-  const uint32_t step = static_cast<uint32_t>(stride) * sizeof(Act), off = e * sizeof(Act);
+// P rows of a wave as loaded; rows behind the last repeat it.
+template <typename Act, int P>
+struct Rows {
+  typename RawOf<Act>::type v[P];
+  __device__ __forceinline__ void load(const void* base, int64_t stride, const Share& s, int e) {
+    const rsrc_t r = make_rsrc(static_cast<const Act*>(base) + s.first * stride);
+    const uint32_t step = static_cast<uint32_t>(stride) * sizeof(Act), off = e * sizeof(Act);
 #pragma unroll
-  for (int j = 0; j < P; ++j) to.load1(j, r, off, static_cast<uint32_t>(min(j, s.count - 1)) * step);
-}
-template <int V>
-__device__ __forceinline__ void store_vals(float* p, const float* v) {
-  p[0] = v[0];
-}
-template <int V>
-__device__ __forceinline__ void store_vals(bf16_bits* p, const float* v) {
-  if constexpr (V == 2)
-    *reinterpret_cast<uint32_t*>(p) =
-        static_cast<uint32_t>(f32_to_bf16(v[0])) | static_cast<uint32_t>(f32_to_bf16(v[1])) << 16;
-  else
-    p[0] = f32_to_bf16(v[0]);
-}
+    for (int j = 0; j < P; ++j) {
+      const uint32_t row = static_cast<uint32_t>(min(j, s.count - 1)) * step;
+      if constexpr (sizeof(Act) == 4) v[j] = __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
+      else v[j] = __builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
+    }
+  }
+  __device__ __forceinline__ float operator[](int j) const { return widen(v[j]); }
+};
 
-template <typename Act, int V>
-__device__ __forceinline__ void store_row(rsrc_t r, uint32_t off, uint32_t row, const float* v) {
-  if constexpr (V == 2)
-    __builtin_amdgcn_raw_buffer_store_b32(
-        static_cast<uint32_t>(f32_to_bf16(v[0])) | static_cast<uint32_t>(f32_to_bf16(v[1])) << 16, r, off, row, 0);
-  else
-    store_buf_s<Act>(r, off, row, v[0]);
-}
-
-// What the tiles in front (behind, in the backward pass) hand on. A tile first publishes its own part
-// (the sum of its log2 a, and h from zero), then, once it knows what enters it, what leaves it. A reader
-// takes the nearest tile that has published the latter and applies the parts between in the order in
-// which those tiles do it themselves, so that the result does not depend on who was first. Both are one
-// atomic of the value itself: a NaN with all bits set stands for nothing, and stored NaNs are others.
+// ---- What tiles tell each other -----------------------------------------------------------------
+// A tile first publishes its own part (the sum of its log2 a, and h from zero), then, once it knows what
+// enters it, what leaves it. A reader takes the nearest tile that has published the latter and applies
+// the parts between in the order in which those tiles do it themselves, so that the result does not
+// depend on who was first. Both are one atomic of the value itself: a NaN with all bits set stands for
+// nothing, and stored NaNs are others.
 __device__ __forceinline__ uint32_t told(float v) {
   return v != v ? 0x7FC00000u : __float_as_uint(v);
 }
@@ -243,46 +202,61 @@ __device__ __forceinline__ float hear(const LinearArgs& g, int from, int left, i
   }
 }
 
-// The tile and channel group of this workgroup: in the order in which workgroups start.
-__device__ __forceinline__ uint32_t take_ticket(const LinearArgs& g, uint32_t* shared) {
-  if (!g.ticket) return blockIdx.x;
-  if (threadIdx.x == 0)
-    *shared = 1 + __hip_atomic_fetch_add(g.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  return __builtin_amdgcn_readfirstlane(*shared);
-}
-
 __global__ __launch_bounds__(256) void linear_clear_kernel(uint4* p, int64_t count) {
   const int64_t step = int64_t(gridDim.x) * 256;
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < count; i += step)
     p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
 }
 
-// What a tile's waves leave for each other: column (i, lane) is channel V lane + i of the group.
-template <int V, int WAVES>
+// What a tile's waves leave for each other, a channel a lane.
+template <int WAVES>
 struct Parts {
-  float logs[WAVES][V][64], decay[WAVES][V][64], part[WAVES][V][64], enter[V][64];
+  float logs[WAVES][64], decay[WAVES][64], part[WAVES][64], enter[64];
   int fresh[WAVES];  // nothing from in front (behind, backwards) reaches the wave's end
+
+  __device__ __forceinline__ void put(int wave, int lane, float log, float own, bool starts) {
+    logs[wave][lane] = log;
+    decay[wave][lane] = carry_of(log);
+    part[wave][lane] = own;
+    if (lane == 0) fresh[wave] = starts;
+  }
 };
 
-// One wave for each of V columns: the tile's own part is told, and what enters the tile is found.
-// alone: nothing enters; DIR as for hear.
-template <int DIR, int V, int WAVES>
-__device__ __forceinline__ void exchange(const LinearArgs& g, Parts<V, WAVES>& sh, int i, int lane,
-                                         int tile, int grp, bool alone, int left) {
+// The tile's waves in front of a wave (behind it for DIR 1): their decay and own part.
+template <int DIR, int WAVES>
+struct Front {
+  float log = 0.0f, part = 0.0f;
+  bool closed = false;  // a sequence begins (ends) among them
+  __device__ __forceinline__ Front(const Parts<WAVES>& sh, int wave, int lane) {
+    for (int w = DIR < 0 ? 0 : WAVES - 1; w != wave; w -= DIR) {
+      const bool f = sh.fresh[w];
+      part = f ? sh.part[w][lane] : advance(sh.decay[w][lane], part, sh.part[w][lane]);
+      log += sh.logs[w][lane];
+      closed |= f;
+    }
+  }
+  __device__ __forceinline__ float enter(float h) const {
+    return closed ? part : advance(carry_of(log), h, part);
+  }
+};
+
+// The tile's own part is told, and what enters it is found. alone: nothing enters; DIR, left as for hear.
+template <int DIR, int WAVES>
+__device__ __forceinline__ void exchange(const LinearArgs& g, Parts<WAVES>& sh, int lane, int tile,
+                                         int grp, bool alone, int left) {
   float sum = 0.0f, own = 0.0f;
   bool closed = false;  // a sequence begins (ends) in the tile: nothing passes through it
 #pragma unroll
   for (int n = 0; n < WAVES; ++n) {
     const int w = DIR < 0 ? n : WAVES - 1 - n;
     const bool f = sh.fresh[w];
-    own = f ? sh.part[w][i][lane] : advance(sh.decay[w][i][lane], own, sh.part[w][i][lane]);
-    sum += sh.logs[w][i][lane];
+    own = f ? sh.part[w][lane] : advance(sh.decay[w][lane], own, sh.part[w][lane]);
+    sum += sh.logs[w][lane];
     closed |= f;
   }
   float before = 0.0f;
   if (g.ticket) {
-    const int64_t columns = int64_t(g.groups) * V * 64, column = (int64_t(grp) * V + i) * 64 + lane;
+    const int64_t columns = int64_t(g.groups) * 64, column = int64_t(grp) * 64 + lane;
     const int64_t at = tile * columns + column;
     if (closed || alone) tell_carry(g.carry + at, own);
     else tell_sums(g.sums + at, sum, own);
@@ -291,338 +265,264 @@ __device__ __forceinline__ void exchange(const LinearArgs& g, Parts<V, WAVES>& s
       if (!closed) tell_carry(g.carry + at, advance(carry_of(sum), before, own));
     }
   }
-  sh.enter[i][lane] = before;
+  sh.enter[lane] = before;
 }
 
-template <typename Act, int V, int P, int WAVES, int GATE, int SCALE>
+// The unit (tile and channel group) of this workgroup: in the order in which workgroups start.
+__device__ __forceinline__ uint32_t take_ticket(const LinearArgs& g, uint32_t* shared) {
+  if (!g.ticket) return blockIdx.x;
+  if (threadIdx.x == 0)
+    *shared = 1 + __hip_atomic_fetch_add(g.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(*shared);
+}
+
+// ---- The scan -----------------------------------------------------------------------------------
+// Waves to a workgroup and registers are chosen for 24 waves a CU.
+template <typename Act, int P, int WAVES, int GATE, int SCALE>
 __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g) {
-  static_assert(V <= WAVES, "a wave a column");
   __shared__ uint32_t ticket;
-  __shared__ Parts<V, WAVES> sh;
+  __shared__ Parts<WAVES> sh;
   const uint32_t t = take_ticket(g, &ticket);
   const int tile = t / g.groups, grp = t - tile * g.groups;
   if (tile >= g.tiles) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const bool in_range = (grp * 64 + lane) * V < g.channels;
-  const int e = min((grp * 64 + lane) * V, g.channels - V);
+  const bool in_range = grp * 64 + lane < g.channels;
+  const int e = min(grp * 64 + lane, g.channels - 1);
   const Share s = share_of<P, WAVES>(g.p, tile, wave);
-  float a[P][V], b[P][V];
-  float h0[V] = {};  // what enters the wave, where it begins a sequence
-  float L[V] = {}, h[V] = {};
+  float a[P], b[P];
+  float h0 = 0.0f;  // what enters the wave, where it begins a sequence
+  float L = 0.0f, h = 0.0f;
   if (s.count > 0) {
-    Rows<Act, V, P> x, raw, in;
-    load_rows(raw, g.dt_raw, g.dt_stride, s, e);
-    load_rows(x, g.x, g.x_stride, s, e);
-    if (g.in_raw) load_rows(in, g.in_raw, g.in_stride, s, e);
+    Rows<Act, P> x, raw, in;
+    raw.load(g.dt_raw, g.dt_stride, s, e);
+    x.load(g.x, g.x_stride, s, e);
+    if (g.in_raw) in.load(g.in_raw, g.in_stride, s, e);
     if (s.begins && g.state_in) {
       const int64_t slot = g.in_slots ? table_at(g.in_slots, s.seq) : s.seq;
-      if (slot >= 0 && slot < g.in_count)
-#pragma unroll
-        for (int i = 0; i < V; ++i) h0[i] = g.state_in[slot * g.channels + e + i];
+      if (slot >= 0 && slot < g.in_count) h0 = g.state_in[slot * g.channels + e];
     }
-    float rate[V], bias[V], ib[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      rate[i] = -expf(g.A_log[e + i]) * kLog2e;
-      bias[i] = g.dt_bias ? g.dt_bias[e + i] : 0.0f;
-      ib[i] = scaled_bias(g.in_raw && g.in_bias ? g.in_bias[e + i] : 0.0f);
-    }
+    const float rate = -expf(g.A_log[e]) * kLog2e;
+    const float bias = g.dt_bias ? g.dt_bias[e] : 0.0f;
+    const float ib = scaled_bias(g.in_raw && g.in_bias ? g.in_bias[e] : 0.0f);
     // a: log2 a first
 #pragma unroll
-    for (int j = 0; j < P; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) a[j][i] = log2_decay<GATE>(rate[i], raw.at(j, i), bias[i]);
+    for (int j = 0; j < P; ++j) a[j] = log2_decay<GATE>(rate, raw[j], bias);
     if (s.count < P) {
 #pragma unroll
       for (int j = 0; j < P; ++j)
-        if (j >= s.count)
-#pragma unroll
-          for (int i = 0; i < V; ++i) a[j][i] = 0.0f;
+        if (j >= s.count) a[j] = 0.0f;
     }
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        L[i] += a[j][i];
-        const float l2 = a[j][i];
-        a[j][i] = __builtin_amdgcn_exp2f(l2);
-        b[j][i] = x.at(j, i) * input_factor<SCALE>(l2, a[j][i]);
-      }
-    if (g.in_raw) {
-#pragma unroll
-      for (int j = 0; j < P; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          b[j][i] *= sigmoid_f32(in.at(j, i), ib[i]);
-        }
-    }
-    if (s.count < P) {
-#pragma unroll
-      for (int j = 0; j < P; ++j)
-        if (j >= s.count)
-#pragma unroll
-          for (int i = 0; i < V; ++i) b[j][i] = 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = h0[i];
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = fmaf(a[j][i], h[i], b[j][i]);
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    sh.logs[wave][i][lane] = L[i];
-    sh.decay[wave][i][lane] = carry_of(L[i]);
-    sh.part[wave][i][lane] = h[i];
-  }
-  if (lane == 0) sh.fresh[wave] = s.begins;
-  __syncthreads();
-  if (wave < V) {
-    const bool alone = tile == 0 || share_of<P, WAVES>(g.p, tile, 0).begins;
-    exchange<-1, V, WAVES>(g, sh, wave, lane, tile, grp, alone, tile);
-  }
-  __syncthreads();
-  if (s.count > 0 && in_range) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      h[i] = sh.enter[i][lane];
-      for (int w = 0; w < wave; ++w)
-        h[i] = sh.fresh[w] ? sh.part[w][i][lane] : advance(sh.decay[w][i][lane], h[i], sh.part[w][i][lane]);
-      if (s.begins) h[i] = h0[i];
-      if (s.opens && g.checkpoints) g.checkpoints[int64_t(s.row) * g.channels + e + i] = h[i];
-    }
-    const rsrc_t y = make_rsrc(static_cast<Act*>(g.y) + int64_t(s.first) * g.channels);
-    const uint32_t step = static_cast<uint32_t>(g.channels) * sizeof(Act), off = e * sizeof(Act);
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = fmaf(a[j][i], h[i], b[j][i]);
-      if (j < s.count) store_row<Act, V>(y, off, j * step, h);
+      const float l2 = a[j];
+      L += l2;
+      a[j] = __builtin_amdgcn_exp2f(l2);
+      b[j] = x[j] * input_factor<SCALE>(l2, a[j]);
     }
-    if (s.ends && g.state_out) {
-      const int64_t slot = g.out_slots ? table_at(g.out_slots, s.seq) : s.seq;
-      if (slot >= 0 && slot < g.out_count)
+    if (g.in_raw) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) g.state_out[slot * g.channels + e + i] = h[i];
+      for (int j = 0; j < P; ++j) b[j] *= sigmoid_f32(in[j], ib);
+    }
+    if (s.count < P) {
+#pragma unroll
+      for (int j = 0; j < P; ++j)
+        if (j >= s.count) b[j] = 0.0f;
+    }
+    h = h0;
+#pragma unroll
+    for (int j = 0; j < P; ++j) h = fmaf(a[j], h, b[j]);
+  }
+  sh.put(wave, lane, L, h, s.begins);
+  __syncthreads();
+  if (wave == 0) exchange<-1, WAVES>(g, sh, lane, tile, grp, tile == 0 || s.begins, tile);
+  const Front<-1, WAVES> front(sh, wave, lane);
+  __syncthreads();
+  if (s.count > 0) {
+    h = s.begins ? h0 : front.enter(sh.enter[lane]);
+    if (in_range) {
+      if (s.opens && g.checkpoints) g.checkpoints[int64_t(s.row) * g.channels + e] = h;
+      const rsrc_t y = make_rsrc(static_cast<Act*>(g.y) + int64_t(s.first) * g.channels);
+      const uint32_t step = static_cast<uint32_t>(g.channels) * sizeof(Act), off = e * sizeof(Act);
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        h = fmaf(a[j], h, b[j]);
+        if (j < s.count) store_buf_s<Act>(y, off, j * step, h);
+      }
+      if (s.ends && g.state_out) {
+        const int64_t slot = g.out_slots ? table_at(g.out_slots, s.seq) : s.seq;
+        if (slot >= 0 && slot < g.out_count) g.state_out[slot * g.channels + e] = h;
+      }
     }
   }
   if (!in_range) return;
   // Sequences without tokens, and rows behind the last one: shared out to the tiles' waves.
   for (int n = tile * WAVES + wave; n < g.p.sequences; n += g.tiles * WAVES) {
     if (!g.state_out || packed_start(g.p, n) < packed_start(g.p, n + 1)) continue;
-    const int64_t from = g.in_slots ? g.in_slots[n] : n, to = g.out_slots ? g.out_slots[n] : n;
+    const int64_t from = g.in_slots ? table_at(g.in_slots, n) : n;
+    const int64_t to = g.out_slots ? table_at(g.out_slots, n) : n;
     if (to >= 0 && to < g.out_count)
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        g.state_out[to * g.channels + e + i] =
-            g.state_in && from >= 0 && from < g.in_count ? g.state_in[from * g.channels + e + i] : 0.0f;
+      g.state_out[to * g.channels + e] =
+          g.state_in && from >= 0 && from < g.in_count ? g.state_in[from * g.channels + e] : 0.0f;
   }
-  if (g.clear_behind) {
-    const float zero[V] = {};
-    for (int64_t r = int64_t(packed_start(g.p, g.p.sequences)) + tile * WAVES + wave;
-         r < g.p.tokens; r += int64_t(g.tiles) * WAVES)
-      store_vals<V>(static_cast<Act*>(g.y) + r * g.channels + e, zero);
-  }
+  if (g.clear_behind)
+    for (int64_t r = int64_t(packed_start(g.p, g.p.sequences)) + tile * WAVES + wave; r < g.p.tokens;
+         r += int64_t(g.tiles) * WAVES)
+      store_act(static_cast<Act*>(g.y), r * g.channels + e, 0.0f);
 }
 
+// ---- Its backward pass --------------------------------------------------------------------------
 // The same from the last tile to the first. A wave finds its block's states again from the block's
 // checkpoint and the parts of the waves in front of it.
-template <typename Act, int V, int P, int WAVES, int GATE, int SCALE>
-__global__ __launch_bounds__(64 * WAVES) void linear_tile_back_kernel(LinearArgs g) {
-  static_assert(WAVES * P % kBlock == 0 && V <= WAVES, "a tile holds whole blocks");
+template <typename Act, int P, int WAVES, int GATE, int SCALE>
+__global__ __launch_bounds__(64 * WAVES, 5) void linear_tile_back_kernel(LinearArgs g) {
+  static_assert(WAVES * P % kBlock == 0, "a tile holds whole blocks");
   constexpr int kBlockWaves = kBlock / P;
   __shared__ uint32_t ticket;
-  __shared__ Parts<V, WAVES> sh;
-  __shared__ float states[WAVES][V][64], totals[WAVES][3][V][64];
+  __shared__ Parts<WAVES> sh;
+  __shared__ float states[WAVES][64], totals[WAVES][3][64];
   const uint32_t t = take_ticket(g, &ticket);
   const int turn = t / g.groups, grp = t - turn * g.groups;
   if (turn >= g.tiles) return;
   const int tile = g.tiles - 1 - turn;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const bool in_range = (grp * 64 + lane) * V < g.channels;
-  const int e = min((grp * 64 + lane) * V, g.channels - V);
+  const bool in_range = grp * 64 + lane < g.channels;
+  const int e = min(grp * 64 + lane, g.channels - 1);
   const Share s = share_of<P, WAVES>(g.p, tile, wave);
-  // Per token: a L, a, what the gate's slope makes of G, the input's gate, u (1 - gate), m, the second term
-  // of G; hb holds the inputs m u first and the states in front of the tokens then.
-  Rows<Act, V, P> d;
-  float aL[P][V], av[P][V], slope[P][V], on[P][V], z[P][V], m[P][V], w2[P][V], hb[P][V];
-  float L[V] = {}, h[V] = {}, k[V] = {}, k0[V] = {}, point[V] = {};
+  // Per token: a, what the gate's slope makes of G, m times the input's gate, m u (1 - gate), dy. G is
+  // g (aL h - w): first aL, w and the inputs m u, then, once the states are known, aL h - w in their place.
+  float av[P], slope[P], mo[P], mz[P], dy[P], aL[P], w[P], hb[P];
+  float L = 0.0f, h = 0.0f, k = 0.0f, k0 = 0.0f, point = 0.0f;
   if (s.count > 0) {
-    Rows<Act, V, P> x, raw, in;
-    load_rows(raw, g.dt_raw, g.dt_stride, s, e);
-    load_rows(x, g.x, g.x_stride, s, e);
-    if (g.in_raw) load_rows(in, g.in_raw, g.in_stride, s, e);
-    load_rows(d, g.dy, g.dy_stride, s, e);
-    float rate[V], bias[V], ib[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (s.opens) point[i] = g.points[int64_t(s.row) * g.channels + e + i];
-      if (s.ends && g.dstate_out) k0[i] = g.dstate_out[int64_t(s.seq) * g.channels + e + i];
-      rate[i] = -expf(g.A_log[e + i]) * kLog2e;
-      bias[i] = g.dt_bias ? g.dt_bias[e + i] : 0.0f;
-      ib[i] = g.in_raw && g.in_bias ? g.in_bias[e + i] : 0.0f;
-    }
+    Rows<Act, P> x, raw, in, d;
+    raw.load(g.dt_raw, g.dt_stride, s, e);
+    x.load(g.x, g.x_stride, s, e);
+    if (g.in_raw) in.load(g.in_raw, g.in_stride, s, e);
+    d.load(g.dy, g.dy_stride, s, e);
+    if (s.opens) point = g.points[int64_t(s.row) * g.channels + e];
+    if (s.ends && g.dstate_out) k0 = g.dstate_out[int64_t(s.seq) * g.channels + e];
+    const float rate = -expf(g.A_log[e]) * kLog2e;
+    const float bias = g.dt_bias ? g.dt_bias[e] : 0.0f;
+    const float ib = g.in_raw && g.in_bias ? g.in_bias[e] : 0.0f;
+    // mo: the input's gate, mz: u (1 - gate), hb: u at first
     if (g.in_raw) {
 #pragma unroll
-      for (int j = 0; j < P; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const Gate q(in.at(j, i), ib[i]);
-          on[j][i] = q.on;
-          z[j][i] = x.at(j, i) * q.on * q.off;
-        }
+      for (int j = 0; j < P; ++j) {
+        const Gate q(in[j], ib);
+        mo[j] = q.on;
+        hb[j] = x[j] * q.on;
+        mz[j] = hb[j] * q.off;
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < P; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) on[j][i] = 1.0f, z[j][i] = 0.0f;
+      for (int j = 0; j < P; ++j) mo[j] = 1.0f, hb[j] = x[j], mz[j] = 0.0f;
     }
+    h = point;
 #pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = point[i];
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const bool held = j < s.count;
-        float l2;
-        if constexpr (GATE == AXON_LINEAR_SIGMOID) {
-          const Gate q(raw.at(j, i), bias[i]);
-          l2 = rate[i] * q.on;
-          slope[j][i] = q.off;
-        } else {
-          const float v = raw.at(j, i) + bias[i], sp = softplus_nan(v);
-          l2 = rate[i] * sp;
-          slope[j][i] = v < -20.0f ? 1.0f : sigmoid_f32(v, 0.0f) * __builtin_amdgcn_rcpf(sp);
-        }
-        l2 = held ? l2 : 0.0f;
-        L[i] += l2;
-        const float a = __builtin_amdgcn_exp2f(l2), u = held ? x.at(j, i) * on[j][i] : 0.0f;
-        av[j][i] = a;
-        aL[j][i] = a * (fmaxf(l2, -200.0f) * kLn2);  // 0 for log a = -inf
-        if constexpr (SCALE == AXON_INPUT_SQRT) {
-          const float em1 = expm1_of(l2, a), q = -em1 * (2.0f + em1);
-          const float rs = q == 0.0f ? 0.0f : __builtin_amdgcn_rsqf(q);
-          m[j][i] = q * rs;
-          w2[j][i] = a * u * rs;
-        } else if constexpr (SCALE == AXON_INPUT_COMPLEMENT) {
-          m[j][i] = -expm1_of(l2, a);
-          w2[j][i] = u;
-        } else {
-          m[j][i] = 1.0f;
-          w2[j][i] = 0.0f;
-        }
-        hb[j][i] = m[j][i] * u;
-        h[i] = fmaf(a, h[i], hb[j][i]);
+    for (int j = 0; j < P; ++j) {
+      const bool held = j < s.count;
+      float l2;
+      if constexpr (GATE == AXON_LINEAR_SIGMOID) {
+        const Gate q(raw[j], bias);
+        l2 = rate * q.on;
+        slope[j] = q.off;
+      } else {
+        const float v = raw[j] + bias, sp = softplus_nan(v);
+        l2 = rate * sp;
+        slope[j] = v < -20.0f ? 1.0f : sigmoid_f32(v, 0.0f) * __builtin_amdgcn_rcpf(sp);
       }
+      l2 = held ? l2 : 0.0f;
+      L += l2;
+      const float u = held ? hb[j] : 0.0f;
+      av[j] = __builtin_amdgcn_exp2f(l2);
+      aL[j] = av[j] * (fmaxf(l2, -200.0f) * kLn2);  // 0 for log a = -inf
+      float m = 1.0f;
+      w[j] = 0.0f;
+      if constexpr (SCALE == AXON_INPUT_SQRT) {
+        // m = sqrt(q) and 1 / m, of q 2^64 so that the least q keep their root
+        const float em1 = expm1_of(l2, av[j]), q = -em1 * (2.0f + em1), big = q * 0x1p64f;
+        const float rm = big == 0.0f ? 0.0f : __builtin_amdgcn_rsqf(big) * 0x1p32f;
+        m = q * rm;
+        w[j] = aL[j] * (av[j] * u * rm);
+      } else if constexpr (SCALE == AXON_INPUT_COMPLEMENT) {
+        m = -expm1_of(l2, av[j]);
+        w[j] = aL[j] * u;
+      }
+      mo[j] *= m;
+      mz[j] *= m;
+      hb[j] = m * u;
+      dy[j] = held ? d[j] : 0.0f;
+      h = fmaf(av[j], h, hb[j]);
+    }
+    k = k0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) k[i] = k0[i];
-#pragma unroll
-    for (int j = P - 1; j >= 0; --j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) k[i] = av[j][i] * (k[i] + (j < s.count ? d.at(j, i) : 0.0f));
+    for (int j = P - 1; j >= 0; --j) k = av[j] * (k + dy[j]);
   }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    sh.logs[wave][i][lane] = L[i];
-    sh.decay[wave][i][lane] = carry_of(L[i]);
-    sh.part[wave][i][lane] = k[i];
-    states[wave][i][lane] = h[i];
-  }
-  if (lane == 0) sh.fresh[wave] = s.ends;
+  sh.put(wave, lane, L, k, s.ends);
+  states[wave][lane] = h;
   __syncthreads();
-  if (wave < V) {
-    const bool alone = turn == 0 || share_of<P, WAVES>(g.p, tile, WAVES - 1).ends;
-    exchange<1, V, WAVES>(g, sh, wave, lane, tile, grp, alone, turn);
-  }
+  if (wave == WAVES - 1) exchange<1, WAVES>(g, sh, lane, tile, grp, turn == 0 || s.ends, turn);
   // The states in front of the wave's tokens.
   if (s.count > 0) {
     const int w0 = wave / kBlockWaves * kBlockWaves;
+    h = s.opens ? point : states[w0][lane];
+    for (int n = w0 + 1; n < wave; ++n) h = advance(sh.decay[n][lane], h, states[n][lane]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      h[i] = s.opens ? point[i] : states[w0][i][lane];
-      for (int w = w0 + 1; w < wave; ++w) h[i] = advance(sh.decay[w][i][lane], h[i], states[w][i][lane]);
+    for (int j = 0; j < P; ++j) {
+      w[j] = fmaf(aL[j], h, -w[j]);
+      h = fmaf(av[j], h, hb[j]);
     }
-#pragma unroll
-    for (int j = 0; j < P; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float u = hb[j][i];
-        hb[j][i] = h[i];
-        h[i] = fmaf(av[j][i], h[i], u);
-      }
   }
+  const Front<1, WAVES> behind(sh, wave, lane);
   __syncthreads();
-  float sA[V] = {}, sdt[V] = {}, sin[V] = {};
+  float sA = 0.0f, sdt = 0.0f, sin = 0.0f;
   if (s.count > 0) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      k[i] = sh.enter[i][lane];
-      for (int w = WAVES - 1; w > wave; --w)
-        k[i] = sh.fresh[w] ? sh.part[w][i][lane] : advance(sh.decay[w][i][lane], k[i], sh.part[w][i][lane]);
-      if (s.ends) k[i] = k0[i];
-    }
+    k = s.ends ? k0 : behind.enter(sh.enter[lane]);
     const int64_t first = int64_t(s.first) * g.channels;
-    const rsrc_t dx = make_rsrc(static_cast<Act*>(g.dx) + first), ddt = make_rsrc(static_cast<Act*>(g.ddt_raw) + first);
+    const rsrc_t dx = make_rsrc(static_cast<Act*>(g.dx) + first);
+    const rsrc_t ddt = make_rsrc(static_cast<Act*>(g.ddt_raw) + first);
     const rsrc_t din = make_rsrc(static_cast<Act*>(g.din_raw) + (g.in_raw ? first : 0));
     const uint32_t step = static_cast<uint32_t>(g.channels) * sizeof(Act), off = e * sizeof(Act);
 #pragma unroll
     for (int j = P - 1; j >= 0; --j) {
       if (j >= s.count) continue;
-      float odt[V], ox[V], oin[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float gt = d.at(j, i) + k[i];
-        k[i] = av[j][i] * gt;
-        const float G = gt * aL[j][i] * (hb[j][i] - w2[j][i]), du = gt * m[j][i];
-        odt[i] = G * slope[j][i];
-        ox[i] = du * on[j][i];
-        oin[i] = du * z[j][i];
-        sA[i] += G;
-        sdt[i] += odt[i];
-        sin[i] += oin[i];
-      }
+      const float gt = dy[j] + k;
+      k = av[j] * gt;
+      const float G = gt * w[j], odt = G * slope[j], oin = gt * mz[j];
+      sA += G;
+      sdt += odt;
+      sin += oin;
       if (in_range) {
-        store_row<Act, V>(ddt, off, j * step, odt);
-        store_row<Act, V>(dx, off, j * step, ox);
-        if (g.in_raw) store_row<Act, V>(din, off, j * step, oin);
+        store_buf_s<Act>(ddt, off, j * step, odt);
+        store_buf_s<Act>(dx, off, j * step, gt * mo[j]);
+        if (g.in_raw) store_buf_s<Act>(din, off, j * step, oin);
       }
     }
-    if (s.begins && g.dstate_in && in_range)
-#pragma unroll
-      for (int i = 0; i < V; ++i) g.dstate_in[int64_t(s.seq) * g.channels + e + i] = k[i];
+    if (s.begins && g.dstate_in && in_range) g.dstate_in[int64_t(s.seq) * g.channels + e] = k;
   }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    totals[wave][0][i][lane] = sA[i];
-    totals[wave][1][i][lane] = sdt[i];
-    totals[wave][2][i][lane] = sin[i];
-  }
+  totals[wave][0][lane] = sA;
+  totals[wave][1][lane] = sdt;
+  totals[wave][2][lane] = sin;
   __syncthreads();
-  for (int q = wave; q < 3 * V; q += WAVES) {
-    const int which = q / V, i = q - which * V;
+  if (!in_range) return;
+  for (int q = wave; q < 3; q += WAVES) {
     float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) sum += totals[w][which][i][lane];
-    if (in_range) g.partial[(int64_t(tile) * 3 + which) * g.channels + e + i] = sum;
+    for (int n = 0; n < WAVES; ++n) sum += totals[n][q][lane];
+    g.partial[(int64_t(tile) * 3 + q) * g.channels + e] = sum;
   }
-  if (!in_range) return;
   if (g.dstate_in)
     for (int n = tile * WAVES + wave; n < g.p.sequences; n += g.tiles * WAVES) {
       if (packed_start(g.p, n) < packed_start(g.p, n + 1)) continue;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int64_t at = int64_t(n) * g.channels + e + i;
-        g.dstate_in[at] = g.dstate_out ? g.dstate_out[at] : 0.0f;
-      }
+      const int64_t at = int64_t(n) * g.channels + e;
+      g.dstate_in[at] = g.dstate_out ? g.dstate_out[at] : 0.0f;
     }
-  const float zero[V] = {};
   for (int64_t r = int64_t(packed_start(g.p, g.p.sequences)) + tile * WAVES + wave; r < g.p.tokens;
        r += int64_t(g.tiles) * WAVES) {
     const int64_t at = r * g.channels + e;
-    store_vals<V>(static_cast<Act*>(g.dx) + at, zero);
-    store_vals<V>(static_cast<Act*>(g.ddt_raw) + at, zero);
-    if (g.in_raw) store_vals<V>(static_cast<Act*>(g.din_raw) + at, zero);
+    store_act(static_cast<Act*>(g.dx), at, 0.0f);
+    store_act(static_cast<Act*>(g.ddt_raw), at, 0.0f);
+    if (g.in_raw) store_act(static_cast<Act*>(g.din_raw), at, 0.0f);
   }
 }
 
@@ -720,30 +620,24 @@ size_t tables_bytes(const Packed& p) {
   return p.starts ? 4 * (2 * (size_t(p.sequences) + 1) + 2 * size_t(p.rows)) : 0;
 }
 
-// Tokens a wave and waves a tile, by channels a lane.
-constexpr int kTokens = 16, kWaves = 8;          // one channel
-constexpr int kTokens2 = 8, kWaves2 = 16;        // two
-constexpr int kBackTokens = 16, kBackWaves = 4;  // one, backwards
-constexpr int kBackTokens2 = 8, kBackWaves2 = 8;
+constexpr int kTokens = 16, kWaves = 12;        // tokens a wave, waves a tile
+constexpr int kBackTokens = 8, kBackWaves = 8;  // of the backward pass
 
 // Tiles, and what of the workspace they use.
 struct Plan {
-  int vec;  // channels a lane
   int64_t tiles, groups;
   size_t sums, carry, ticket, chain;  // offsets and bytes of what tiles tell each other; chain 0: nothing
   size_t bytes;
 };
 
-Plan plan_linear(const axon_linear_shape& s, bool packed, int vec, bool backward) {
+Plan plan_linear(const axon_linear_shape& s, bool packed, bool backward) {
   Plan p{};
-  p.vec = vec;
   // rows of the tables, or sequences without tokens, at least one tile
   const int64_t rows = std::max<int64_t>(packed_rows(s.sequences, s.tokens, packed), 1);
-  const int64_t blocks = (backward ? vec == 2 ? kBackTokens2 * kBackWaves2 : kBackTokens * kBackWaves
-                                   : vec == 2 ? kTokens2 * kWaves2 : kTokens * kWaves) / kBlock;
+  const int64_t blocks = (backward ? kBackTokens * kBackWaves : kTokens * kWaves) / kBlock;
   p.tiles = (rows + blocks - 1) / blocks;
-  p.groups = (s.channels + 64 * vec - 1) / (64 * vec);
-  const size_t cells = size_t(p.tiles) * size_t(p.groups) * 64 * size_t(vec);
+  p.groups = (s.channels + 63) / 64;
+  const size_t cells = size_t(p.tiles) * size_t(p.groups) * 64;
   if (p.tiles > 1) {
     p.sums = 0;
     p.carry = 8 * cells;
@@ -754,19 +648,9 @@ Plan plan_linear(const axon_linear_shape& s, bool packed, int vec, bool backward
   return p;
 }
 
-// The workspace holds for either kind of batch (a uniform one has no more blocks than a packed one can)
-// and any alignment.
+// The workspace holds for either kind of batch: a uniform one has no more blocks than a packed one can.
 size_t workspace_of(const axon_linear_shape& s, bool backward) {
-  return std::max(plan_linear(s, true, 1, backward).bytes, plan_linear(s, true, 2, backward).bytes);
-}
-
-// Two channels a lane where a pair never straddles: bf16, even width and rows, pointers of four bytes.
-int vec_of(const LinearArgs& a, bool bf, bool backward) {
-  if (!bf || a.channels % 2 || a.x_stride % 2 || a.dt_stride % 2 || a.in_stride % 2) return 1;
-  const void* ps[] = {a.x, a.dt_raw, a.in_raw, a.y, a.dx, a.ddt_raw, a.din_raw, a.dy};
-  for (const void* p : ps)
-    if (!aligned_to(p, 4)) return 1;
-  return backward ? (a.dy_stride % 2 ? 1 : 2) : 1;
+  return plan_linear(s, true, backward).bytes;
 }
 
 void use_plan(LinearArgs* a, const Plan& p, void* workspace) {
@@ -793,13 +677,14 @@ dim3 tile_grid(const Plan& p) {
   return dim3(static_cast<unsigned>(x), static_cast<unsigned>((n + x - 1) / x));
 }
 
-template <bool BACK, typename Act, int V, int P, int WAVES, int GATE>
+template <bool BACK, typename Act, int GATE>
 void launch_scale(const LinearArgs& a, dim3 grid, hipStream_t st) {
-#define AXON_LAUNCH(SCALE)                                                                            \
-  if constexpr (BACK)                                                                                 \
-    hipLaunchKernelGGL((linear_tile_back_kernel<Act, V, P, WAVES, GATE, SCALE>), grid, dim3(64 * WAVES), 0, st, a); \
-  else                                                                                                \
-    hipLaunchKernelGGL((linear_tile_kernel<Act, V, P, WAVES, GATE, SCALE>), grid, dim3(64 * WAVES), 0, st, a)
+  constexpr int P = BACK ? kBackTokens : kTokens, W = BACK ? kBackWaves : kWaves;
+#define AXON_LAUNCH(SCALE)                                                                              \
+  if constexpr (BACK)                                                                                   \
+    hipLaunchKernelGGL((linear_tile_back_kernel<Act, P, W, GATE, SCALE>), grid, dim3(64 * W), 0, st, a); \
+  else                                                                                                  \
+    hipLaunchKernelGGL((linear_tile_kernel<Act, P, W, GATE, SCALE>), grid, dim3(64 * W), 0, st, a)
   if (a.input_scale == AXON_INPUT_SQRT) {
     AXON_LAUNCH(AXON_INPUT_SQRT);
   } else if (a.input_scale == AXON_INPUT_COMPLEMENT) {
@@ -810,23 +695,16 @@ void launch_scale(const LinearArgs& a, dim3 grid, hipStream_t st) {
 #undef AXON_LAUNCH
 }
 
-template <bool BACK, typename Act, int V, int P, int WAVES>
-void launch_gate(const LinearArgs& a, dim3 grid, hipStream_t st) {
-  if (a.gate == AXON_LINEAR_SIGMOID)
-    launch_scale<BACK, Act, V, P, WAVES, AXON_LINEAR_SIGMOID>(a, grid, st);
-  else
-    launch_scale<BACK, Act, V, P, WAVES, AXON_LINEAR_SOFTPLUS>(a, grid, st);
-}
-
 template <bool BACK>
 void launch_tiles(const LinearArgs& a, const Plan& plan, bool bf, hipStream_t st) {
   const dim3 grid = tile_grid(plan);
-  if (plan.vec == 2)
-    launch_gate<BACK, bf16_bits, 2, BACK ? kBackTokens2 : kTokens2, BACK ? kBackWaves2 : kWaves2>(a, grid, st);
-  else if (bf)
-    launch_gate<BACK, bf16_bits, 1, BACK ? kBackTokens : kTokens, BACK ? kBackWaves : kWaves>(a, grid, st);
+  const bool sigmoid = a.gate == AXON_LINEAR_SIGMOID;
+  if (bf)
+    sigmoid ? launch_scale<BACK, bf16_bits, AXON_LINEAR_SIGMOID>(a, grid, st)
+            : launch_scale<BACK, bf16_bits, AXON_LINEAR_SOFTPLUS>(a, grid, st);
   else
-    launch_gate<BACK, float, 1, BACK ? kBackTokens : kTokens, BACK ? kBackWaves : kWaves>(a, grid, st);
+    sigmoid ? launch_scale<BACK, float, AXON_LINEAR_SIGMOID>(a, grid, st)
+            : launch_scale<BACK, float, AXON_LINEAR_SOFTPLUS>(a, grid, st);
 }
 
 unsigned channel_groups(int channels, int width) {
@@ -900,7 +778,7 @@ axon_status axon_linear_scan(const axon_linear_shape* shape, const axon_linear_p
   a.state_in = state_in, a.in_slots = in_slots, a.in_count = s.state_slots;
   a.state_out = state_out, a.out_slots = out_slots, a.out_count = s.out_slots;
   a.y = y, a.checkpoints = checkpoints;
-  const Plan plan = plan_linear(s, tables != nullptr, vec_of(a, bf, false), false);
+  const Plan plan = plan_linear(s, tables != nullptr, false);
   use_plan(&a, plan, workspace);
   hipStream_t st = static_cast<hipStream_t>(stream);
   clear_chain(plan, workspace, st);
@@ -964,7 +842,7 @@ axon_status axon_linear_scan_backward(const axon_linear_shape* shape,
   a.dy = dy, a.points = checkpoints, a.dstate_out = dstate_out;
   a.dx = dx, a.ddt_raw = ddt_raw, a.din_raw = din_raw;
   a.dA_log = dA_log, a.ddt_bias = ddt_bias, a.din_bias = din_bias, a.dstate_in = dstate_in;
-  const Plan plan = plan_linear(s, tables != nullptr, vec_of(a, bf, true), true);
+  const Plan plan = plan_linear(s, tables != nullptr, true);
   use_plan(&a, plan, workspace);
   hipStream_t st = static_cast<hipStream_t>(stream);
   clear_chain(plan, workspace, st);

@@ -16,7 +16,9 @@ and likewise the gradient that runs backwards. What is formed from both takes th
 of their terms' bounds and 64 u of their terms' sizes. The exponential's results below 2^-126, the least
 normal fp32, are zeros: a is off by 2^-126 at most beside all that, which large factors (a state of
 1e6, a gradient of 1e3, |L| of 100) bring up to 1e-27. Likewise dt, so that |L| is off by up to rate
-2^-126 and m = sqrt(1 - a^2) = sqrt(2 |L|) by sqrt(2 rate 2^-126), about 1e-19. A bf16 result adds half a step, 2^-8 of its
+2^-126 and m = sqrt(1 - a^2) = sqrt(2 |L|) by sqrt(2 rate 2^-126), about 1e-19; and the input's gate,
+so that u is off by |x| 2^-126 (where the least reciprocal of a number below 2^126 stands for zero, by
+1.001 times that: TINY). A bf16 result adds half a step, 2^-8 of its
 size.
 """
 from __future__ import annotations
@@ -24,7 +26,7 @@ from __future__ import annotations
 import torch
 
 U = 2.0 ** -24
-TINY = 2.0 ** -126
+TINY = 1.001 * 2.0 ** -126
 BF16_HALF = 2.0 ** -8
 
 
@@ -78,6 +80,7 @@ class Linear:
         self.EL = (4 * v.abs() + 96) * U
         self.EB = self.EL + (4 * vi.abs() + 32) * U
         b = self.m * self.u
+        self.uoff = TINY * x.abs() if self.i is not None else torch.zeros_like(x)
         n = x.shape[0]
         h, M = s0.clone(), s0.abs()
         N, E, R = torch.zeros_like(h), torch.zeros_like(h), torch.zeros_like(h)
@@ -88,7 +91,7 @@ class Linear:
             a = self.a[t]
             self.before[t], self.size[t], self.before_bound[t] = h, M, N + E + R
             N = a * (N + self.EL[t] * L[t].abs() * M) + TINY * M
-            E = a * E + self.EB[t] * b[t].abs() + self.moff * self.u[t].abs()
+            E = a * E + self.EB[t] * b[t].abs() + self.moff * self.u[t].abs() + self.uoff[t]
             h = a * h + b[t]
             M = a * M + b[t].abs()
             R = a * R + 6 * U * M
@@ -123,6 +126,7 @@ class Linear:
         Gb = Gb + (aL.abs() * self.size + second.abs() * self.u.abs()) * Mg * (own + self.EB)
         Gb = Gb + 2 * TINY * absL * Mg * (self.size + self.u.abs())
         Gb = Gb + Mg * (self.moff * self.u.abs() + self.moff ** 2 * self.size)
+        Gb = Gb + Mg * second.abs() * self.uoff
         draw, drawb = G * self.slope, Gb * self.slope + G.abs() * self.slope * own
         du = g * self.m
         dub = gb * self.m + Mg * (self.m * self.EB + self.moff)
@@ -130,9 +134,9 @@ class Linear:
         if self.i is None:
             out["dx"] = (du, dub)
         else:
-            out["dx"] = (du * self.i, dub * self.i + (du * self.i).abs() * self.EB)
+            out["dx"] = (du * self.i, dub * self.i + (du * self.i).abs() * self.EB + Mg * self.m * TINY)
             di = du * self.x * self.i * self.ioff
-            dib = (dub * self.x * self.i * self.ioff).abs() + di.abs() * 2 * self.EB
+            dib = (dub * self.x * self.i * self.ioff).abs() + di.abs() * 2 * self.EB + Mg * self.m * self.uoff
             out["din_raw"] = (di, dib)
             out["din_bias"] = (di.sum(0), dib.sum(0) + 64 * U * di.abs().sum(0))
         out["dA_log"] = (G.sum(0), Gb.sum(0) + 64 * U * G.abs().sum(0))
