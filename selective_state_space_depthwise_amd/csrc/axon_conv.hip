@@ -343,21 +343,24 @@ __global__ __launch_bounds__(64 * kBackWaves) void conv_back_kernel(ConvArgs g) 
     Raw<Act, V>::store(static_cast<Act*>(g.dx) + e + t * g.channels, zero);
 }
 
-// Sums of the workgroups' parts in 64 bits: a lane a sum, four waves take every fourth part.
-__global__ __launch_bounds__(256) void conv_sum_kernel(ConvArgs g, int parts) {
-  __shared__ double sums[4][64];
+// Sums of the workgroups' parts in 64 bits: a lane a sum, each wave takes every 16th part.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void conv_sum_kernel(ConvArgs g, int parts) {
+  __shared__ double sums[kSumWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e = blockIdx.x * 64 + lane, k = blockIdx.y;
   double s = 0.0;
   if (e < g.channels) {
     const float* from = g.partial + int64_t(k) * g.channels + e;
 #pragma unroll 8
-    for (int j = wave; j < parts; j += 4) s += from[int64_t(j) * kSums * g.channels];
+    for (int j = wave; j < parts; j += kSumWaves) s += from[int64_t(j) * kSums * g.channels];
   }
   sums[wave][lane] = s;
   __syncthreads();
   if (wave || e >= g.channels) return;
-  const float all = static_cast<float>(sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane]);
+#pragma unroll
+  for (int w = 1; w < kSumWaves; ++w) s += sums[w][lane];
+  const float all = static_cast<float>(s);
   if (k < kConv)
     g.dw[int64_t(e) * kConv + k] = all;
   else
@@ -546,7 +549,7 @@ axon_status axon_causal_conv_backward(const axon_conv_shape* shape, const void* 
     launch_back<bf16_bits, 4>(a, st);
   else
     vectors_ok(a, 2, es, true) ? launch_back<bf16_bits, 2>(a, st) : launch_back<bf16_bits, 1>(a, st);
-  hipLaunchKernelGGL(conv_sum_kernel, dim3((a.channels + 63) / 64, kSums), dim3(256), 0, st, a,
+  hipLaunchKernelGGL(conv_sum_kernel, dim3((a.channels + 63) / 64, kSums), dim3(64 * kSumWaves), 0, st, a,
                      static_cast<int>(back_parts(a.p.rows)));
   return hipGetLastError() == hipSuccess ? AXON_OK : AXON_ERR_HIP;
 }

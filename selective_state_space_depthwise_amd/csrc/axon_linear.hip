@@ -375,7 +375,7 @@ __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g
 // The same from the last tile to the first. A wave finds its block's states again from the block's
 // checkpoint and the parts of the waves in front of it.
 template <typename Act, int P, int WAVES, int GATE, int SCALE>
-__global__ __launch_bounds__(64 * WAVES, 5) void linear_tile_back_kernel(LinearArgs g) {
+__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_back_kernel(LinearArgs g) {
   static_assert(WAVES * P % kBlock == 0, "a tile holds whole blocks");
   constexpr int kBlockWaves = kBlock / P;
   __shared__ uint32_t ticket;
@@ -526,21 +526,25 @@ __global__ __launch_bounds__(64 * WAVES, 5) void linear_tile_back_kernel(LinearA
   }
 }
 
-// Sums of the tiles' parts in 64 bits: four waves take every fourth tile.
-__global__ __launch_bounds__(256) void linear_sum_kernel(LinearArgs g, int parts) {
-  __shared__ double sums[4][64];
+// Sums of the tiles' parts in 64 bits: a channel a lane, each wave takes every 16th tile.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void linear_sum_kernel(LinearArgs g, int parts) {
+  __shared__ double sums[kSumWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e = blockIdx.x * 64 + lane, which = blockIdx.y;
   double s = 0.0;
-  if (e < g.channels)
+  if (e < g.channels) {
+    const float* from = g.partial + int64_t(which) * g.channels + e;
 #pragma unroll 8
-    for (int j = wave; j < parts; j += 4)
-      s += g.partial[(int64_t(j) * 3 + which) * g.channels + e];
+    for (int j = wave; j < parts; j += kSumWaves) s += from[int64_t(j) * 3 * g.channels];
+  }
   sums[wave][lane] = s;
   __syncthreads();
   if (wave || e >= g.channels) return;
+#pragma unroll
+  for (int w = 1; w < kSumWaves; ++w) s += sums[w][lane];
   float* out = which == 0 ? g.dA_log : which == 1 ? g.ddt_bias : g.din_bias;
-  out[e] = static_cast<float>(sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane]);
+  out[e] = static_cast<float>(s);
 }
 
 template <typename Act>
@@ -620,8 +624,13 @@ size_t tables_bytes(const Packed& p) {
   return p.starts ? 4 * (2 * (size_t(p.sequences) + 1) + 2 * size_t(p.rows)) : 0;
 }
 
-constexpr int kTokens = 16, kWaves = 12;        // tokens a wave, waves a tile
-constexpr int kBackTokens = 8, kBackWaves = 8;  // of the backward pass
+// Tokens a wave and waves a tile. Forward: 12 waves of 16 tokens, two workgroups a CU (16384 tokens x
+// 2560 bf16 102 us; 8 waves 107 us, 4 waves 148 us, 8 waves of 8 tokens 143 us). Backward bf16: 4 waves of
+// 16 tokens, three workgroups a CU (8 x 2048 tokens x 2560, with the forward pass, 275 us; 8 waves of 8
+// tokens 304 us); fp32: 8 waves of 8 (3 x 1999 tokens x 1001 79 us against 86 us).
+constexpr int kTokens = 16, kWaves = 12;
+constexpr int kBackTokens = 16, kBackWaves = 4;      // bf16
+constexpr int kBackTokens32 = 8, kBackWaves32 = 8;   // fp32
 
 // Tiles, and what of the workspace they use.
 struct Plan {
@@ -634,6 +643,7 @@ Plan plan_linear(const axon_linear_shape& s, bool packed, bool backward) {
   Plan p{};
   // rows of the tables, or sequences without tokens, at least one tile
   const int64_t rows = std::max<int64_t>(packed_rows(s.sequences, s.tokens, packed), 1);
+  static_assert(kBackTokens * kBackWaves == kBackTokens32 * kBackWaves32, "tiles of one size");
   const int64_t blocks = (backward ? kBackTokens * kBackWaves : kTokens * kWaves) / kBlock;
   p.tiles = (rows + blocks - 1) / blocks;
   p.groups = (s.channels + 63) / 64;
@@ -679,7 +689,9 @@ dim3 tile_grid(const Plan& p) {
 
 template <bool BACK, typename Act, int GATE>
 void launch_scale(const LinearArgs& a, dim3 grid, hipStream_t st) {
-  constexpr int P = BACK ? kBackTokens : kTokens, W = BACK ? kBackWaves : kWaves;
+  constexpr bool kWide = sizeof(Act) == 4;
+  constexpr int P = !BACK ? kTokens : kWide ? kBackTokens32 : kBackTokens;
+  constexpr int W = !BACK ? kWaves : kWide ? kBackWaves32 : kBackWaves;
 #define AXON_LAUNCH(SCALE)                                                                              \
   if constexpr (BACK)                                                                                   \
     hipLaunchKernelGGL((linear_tile_back_kernel<Act, P, W, GATE, SCALE>), grid, dim3(64 * W), 0, st, a); \
@@ -848,7 +860,7 @@ axon_status axon_linear_scan_backward(const axon_linear_shape* shape,
   clear_chain(plan, workspace, st);
   launch_tiles<true>(a, plan, bf, st);
   hipLaunchKernelGGL(linear_sum_kernel, dim3(channel_groups(a.channels, 64), din_bias ? 3 : 2),
-                     dim3(256), 0, st, a, a.tiles);
+                     dim3(64 * kSumWaves), 0, st, a, a.tiles);
   return hipGetLastError() == hipSuccess ? AXON_OK : AXON_ERR_HIP;
 }
 
