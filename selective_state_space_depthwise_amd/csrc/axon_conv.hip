@@ -25,6 +25,7 @@ struct ConvArgs {
   Packed p;
   int64_t x_stride, dy_stride;
   int channels, silu, clear_behind;
+  bool past;  // y, dx are stored past the caches
   const float* cache_in;
   const int32_t *in_slots, *out_slots;
   int64_t in_count, out_count;
@@ -43,6 +44,7 @@ struct Raw {
   Act v;
   __device__ __forceinline__ void load(const Act* p) { v = *p; }
   __device__ __forceinline__ void get(float* o) const { o[0] = load_act(&v, 0); }
+  template <bool>
   static __device__ __forceinline__ void store(Act* p, const float* o) { store_act(p, 0, o[0]); }
 };
 template <>
@@ -50,23 +52,20 @@ struct Raw<float, 4> {
   float4 v;
   __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
   __device__ __forceinline__ void get(float* o) const { o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w; }
-  static __device__ __forceinline__ void store(float* p, const float* o) {
-    *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
-  }
+  template <bool PAST>
+  static __device__ __forceinline__ void store(float* p, const float* o) { store4<PAST>(p, o); }
 };
 __device__ __forceinline__ void widen2(uint32_t w, float* o) {
   o[0] = __uint_as_float(w << 16), o[1] = __uint_as_float(w & 0xFFFF0000u);
-}
-__device__ __forceinline__ uint32_t narrow2(const float* o) {
-  return static_cast<uint32_t>(f32_to_bf16(o[0])) | static_cast<uint32_t>(f32_to_bf16(o[1])) << 16;
 }
 template <>
 struct Raw<bf16_bits, 2> {
   uint32_t v;
   __device__ __forceinline__ void load(const bf16_bits* p) { v = *reinterpret_cast<const uint32_t*>(p); }
   __device__ __forceinline__ void get(float* o) const { widen2(v, o); }
+  template <bool>
   static __device__ __forceinline__ void store(bf16_bits* p, const float* o) {
-    *reinterpret_cast<uint32_t*>(p) = narrow2(o);
+    *reinterpret_cast<uint32_t*>(p) = f32_to_bf16x2(o[0], o[1]);
   }
 };
 template <>
@@ -74,9 +73,8 @@ struct Raw<bf16_bits, 4> {
   uint2 v;
   __device__ __forceinline__ void load(const bf16_bits* p) { v = *reinterpret_cast<const uint2*>(p); }
   __device__ __forceinline__ void get(float* o) const { widen2(v.x, o), widen2(v.y, o + 2); }
-  static __device__ __forceinline__ void store(bf16_bits* p, const float* o) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(narrow2(o), narrow2(o + 2));
-  }
+  template <bool PAST>
+  static __device__ __forceinline__ void store(bf16_bits* p, const float* o) { store4<PAST>(p, o); }
 };
 
 // The cache of sequence n at V channels from e on, zeros where there is none.
@@ -131,7 +129,7 @@ __device__ __forceinline__ int block_rows() {
 }
 
 // A wave: 64 V channels of one block. The next kAhead rows are on their way while kAhead are computed.
-template <typename Act, int V>
+template <typename Act, int V, bool PAST>
 __global__ __launch_bounds__(64) void conv_kernel(ConvArgs g) {
   constexpr int kAhead = 8;
   const int e = (blockIdx.x * 64 + threadIdx.x) * V;
@@ -191,7 +189,7 @@ __global__ __launch_bounds__(64) void conv_kernel(ConvArgs g) {
           if (g.silu) p[i] = silu(p[i]);
           h[0][i] = h[1][i], h[1][i] = h[2][i], h[2][i] = v[i];
         }
-        if (j0 + j < b.count) Raw<Act, V>::store(yb + int64_t(j0 + j) * g.channels, p);
+        if (j0 + j < b.count) Raw<Act, V>::template store<PAST>(yb + int64_t(j0 + j) * g.channels, p);
       }
     }
   }
@@ -204,13 +202,13 @@ __global__ __launch_bounds__(64) void conv_kernel(ConvArgs g) {
   if (g.clear_behind) {
     const float zero[V] = {};
     for (int64_t t = int64_t(packed_start(g.p, g.p.sequences)) + row; t < g.p.tokens; t += rows)
-      Raw<Act, V>::store(y + t * g.channels, zero);
+      Raw<Act, V>::template store<false>(y + t * g.channels, zero);
   }
 }
 
 constexpr int kBackWaves = 4;  // blocks of a workgroup, whose sums are joined
 
-template <typename Act, int V>
+template <typename Act, int V, bool PAST>
 __global__ __launch_bounds__(64 * kBackWaves) void conv_back_kernel(ConvArgs g) {
   constexpr int kAhead = 4;
   __shared__ float joined[kBackWaves][kSums * V][64];
@@ -297,7 +295,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void conv_back_kernel(ConvArgs g) 
                         fmaf(taps.w[2][i], s2d[i], fmaf(taps.w[1][i], s1d[i], taps.w[0][i] * s[i])));
             if (dco && kept >= 0) d[i] += dco[int64_t(kept) * g.channels + i];
           }
-          Raw<Act, V>::store(dxb + int64_t(j - kHalo) * g.channels, d);
+          Raw<Act, V>::template store<PAST>(dxb + int64_t(j - kHalo) * g.channels, d);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) s3d[i] = s2d[i], s2d[i] = s1d[i], s1d[i] = s[i];
@@ -340,7 +338,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void conv_back_kernel(ConvArgs g) 
         }
   const float zero[V] = {};
   for (int64_t t = int64_t(packed_start(g.p, g.p.sequences)) + row; t < g.p.tokens; t += rows)
-    Raw<Act, V>::store(static_cast<Act*>(g.dx) + e + t * g.channels, zero);
+    Raw<Act, V>::template store<false>(static_cast<Act*>(g.dx) + e + t * g.channels, zero);
 }
 
 // Sums of the workgroups' parts in 64 bits: a lane a sum, each wave takes every 16th part.
@@ -410,6 +408,7 @@ ConvArgs make_args(const axon_conv_shape& s, const void* x, const float* w, cons
   a.dy_stride = s.dy_stride ? s.dy_stride : s.channels;
   a.channels = static_cast<int>(s.channels);
   a.silu = s.activation == AXON_CONV_SILU, a.clear_behind = s.clear_behind;
+  a.past = past_caches(size_t(s.tokens * s.channels) * (s.act_dtype == AXON_BF16 ? 2 : 4));
   return a;
 }
 
@@ -438,12 +437,19 @@ bool vectors_ok(const ConvArgs& a, int v, size_t es, bool backward) {
 
 template <typename Act, int V>
 void launch_conv(const ConvArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((conv_kernel<Act, V>), block_grid(a.channels, 64 * V, a.p.rows), dim3(64), 0, st, a);
+  const dim3 grid = block_grid(a.channels, 64 * V, a.p.rows);
+  if (V == 4 && a.past)
+    hipLaunchKernelGGL((conv_kernel<Act, V, V == 4>), grid, dim3(64), 0, st, a);
+  else
+    hipLaunchKernelGGL((conv_kernel<Act, V, false>), grid, dim3(64), 0, st, a);
 }
 template <typename Act, int V>
 void launch_back(const ConvArgs& a, hipStream_t st) {
   const dim3 grid = block_grid(a.channels, 64 * V, (a.p.rows + kBackWaves - 1) / kBackWaves);
-  hipLaunchKernelGGL((conv_back_kernel<Act, V>), grid, dim3(64 * kBackWaves), 0, st, a);
+  if (V == 4 && a.past)
+    hipLaunchKernelGGL((conv_back_kernel<Act, V, V == 4>), grid, dim3(64 * kBackWaves), 0, st, a);
+  else
+    hipLaunchKernelGGL((conv_back_kernel<Act, V, false>), grid, dim3(64 * kBackWaves), 0, st, a);
 }
 
 }  // namespace

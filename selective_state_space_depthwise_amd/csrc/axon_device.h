@@ -55,8 +55,29 @@ __device__ __forceinline__ void store_act(float* p, int64_t i, float v) { p[i] =
 __device__ __forceinline__ bf16_bits f32_to_bf16(float v) {
   return __builtin_bit_cast(bf16_bits, static_cast<__bf16>(v));
 }
+// Two of them side by side, the first in the low half: one instruction.
+__device__ __forceinline__ uint32_t f32_to_bf16x2(float a, float b) {
+  typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+  const pair_t p = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+  return __builtin_bit_cast(uint32_t, p);
+}
 __device__ __forceinline__ void store_act(bf16_bits* p, int64_t i, float v) {
   p[i] = f32_to_bf16(v);
+}
+// Four values at once; PAST: not kept in the caches, for outputs larger than those (past_caches).
+template <bool PAST>
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  const f4 t = {v[0], v[1], v[2], v[3]};
+  if constexpr (PAST) __builtin_nontemporal_store(t, reinterpret_cast<f4*>(p));
+  else *reinterpret_cast<f4*>(p) = t;
+}
+template <bool PAST>
+__device__ __forceinline__ void store4(bf16_bits* p, const float* v) {
+  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+  const u2 t = {f32_to_bf16x2(v[0], v[1]), f32_to_bf16x2(v[2], v[3])};
+  if constexpr (PAST) __builtin_nontemporal_store(t, reinterpret_cast<u2*>(p));
+  else *reinterpret_cast<u2*>(p) = t;
 }
 
 // Raw buffer access: a wave-uniform 128-bit resource (base address in SGPRs) plus a 32-bit
