@@ -25,6 +25,7 @@ struct LinearArgs {
   Packed p;
   int64_t x_stride, dt_stride, in_stride, dy_stride;
   int channels, gate, input_scale, clear_behind;
+  bool past;  // y and the gradients are stored past the caches
   int tiles, groups;  // tiles of blocks, groups of 64 channels
   // scan, step
   const float* state_in;
@@ -143,6 +144,18 @@ struct Rows {
   }
   __device__ __forceinline__ float operator[](int j) const { return widen(v[j]); }
 };
+
+// A value of the row at the scalar offset `row`; PAST: not kept in the caches (past_caches).
+template <bool PAST>
+__device__ __forceinline__ void store_row(const float*, rsrc_t r, uint32_t off, uint32_t row, float v) {
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, off, row, PAST ? 2 : 0);
+}
+template <bool PAST>
+__device__ __forceinline__ void store_row(const bf16_bits*, rsrc_t r, uint32_t off, uint32_t row, float v) {
+  __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v), r, off, row, PAST ? 2 : 0);
+}
+struct Past { static constexpr bool value = true; };
+struct Kept { static constexpr bool value = false; };
 
 // ---- What tiles tell each other -----------------------------------------------------------------
 // A tile first publishes its own part (the sum of its log2 a, and h from zero), then, once it knows what
@@ -344,11 +357,15 @@ __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g
       if (s.opens && g.checkpoints) g.checkpoints[int64_t(s.row) * g.channels + e] = h;
       const rsrc_t y = make_rsrc(static_cast<Act*>(g.y) + int64_t(s.first) * g.channels);
       const uint32_t step = static_cast<uint32_t>(g.channels) * sizeof(Act), off = e * sizeof(Act);
+      auto states = [&](auto past) {
 #pragma unroll
-      for (int j = 0; j < P; ++j) {
-        h = fmaf(a[j], h, b[j]);
-        if (j < s.count) store_buf_s<Act>(y, off, j * step, h);
-      }
+        for (int j = 0; j < P; ++j) {
+          h = fmaf(a[j], h, b[j]);
+          if (j < s.count) store_row<decltype(past)::value>(static_cast<Act*>(nullptr), y, off, j * step, h);
+        }
+      };
+      if (g.past) states(Past{});
+      else states(Kept{});
       if (s.ends && g.state_out) {
         const int64_t slot = g.out_slots ? table_at(g.out_slots, s.seq) : s.seq;
         if (slot >= 0 && slot < g.out_count) g.state_out[slot * g.channels + e] = h;
@@ -483,21 +500,27 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
     const rsrc_t ddt = make_rsrc(static_cast<Act*>(g.ddt_raw) + first);
     const rsrc_t din = make_rsrc(static_cast<Act*>(g.din_raw) + (g.in_raw ? first : 0));
     const uint32_t step = static_cast<uint32_t>(g.channels) * sizeof(Act), off = e * sizeof(Act);
+    auto grads = [&](auto past) {
+      constexpr Act* kType = nullptr;
+      constexpr bool kPast = decltype(past)::value;
 #pragma unroll
-    for (int j = P - 1; j >= 0; --j) {
-      if (j >= s.count) continue;
-      const float gt = dy[j] + k;
-      k = av[j] * gt;
-      const float G = gt * w[j], odt = G * slope[j], oin = gt * mz[j];
-      sA += G;
-      sdt += odt;
-      sin += oin;
-      if (in_range) {
-        store_buf_s<Act>(ddt, off, j * step, odt);
-        store_buf_s<Act>(dx, off, j * step, gt * mo[j]);
-        if (g.in_raw) store_buf_s<Act>(din, off, j * step, oin);
+      for (int j = P - 1; j >= 0; --j) {
+        if (j >= s.count) continue;
+        const float gt = dy[j] + k;
+        k = av[j] * gt;
+        const float G = gt * w[j], odt = G * slope[j], oin = gt * mz[j];
+        sA += G;
+        sdt += odt;
+        sin += oin;
+        if (in_range) {
+          store_row<kPast>(kType, ddt, off, j * step, odt);
+          store_row<kPast>(kType, dx, off, j * step, gt * mo[j]);
+          if (g.in_raw) store_row<kPast>(kType, din, off, j * step, oin);
+        }
       }
-    }
+    };
+    if (g.past) grads(Past{});
+    else grads(Kept{});
     if (s.begins && g.dstate_in && in_range) g.dstate_in[int64_t(s.seq) * g.channels + e] = k;
   }
   totals[wave][0][lane] = sA;
@@ -606,6 +629,7 @@ LinearArgs make_args(const axon_linear_shape& s, const axon_linear_params& p, co
   a.dy_stride = s.dy_stride ? s.dy_stride : s.channels;
   a.channels = static_cast<int>(s.channels);
   a.gate = s.gate, a.input_scale = s.input_scale, a.clear_behind = s.clear_behind;
+  a.past = past_caches(size_t(s.tokens * s.channels) * (s.act_dtype == AXON_BF16 ? 2 : 4));
   return a;
 }
 
