@@ -23,6 +23,14 @@ namespace {
 constexpr int kWaves = 4;   // of a workgroup
 constexpr int kFlush = 32;  // rows
 
+// Backward workgroups that a CU holds at once, as registers allow; as many are started, since a second
+// round of them finds the CUs half empty (16384 rows of 40 heads of 128 bf16 with four a CU 111 us, of which
+// one head group a wave is asked for at a time; three a CU and two groups 120 us, and 150 us with four started.
+// fp32, 8192 rows of 20 heads: 54 us and 48 us, for four spill).
+template <typename Act>
+constexpr int kBackFit = sizeof(Act) == 2 ? 4 : 3;
+constexpr int kCus = 256;
+
 struct RotateArgs {
   const void *q, *k, *dq_out, *dk_out;
   const int32_t* positions;
@@ -153,7 +161,7 @@ struct Tensor {
 
 // Groups of heads are of q or of k, so that a wave's pointers and weights do not differ between lanes.
 template <typename Act, int V, int UNITS, int G, bool SIDE, bool PAST, bool BACK>
-__global__ __launch_bounds__(64 * kWaves) void rotate_kernel(RotateArgs g) {
+__global__ __launch_bounds__(64 * kWaves, BACK ? kBackFit<Act> : 1) void rotate_kernel(RotateArgs g) {
   using P = Pairs<Act, V, SIDE>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = lane & (g.lanes - 1), sub = lane / g.lanes, per = 64 / g.lanes;
@@ -347,31 +355,46 @@ __global__ __launch_bounds__(64 * kWaves) void rotate_kernel(RotateArgs g) {
   }
 }
 
-// Sums of the workgroups' parts: a wave for each of 2 D values.
-__global__ __launch_bounds__(64) void rotate_sum_kernel(const float* partial, int parts, int dim,
-                                                        float* dq_weight, float* dk_weight) {
-  const int t = blockIdx.x;
-  float* out = t < dim ? dq_weight : dk_weight;
-  if (!out) return;
+// Sums of the workgroups' parts, 16 of the 2 D values a workgroup: 64 threads take a value's parts in turn,
+// in 64 bits, joined in a fixed order.
+constexpr int kSumWaves = 16, kSumValues = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void rotate_sum_kernel(const float* partial, int parts, int dim,
+                                                                    float* dq_weight, float* dk_weight) {
+  __shared__ double part[kSumWaves][kSumValues];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = blockIdx.x * kSumValues + (threadIdx.x & (kSumValues - 1));
   double s = 0.0;
-  for (int p = threadIdx.x; p < parts; p += 64) s += partial[int64_t(p) * 2 * dim + t];
-  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d, 64);
-  if (threadIdx.x == 0) out[t < dim ? t : t - dim] = static_cast<float>(s);
+  if (t < 2 * dim) {
+#pragma unroll 8
+    for (int p = threadIdx.x / kSumValues; p < parts; p += 64 * kSumWaves / kSumValues)
+      s += partial[int64_t(p) * 2 * dim + t];
+  }
+  for (int d = kSumValues; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+  if (lane < kSumValues) part[wave][lane] = s;
+  __syncthreads();
+  if (threadIdx.x >= kSumValues || t >= 2 * dim) return;
+  s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kSumWaves; ++w) s += part[w][threadIdx.x];
+  float* out = t < dim ? dq_weight : dk_weight;
+  if (out) out[t < dim ? t : t - dim] = static_cast<float>(s);
 }
 
 // Workgroups that run at once and take item after item, so that weights and frequencies are read seldom:
 // five a CU forward (16384 rows of 40 heads of 128 bf16 73 us; 2048 of them 83 us, 1024 80 us).
-constexpr int kWorkgroups = 1280, kBackWorkgroups = 1024;
-int back_workgroups(int64_t rows) {
-  return static_cast<int>(std::min<int64_t>((rows + kWaves - 1) / kWaves, kBackWorkgroups));
+constexpr int kWorkgroups = 1280;
+int back_workgroups(int64_t rows, bool bf16) {
+  const int64_t most = kCus * (bf16 ? kBackFit<bf16_bits> : kBackFit<float>);
+  return static_cast<int>(std::min((rows + kWaves - 1) / kWaves, most));
 }
 
 template <typename Act, int V, int UNITS, bool SIDE, bool BACK>
 void launch_units(RotateArgs a, hipStream_t st) {
-  constexpr int G = BACK ? 2 : V == 1 ? 2 : 5;
+  constexpr bool bf16 = sizeof(Act) == 2;
+  constexpr int G = BACK ? (bf16 ? 1 : 2) : V == 1 ? 2 : 5;
   const int per = 64 / a.lanes;
   const int groups = (a.q_heads + per - 1) / per + (a.heads - a.q_heads + per - 1) / per;
-  int64_t wgs = back_workgroups(a.rows);
+  int64_t wgs = back_workgroups(a.rows, bf16);
   a.splits = 1;
   if constexpr (!BACK) {
     // A row's heads are shared out to as many waves as keep G groups each: more even than whole rows (73 us
@@ -494,7 +517,7 @@ axon_status axon_norm_rotate(const axon_norm_rotate_desc* desc, const void* q, c
 
 size_t axon_norm_rotate_backward_workspace_bytes(const axon_norm_rotate_desc* desc) {
   if (axon::check_desc(desc, true) != AXON_OK) return 0;
-  return 4 * 2 * size_t(axon::back_workgroups(desc->rows)) * size_t(desc->head_dim);
+  return 4 * 2 * size_t(axon::back_workgroups(desc->rows, desc->act_dtype == AXON_BF16)) * size_t(desc->head_dim);
 }
 
 axon_status axon_norm_rotate_backward(const axon_norm_rotate_desc* desc, const void* dq_out,
@@ -550,8 +573,8 @@ axon_status axon_norm_rotate_backward(const axon_norm_rotate_desc* desc, const v
     bf ? launch_rotate<bf16_bits, true>(a, wide, st) : launch_rotate<float, true>(a, wide, st);
   }
   if (dq_weight || dk_weight)
-    hipLaunchKernelGGL(rotate_sum_kernel, dim3(static_cast<unsigned>(2 * d.head_dim)), dim3(64), 0,
-                       st, a.partial, back_workgroups(d.rows), a.dim, dq_weight, dk_weight);
+    hipLaunchKernelGGL(rotate_sum_kernel, dim3(static_cast<unsigned>((2 * d.head_dim + kSumValues - 1) / kSumValues)),
+                       dim3(64 * kSumWaves), 0, st, a.partial, back_workgroups(d.rows, bf), a.dim, dq_weight, dk_weight);
   return hipGetLastError() == hipSuccess ? AXON_OK : AXON_ERR_HIP;
 }
 
