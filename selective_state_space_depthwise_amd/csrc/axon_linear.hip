@@ -15,6 +15,7 @@
 
 #include "axon_device.h"
 #include "axon_packed.h"
+#include "axon_wide.h"
 
 namespace axon {
 namespace {
@@ -177,12 +178,14 @@ constexpr int kWindow = 2;  // tiles looked at
 
 // Waits for what tile `from` hands on; tiles go down from it (DIR -1) or up (DIR 1), `left` of them.
 // `column`: of the lane, among the `columns` of a tile. Every tile's workgroup has started once a later
-// ticket is out, and none of them waits for a later one, so that the wait ends.
+// ticket is out, and none of them waits for a later one, so that the wait ends. (Two calls at once in one
+// workspace, which no caller may make, could wipe what was told: the wait is given up after seconds, as NaN.)
+constexpr int kPatience = 1 << 22;
 template <int DIR>
 __device__ __forceinline__ float hear(const LinearArgs& g, int from, int left, int64_t columns,
                                       int64_t column) {
   const int n = min(left, kWindow);
-  for (;;) {
+  for (int looks = 0; looks < kPatience; ++looks) {
     uint32_t c[kWindow];
     uint64_t s[kWindow];
 #pragma unroll
@@ -213,6 +216,7 @@ __device__ __forceinline__ float hear(const LinearArgs& g, int from, int left, i
     }
     __builtin_amdgcn_s_sleep(2);
   }
+  return __builtin_nanf("");
 }
 
 __global__ __launch_bounds__(256) void linear_clear_kernel(uint4* p, int64_t count) {
@@ -298,7 +302,7 @@ __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g
   __shared__ Parts<WAVES> sh;
   const uint32_t t = take_ticket(g, &ticket);
   const int tile = t / g.groups, grp = t - tile * g.groups;
-  if (tile >= g.tiles) return;
+  if (static_cast<uint32_t>(tile) >= static_cast<uint32_t>(g.tiles)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const bool in_range = grp * 64 + lane < g.channels;
   const int e = min(grp * 64 + lane, g.channels - 1);
@@ -400,7 +404,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
   __shared__ float states[WAVES][64], totals[WAVES][3][64];
   const uint32_t t = take_ticket(g, &ticket);
   const int turn = t / g.groups, grp = t - turn * g.groups;
-  if (turn >= g.tiles) return;
+  if (static_cast<uint32_t>(turn) >= static_cast<uint32_t>(g.tiles)) return;
   const int tile = g.tiles - 1 - turn;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const bool in_range = grp * 64 + lane < g.channels;
@@ -570,27 +574,45 @@ __global__ __launch_bounds__(64 * kSumWaves) void linear_sum_kernel(LinearArgs g
   out[e] = static_cast<float>(s);
 }
 
-template <typename Act>
+// V channels of a row a thread, all asked for before the first is used.
+template <typename Act, int V>
 __global__ __launch_bounds__(256) void linear_step_kernel(LinearArgs g) {
-  const int e = blockIdx.x * 256 + threadIdx.x, n = blockIdx.y;
+  const int e = (blockIdx.x * 256 + threadIdx.x) * V, n = blockIdx.y;
   if (e >= g.channels) return;
   const int64_t slot = g.in_slots ? g.in_slots[n] : n;
   if (slot < 0 || slot >= g.in_count) return;
-  const Act* in = static_cast<const Act*>(g.in_raw);
-  const float v =
-      load_act(static_cast<const Act*>(g.dt_raw), n * g.dt_stride + e) + (g.dt_bias ? g.dt_bias[e] : 0.0f);
-  float u = load_act(static_cast<const Act*>(g.x), n * g.x_stride + e);
-  const float rate = -expf(g.A_log[e]) * kLog2e;
-  const float l2 = g.gate == AXON_LINEAR_SIGMOID ? log2_decay<AXON_LINEAR_SIGMOID>(rate, v, 0.0f)
-                                                 : log2_decay<AXON_LINEAR_SOFTPLUS>(rate, v, 0.0f);
-  const float a = __builtin_amdgcn_exp2f(l2);
-  if (g.input_scale == AXON_INPUT_COMPLEMENT) u *= input_factor<AXON_INPUT_COMPLEMENT>(l2, a);
-  if (g.input_scale == AXON_INPUT_SQRT) u *= input_factor<AXON_INPUT_SQRT>(l2, a);
-  if (in) u *= sigmoid_f32(load_act(in, n * g.in_stride + e) + (g.in_bias ? g.in_bias[e] : 0.0f), 0.0f);
   float* state = g.state_out + slot * g.channels + e;
-  const float h = advance(carry_of(l2), *state, u);
-  *state = h;
-  store_act(static_cast<Act*>(g.y), int64_t(n) * g.channels + e, h);
+  Raw<Act, V> x, raw, in;
+  Raw<float, V> old, A_log, bias, in_bias;
+  raw.load(static_cast<const Act*>(g.dt_raw) + n * g.dt_stride + e);
+  x.load(static_cast<const Act*>(g.x) + n * g.x_stride + e);
+  if (g.in_raw) in.load(static_cast<const Act*>(g.in_raw) + n * g.in_stride + e);
+  old.load(state);
+  A_log.load(g.A_log + e);
+  if (g.dt_bias) bias.load(g.dt_bias + e);
+  if (g.in_raw && g.in_bias) in_bias.load(g.in_bias + e);
+  float u[V], v[V], i_raw[V], h[V], rate[V], b[V] = {}, ib[V] = {};
+  x.get(u);
+  raw.get(v);
+  old.get(h);
+  A_log.get(rate);
+  if (g.in_raw) in.get(i_raw);
+  if (g.dt_bias) bias.get(b);
+  if (g.in_raw && g.in_bias) in_bias.get(ib);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    rate[i] = -expf(rate[i]) * kLog2e;
+    const float l2 = g.gate == AXON_LINEAR_SIGMOID
+                         ? log2_decay<AXON_LINEAR_SIGMOID>(rate[i], v[i] + b[i], 0.0f)
+                         : log2_decay<AXON_LINEAR_SOFTPLUS>(rate[i], v[i], b[i]);
+    const float a = __builtin_amdgcn_exp2f(l2);
+    if (g.input_scale == AXON_INPUT_COMPLEMENT) u[i] *= input_factor<AXON_INPUT_COMPLEMENT>(l2, a);
+    if (g.input_scale == AXON_INPUT_SQRT) u[i] *= input_factor<AXON_INPUT_SQRT>(l2, a);
+    if (g.in_raw) u[i] *= sigmoid_f32(i_raw[i] + ib[i], 0.0f);
+    h[i] = advance(carry_of(l2), h[i], u[i]);
+  }
+  Raw<float, V>::template store<false>(state, h);
+  Raw<Act, V>::template store<false>(static_cast<Act*>(g.y) + int64_t(n) * g.channels + e, h);
 }
 
 axon_status check_shape(const axon_linear_shape* s, bool backward) {
@@ -655,6 +677,10 @@ size_t tables_bytes(const Packed& p) {
 constexpr int kTokens = 16, kWaves = 12;
 constexpr int kBackTokens = 16, kBackWaves = 4;      // bf16
 constexpr int kBackTokens32 = 8, kBackWaves32 = 8;   // fp32
+
+// Rows x channels from which a step takes four channels a thread: 512 rows x 2560 bf16 16.4 -> 12.0 us from
+// memory, 256 rows 4.0 and 4.1 us in the caches, one row 2.1 and 2.9 us.
+constexpr int64_t kStepWide = 1 << 20;
 
 // Tiles, and what of the workspace they use.
 struct Plan {
@@ -745,6 +771,22 @@ void launch_tiles(const LinearArgs& a, const Plan& plan, bool bf, hipStream_t st
 
 unsigned channel_groups(int channels, int width) {
   return static_cast<unsigned>((channels + width - 1) / width);
+}
+
+// Four channels a thread where alignment allows it and there are threads enough.
+template <typename Act>
+void launch_step(const LinearArgs& a, hipStream_t st) {
+  const size_t wide = 4 * sizeof(Act);
+  const int64_t values = int64_t(a.channels) * a.p.sequences;
+  if (values >= kStepWide && a.channels % 4 == 0 && a.x_stride % 4 == 0 && a.dt_stride % 4 == 0 &&
+      a.in_stride % 4 == 0 && aligned_to(a.x, wide) && aligned_to(a.dt_raw, wide) && aligned_to(a.in_raw, wide) &&
+      aligned_to(a.y, wide) && aligned_to(a.state_out, 16) && aligned_to(a.A_log, 16) &&
+      aligned_to(a.dt_bias, 16) && aligned_to(a.in_bias, 16))
+    hipLaunchKernelGGL((linear_step_kernel<Act, 4>), dim3(channel_groups(a.channels, 1024), a.p.sequences),
+                       dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((linear_step_kernel<Act, 1>), dim3(channel_groups(a.channels, 256), a.p.sequences),
+                       dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -913,12 +955,8 @@ axon_status axon_linear_step(const axon_linear_shape* shape, const axon_linear_p
     if (overlaps(out, r) || overlaps(pool, r)) return AXON_ERR_INVALID_ARGUMENT;
   if (overlaps(out, pool)) return AXON_ERR_INVALID_ARGUMENT;
   a.state_out = state, a.in_slots = slots, a.in_count = s.state_slots, a.y = y;
-  const dim3 grid(channel_groups(a.channels, 256), a.p.sequences);
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  if (bf)
-    hipLaunchKernelGGL(linear_step_kernel<bf16_bits>, grid, dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL(linear_step_kernel<float>, grid, dim3(256), 0, st, a);
+  bf ? launch_step<bf16_bits>(a, static_cast<hipStream_t>(stream))
+     : launch_step<float>(a, static_cast<hipStream_t>(stream));
   return hipGetLastError() == hipSuccess ? AXON_OK : AXON_ERR_HIP;
 }
 

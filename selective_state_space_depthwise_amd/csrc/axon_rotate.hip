@@ -16,6 +16,7 @@
 
 #include "axon_device.h"
 #include "axon_packed.h"
+#include "axon_wide.h"
 
 namespace axon {
 namespace {
@@ -44,36 +45,6 @@ struct RotateArgs {
   float eps, inv_dim;
   float* partial;  // backward: (workgroups, 2, dim)
 };
-
-// V channels as loaded, and as fp32.
-template <typename Act, int V>
-struct Raw {
-  Act v;
-  __device__ __forceinline__ void load(const Act* p) { v = *p; }
-  __device__ __forceinline__ void get(float* o) const { o[0] = load_act(&v, 0); }
-};
-template <>
-struct Raw<float, 4> {
-  float4 v;
-  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
-  __device__ __forceinline__ void get(float* o) const { o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w; }
-};
-template <>
-struct Raw<bf16_bits, 4> {
-  uint2 v;
-  __device__ __forceinline__ void load(const bf16_bits* p) { v = *reinterpret_cast<const uint2*>(p); }
-  __device__ __forceinline__ void get(float* o) const {
-    o[0] = __uint_as_float(v.x << 16), o[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    o[2] = __uint_as_float(v.y << 16), o[3] = __uint_as_float(v.y & 0xFFFF0000u);
-  }
-};
-template <typename Act, int V, bool PAST>
-__device__ __forceinline__ void store_v(Act* p, const float* v) {
-  if constexpr (V == 1)
-    store_act(p, 0, v[0]);
-  else
-    store4<PAST>(p, v);
-}
 
 // Where a unit's two pieces of V channels lie, and its first pair (turned units only).
 template <int V>
@@ -120,8 +91,8 @@ struct Pairs {
       z[SIDE ? 2 * i : i] = first[i];
       z[SIDE ? 2 * i + 1 : V + i] = second[i];
     }
-    store_v<Act, V, PAST>(p + u.lo, z);
-    store_v<Act, V, PAST>(p + u.hi, z + V);
+    Raw<Act, V>::template store<PAST>(p + u.lo, z);
+    Raw<Act, V>::template store<PAST>(p + u.hi, z + V);
   }
 };
 
