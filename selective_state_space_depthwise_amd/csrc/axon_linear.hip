@@ -26,7 +26,8 @@ struct LinearArgs {
   Packed p;
   int64_t x_stride, dt_stride, in_stride, dy_stride;
   int channels, gate, input_scale, clear_behind;
-  bool past;  // y and the gradients are stored past the caches
+  bool past;      // y and the gradients are stored past the caches
+  bool together;  // all waves of a tile look at the tiles in front
   int tiles, groups;  // tiles of blocks, groups of 64 channels
   // scan, step
   const float* state_in;
@@ -41,7 +42,7 @@ struct LinearArgs {
   float* partial;  // (tiles, 3, channels)
   // What tiles tell each other (tiles, 64 groups): all bits set where nothing is told yet.
   uint32_t* ticket;  // null: one tile
-  uint64_t* sums;    // log2 of the decay over a tile, and its own part
+  uint64_t* sums;    // decay over a tile, and its own part
   uint32_t* carry;   // what leaves it
 };
 
@@ -159,7 +160,7 @@ struct Past { static constexpr bool value = true; };
 struct Kept { static constexpr bool value = false; };
 
 // ---- What tiles tell each other -----------------------------------------------------------------
-// A tile first publishes its own part (the sum of its log2 a, and h from zero), then, once it knows what
+// A tile first publishes its own part (its decay, as for advance, and h from zero), then, once it knows what
 // enters it, what leaves it. A reader takes the nearest tile that has published the latter and applies
 // the parts between in the order in which those tiles do it themselves, so that the result does not
 // depend on who was first. Both are one atomic of the value itself: a NaN with all bits set stands for
@@ -167,8 +168,8 @@ struct Kept { static constexpr bool value = false; };
 __device__ __forceinline__ uint32_t told(float v) {
   return v != v ? 0x7FC00000u : __float_as_uint(v);
 }
-__device__ __forceinline__ void tell_sums(uint64_t* p, float log, float h) {
-  __hip_atomic_store(p, static_cast<uint64_t>(told(h)) << 32 | told(log), __ATOMIC_RELAXED,
+__device__ __forceinline__ void tell_part(uint64_t* p, float decay, float h) {
+  __hip_atomic_store(p, static_cast<uint64_t>(told(h)) << 32 | told(decay), __ATOMIC_RELAXED,
                      __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ void tell_carry(uint32_t* p, float h) {
@@ -209,7 +210,7 @@ __device__ __forceinline__ float hear(const LinearArgs& g, int from, int left, i
       for (int k = kWindow - 1; k >= 0; --k) {
         if (k == found) h = __uint_as_float(c[k]);
         else if (k < found)
-          h = advance(carry_of(__uint_as_float(static_cast<uint32_t>(s[k]))), h,
+          h = advance(__uint_as_float(static_cast<uint32_t>(s[k])), h,
                       __uint_as_float(static_cast<uint32_t>(s[k] >> 32)));
       }
       return h;
@@ -257,10 +258,61 @@ struct Front {
   }
 };
 
-// The tile's own part is told, and what enters it is found. alone: nothing enters; DIR, left as for hear.
+// Tiles looked at by each wave, where all do: with four waves three of them (131072 tokens x 64 bf16 backward
+// 229 us, two 302 us; four cost registers, 16384 x 2560 157 -> 165 us).
+template <int WAVES>
+constexpr int kLook = WAVES == 4 ? 3 : 2;
+// What all waves of a tile have read for each other.
+template <int WAVES>
+struct Look {
+  uint32_t carry[kLook<WAVES> * WAVES][64];
+  uint64_t sums[kLook<WAVES> * WAVES][64];
+  int told[kLook<WAVES> * WAVES];  // bit 0: the carry, bit 1: the sums
+};
+
+// As hear, by all waves of a tile.
 template <int DIR, int WAVES>
-__device__ __forceinline__ void exchange(const LinearArgs& g, Parts<WAVES>& sh, int lane, int tile,
-                                         int grp, bool alone, int left) {
+__device__ __forceinline__ float hear_all(const LinearArgs& g, Look<WAVES>& look, int wave, int lane, int from,
+                                          int left, int64_t columns, int64_t column) {
+  const int n = min(left, kLook<WAVES> * WAVES);
+  for (int looks = 0; looks < kPatience; ++looks) {
+#pragma unroll
+    for (int i = 0; i < kLook<WAVES>; ++i) {
+      const int k = wave * kLook<WAVES> + i;
+      const int64_t at = (from + DIR * min(k, n - 1)) * columns + column;
+      const uint32_t c = __hip_atomic_load(g.carry + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const uint64_t s = __hip_atomic_load(g.sums + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      look.carry[k][lane] = c;
+      look.sums[k][lane] = s;
+      const int told = (__all(c != ~0u) ? 1 : 0) | (__all(s != ~uint64_t(0)) ? 2 : 0);
+      if (lane == 0) look.told[k] = told;
+    }
+    __syncthreads();
+    const int told = lane < n ? look.told[lane] : 0;
+    const uint64_t carries = __ballot(told & 1), sums = __ballot(told & 2);
+    const int found = carries ? __builtin_ctzll(carries) : -1;
+    if (found >= 0 && (~sums & ((uint64_t(1) << found) - 1)) == 0) {
+      float h = __uint_as_float(look.carry[found][lane]);
+#pragma unroll 8
+      for (int k = found - 1; k >= 0; --k) {
+        const uint64_t s = look.sums[k][lane];
+        h = advance(__uint_as_float(static_cast<uint32_t>(s)), h, __uint_as_float(static_cast<uint32_t>(s >> 32)));
+      }
+      return h;
+    }
+    __syncthreads();
+    __builtin_amdgcn_s_sleep(2);
+  }
+  return __builtin_nanf("");
+}
+
+// The tile's own part is told, and what enters it is found, by the wave that it enters first; where channels
+// are few by all waves, since then the chain of tiles is what takes the time. left as for hear.
+template <int DIR, int WAVES>
+__device__ __forceinline__ void exchange(const LinearArgs& g, Parts<WAVES>& sh, Look<WAVES>& look, int wave,
+                                         int lane, int tile, int grp, int left) {
+  constexpr int kFirst = DIR < 0 ? 0 : WAVES - 1;
+  if (wave != kFirst && !g.together) return;
   float sum = 0.0f, own = 0.0f;
   bool closed = false;  // a sequence begins (ends) in the tile: nothing passes through it
 #pragma unroll
@@ -273,16 +325,21 @@ __device__ __forceinline__ void exchange(const LinearArgs& g, Parts<WAVES>& sh, 
   }
   float before = 0.0f;
   if (g.ticket) {
+    const bool alone = left == 0 || sh.fresh[kFirst];  // nothing enters
     const int64_t columns = int64_t(g.groups) * 64, column = int64_t(grp) * 64 + lane;
     const int64_t at = tile * columns + column;
-    if (closed || alone) tell_carry(g.carry + at, own);
-    else tell_sums(g.sums + at, sum, own);
+    const float decay = carry_of(sum);
+    if (wave == kFirst) {
+      if (closed || alone) tell_carry(g.carry + at, own);
+      else tell_part(g.sums + at, decay, own);
+    }
     if (!alone) {
-      before = hear<DIR>(g, tile + DIR, left, columns, column);
-      if (!closed) tell_carry(g.carry + at, advance(carry_of(sum), before, own));
+      before = g.together ? hear_all<DIR>(g, look, wave, lane, tile + DIR, left, columns, column)
+                          : hear<DIR>(g, tile + DIR, left, columns, column);
+      if (wave == kFirst && !closed) tell_carry(g.carry + at, advance(decay, before, own));
     }
   }
-  sh.enter[lane] = before;
+  if (wave == kFirst) sh.enter[lane] = before;
 }
 
 // The unit (tile and channel group) of this workgroup: in the order in which workgroups start.
@@ -300,6 +357,7 @@ template <typename Act, int P, int WAVES, int GATE, int SCALE>
 __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g) {
   __shared__ uint32_t ticket;
   __shared__ Parts<WAVES> sh;
+  __shared__ Look<WAVES> look;
   const uint32_t t = take_ticket(g, &ticket);
   const int tile = t / g.groups, grp = t - tile * g.groups;
   if (static_cast<uint32_t>(tile) >= static_cast<uint32_t>(g.tiles)) return;
@@ -352,7 +410,7 @@ __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g
   }
   sh.put(wave, lane, L, h, s.begins);
   __syncthreads();
-  if (wave == 0) exchange<-1, WAVES>(g, sh, lane, tile, grp, tile == 0 || s.begins, tile);
+  exchange<-1, WAVES>(g, sh, look, wave, lane, tile, grp, tile);
   const Front<-1, WAVES> front(sh, wave, lane);
   __syncthreads();
   if (s.count > 0) {
@@ -401,6 +459,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
   constexpr int kBlockWaves = kBlock / P;
   __shared__ uint32_t ticket;
   __shared__ Parts<WAVES> sh;
+  __shared__ Look<WAVES> look;
   __shared__ float states[WAVES][64], totals[WAVES][3][64];
   const uint32_t t = take_ticket(g, &ticket);
   const int turn = t / g.groups, grp = t - turn * g.groups;
@@ -482,7 +541,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
   sh.put(wave, lane, L, k, s.ends);
   states[wave][lane] = h;
   __syncthreads();
-  if (wave == WAVES - 1) exchange<1, WAVES>(g, sh, lane, tile, grp, turn == 0 || s.ends, turn);
+  exchange<1, WAVES>(g, sh, look, wave, lane, tile, grp, turn);
   // The states in front of the wave's tokens.
   if (s.count > 0) {
     const int w0 = wave / kBlockWaves * kBlockWaves;
@@ -682,11 +741,18 @@ constexpr int kBackTokens32 = 8, kBackWaves32 = 8;   // fp32
 // memory, 256 rows 4.0 and 4.1 us in the caches, one row 2.1 and 2.9 us.
 constexpr int64_t kStepWide = 1 << 20;
 
+// Groups of channels up to which all waves of a tile look at the tiles in front, and tiles in a row from which
+// they do. Forward, bf16: 131072 tokens x 64 204 -> 61 us, 16384 x 512 46 -> 39 us, x 1024 52 -> 56 us, 21 tiles
+// in a row x 512 38 -> 39.5 us. Backward: 131072 x 64 572 -> 229 us, 16384 x 1024 108 -> 86 us, x 2560 158 ->
+// 167 us.
+constexpr int kFewGroups = 8, kFewGroupsBack = 16, kLongChain = 32;
+
 // Tiles, and what of the workspace they use.
 struct Plan {
   int64_t tiles, groups;
   size_t sums, carry, ticket, chain;  // offsets and bytes of what tiles tell each other; chain 0: nothing
   size_t bytes;
+  bool together;
 };
 
 Plan plan_linear(const axon_linear_shape& s, bool packed, bool backward) {
@@ -697,6 +763,8 @@ Plan plan_linear(const axon_linear_shape& s, bool packed, bool backward) {
   const int64_t blocks = (backward ? kBackTokens * kBackWaves : kTokens * kWaves) / kBlock;
   p.tiles = (rows + blocks - 1) / blocks;
   p.groups = (s.channels + 63) / 64;
+  p.together = p.groups <= (backward ? kFewGroupsBack : kFewGroups) &&
+               p.tiles / (packed ? 1 : s.sequences) >= kLongChain;
   const size_t cells = size_t(p.tiles) * size_t(p.groups) * 64;
   if (p.tiles > 1) {
     p.sums = 0;
@@ -715,6 +783,7 @@ size_t workspace_of(const axon_linear_shape& s, bool backward) {
 
 void use_plan(LinearArgs* a, const Plan& p, void* workspace) {
   a->tiles = static_cast<int>(p.tiles), a->groups = static_cast<int>(p.groups);
+  a->together = p.together;
   char* w = static_cast<char*>(workspace);
   if (p.chain) {
     a->sums = reinterpret_cast<uint64_t*>(w + p.sums);
