@@ -6,13 +6,19 @@
 // A head is held by LANES lanes (a power of two), a lane holds up to UNITS pieces of 2 V of its
 // channels: V of the first and V of the second halves of V pairs, or 2 V channels in order (pairs side
 // by side, or not turned). A wave takes 64 / LANES heads at a time and one row's heads one group after
-// the other, so that its angles are found once a row. Angles: p freqs / (2 pi) turns in 64 bits, of which only the
-// fraction goes to 32 bits.
+// the other, so that its angles are found once a row; where heads are few, the heads of several rows (ROWS).
+// Angles: p freqs / (2 pi) turns in 64 bits, of which only the fraction goes to 32 bits.
+//
+// Bound by memory: 16384 rows of 40 heads of 128 bf16 (336 MB) in 69-73 us, 4.6-4.9 TB/s where a copy of that
+// type reaches 5.4. What it took from 81 us: groups of one tensor (pointers and weights the same in all
+// lanes), sums whose exchanges are part of the addition, the values of five groups asked for before the
+// first is used, stores past the caches.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "axon_device.h"
 #include "axon_packed.h"
@@ -41,6 +47,7 @@ struct RotateArgs {
   int64_t rows, q_stride, k_stride, dq_stride, dk_stride;
   int q_heads, heads, dim, rotary, lanes, interleaved;
   int splits;  // forward: waves that share a row's heads
+  int group;   // heads of a row that a wave takes at a time; lanes beyond take other rows
   bool past;   // outputs are stored past the caches
   float eps, inv_dim;
   float* partial;  // backward: (workgroups, 2, dim)
@@ -131,11 +138,14 @@ struct Tensor {
 };
 
 // Groups of heads are of q or of k, so that a wave's pointers and weights do not differ between lanes.
-template <typename Act, int V, int UNITS, int G, bool SIDE, bool PAST, bool BACK>
+template <typename Act, int V, int UNITS, int G, bool SIDE, bool PAST, bool BACK, bool ROWS>
 __global__ __launch_bounds__(64 * kWaves, BACK ? kBackFit<Act> : 1) void rotate_kernel(RotateArgs g) {
   using P = Pairs<Act, V, SIDE>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l = lane & (g.lanes - 1), sub = lane / g.lanes, per = 64 / g.lanes;
+  const int l = lane & (g.lanes - 1), place = lane / g.lanes, per = ROWS ? g.group : 64 / g.lanes;
+  const int sub = ROWS ? place & (per - 1) : place;           // head of a group
+  const int ahead = ROWS ? place / per : 0;                   // row of an item's
+  const uint32_t together = ROWS ? 64 / (g.lanes * per) : 1;  // rows of an item
   const int q_groups = (g.q_heads + per - 1) / per, groups = q_groups + (g.heads - g.q_heads + per - 1) / per;
   P wq[UNITS], wk[UNITS], sq[BACK ? UNITS : 1], sk[BACK ? UNITS : 1];
   double turns[UNITS][V];
@@ -170,7 +180,7 @@ __global__ __launch_bounds__(64 * kWaves, BACK ? kBackFit<Act> : 1) void rotate_
         // lanes that hold the same channels of other heads, in a fixed order
         auto add = [&](float& v, int which, int at) {
           for (int d = g.lanes; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-          if (sub == 0 && u.live) part[wave][which][at] += v;
+          if (place == 0 && u.live) part[wave][which][at] += v;
           v = 0.0f;
         };
         const int first = SIDE ? (2 * i < V ? u.lo + 2 * i : u.hi + 2 * i - V) : u.lo + i;
@@ -188,10 +198,13 @@ __global__ __launch_bounds__(64 * kWaves, BACK ? kBackFit<Act> : 1) void rotate_
   }
   int pending = 0;
   // rows * splits < 2^31
-  const uint32_t items = static_cast<uint32_t>(g.rows * g.splits), step = gridDim.x * kWaves;
+  const uint32_t rows = static_cast<uint32_t>(g.rows), step = gridDim.x * kWaves;
+  const uint32_t items = (ROWS ? (rows + together - 1) / together : rows) * g.splits;
   for (uint32_t item = blockIdx.x * kWaves + wave; item < items; item += step) {
-    const uint32_t row = g.splits == 1 ? item : item / g.splits;
-    const int split = static_cast<int>(item - row * g.splits);
+    const uint32_t which = g.splits == 1 ? item : item / g.splits;
+    const int split = static_cast<int>(item - which * g.splits);
+    const bool held = !ROWS || which * together + ahead < rows;
+    const uint32_t row = ROWS ? min(which * together + ahead, rows - 1) : which;
     P c[UNITS];  // cosines and sines of the row
     for (int first = split; first < groups; first += g.splits * G) {
       // The values of G groups are asked for before the first is used (and before the row's angles).
@@ -206,7 +219,7 @@ __global__ __launch_bounds__(64 * kWaves, BACK ? kBackFit<Act> : 1) void rotate_
 #pragma unroll
         for (int n = 0; n < UNITS; ++n) {
           const Unit<V> u(g, l + n * g.lanes);
-          if (grp < groups && head + sub < t.heads && u.live) {
+          if (held && grp < groups && head + sub < t.heads && u.live) {
             rx[k][n][0].load(x + (sub * g.dim + u.lo));
             rx[k][n][1].load(x + (sub * g.dim + u.hi));
             if constexpr (BACK) {
@@ -236,7 +249,7 @@ __global__ __launch_bounds__(64 * kWaves, BACK ? kBackFit<Act> : 1) void rotate_
         const bool is_q = grp < q_groups;
         const Tensor<Act> t(g, is_q);
         const int head = (is_q ? grp : grp - q_groups) * per;
-        const bool in = head + sub < t.heads;
+        const bool in = held && head + sub < t.heads;
         Act* out = t.out + row * t.out_stride + int64_t(head) * g.dim;
         P v[UNITS];
         float sum = 0.0f;
@@ -351,9 +364,10 @@ __global__ __launch_bounds__(64 * kSumWaves) void rotate_sum_kernel(const float*
   if (out) out[t < dim ? t : t - dim] = static_cast<float>(s);
 }
 
-// Workgroups that run at once and take item after item, so that weights and frequencies are read seldom:
-// five a CU forward (16384 rows of 40 heads of 128 bf16 73 us; 2048 of them 83 us, 1024 80 us).
-constexpr int kWorkgroups = 1280;
+// Workgroups that run at once and take item after item, so that weights and frequencies are read seldom. Forward
+// five a CU, with their registers, else four (16384 rows of 40 heads of 128 bf16 73 us; eight 83 us, four 80 us;
+// fp32, 32768 rows of 16 heads of 64: four 45 us, five 49 us).
+int64_t forward_workgroups(bool bf16, bool rows) { return kCus * (bf16 && !rows ? 5 : 4); }
 int back_workgroups(int64_t rows, bool bf16) {
   const int64_t most = kCus * (bf16 ? kBackFit<bf16_bits> : kBackFit<float>);
   return static_cast<int>(std::min((rows + kWaves - 1) / kWaves, most));
@@ -363,21 +377,33 @@ template <typename Act, int V, int UNITS, bool SIDE, bool BACK>
 void launch_units(RotateArgs a, hipStream_t st) {
   constexpr bool bf16 = sizeof(Act) == 2;
   constexpr int G = BACK ? (bf16 ? 1 : 2) : V == 1 ? 2 : 5;
-  const int per = 64 / a.lanes;
-  const int groups = (a.q_heads + per - 1) / per + (a.heads - a.q_heads + per - 1) / per;
+  const int per = 64 / a.lanes, k_heads = a.heads - a.q_heads;
+  auto groups_of = [&](int n) { return (a.q_heads + n - 1) / n + (k_heads + n - 1) / n; };
+  // Heads of a wave at a time: as many as leave no more than a quarter of its places empty. Where one row cannot
+  // fill them a wave takes several (131072 rows of 1 + 1 heads of 64 bf16 93 -> 21 us, backward 136 -> 34 us).
+  a.group = per;
+  while (a.group > 1 && 4 * groups_of(a.group) * a.group > 5 * a.heads) a.group /= 2;
+  const int groups = groups_of(a.group), together = per / a.group;
+  const int64_t items = (a.rows + together - 1) / together;
   int64_t wgs = back_workgroups(a.rows, bf16);
   a.splits = 1;
   if constexpr (!BACK) {
     // A row's heads are shared out to as many waves as keep G groups each: more even than whole rows (73 us
     // against 77 us), and a decode batch has as many waves as it can.
     a.splits = static_cast<int>(std::min<int64_t>((groups + G - 1) / G, ((int64_t(1) << 31) - 1) / a.rows));
-    wgs = std::min<int64_t>((a.rows * a.splits + kWaves - 1) / kWaves, kWorkgroups);
+    wgs = std::min<int64_t>((items * a.splits + kWaves - 1) / kWaves,
+                            forward_workgroups(bf16, together > 1));
   }
   const dim3 grid(static_cast<unsigned>(wgs)), threads(64 * kWaves);
-  if (V == 4 && a.past)
-    hipLaunchKernelGGL((rotate_kernel<Act, V, UNITS, G, SIDE, V == 4, BACK>), grid, threads, 0, st, a);
-  else
-    hipLaunchKernelGGL((rotate_kernel<Act, V, UNITS, G, SIDE, false, BACK>), grid, threads, 0, st, a);
+  auto launch = [&](auto past, auto rows) {
+    hipLaunchKernelGGL((rotate_kernel<Act, V, UNITS, G, SIDE, decltype(past)::value, BACK, decltype(rows)::value>),
+                       grid, threads, 0, st, a);
+  };
+  const std::bool_constant<V == 4> past;  // one channel at a time is not stored so
+  const std::true_type yes;
+  const std::false_type no;
+  if (past && a.past) together > 1 ? launch(past, yes) : launch(past, no);
+  else together > 1 ? launch(no, yes) : launch(no, no);
 }
 
 template <typename Act, bool BACK>
