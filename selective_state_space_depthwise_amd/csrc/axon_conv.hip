@@ -1,11 +1,16 @@
 // Causal depthwise convolution of width 4 over packed or uniform sequences (see axonscan.h).
 //
-// A thread walks one channel of a block of 64 tokens with the last three inputs in registers.
-// Only a sequence's first block reads its cache, and the same thread then writes the final cache from
-// the sequence's last inputs, so that a cache may be updated in place without a wait between threads.
+// A wave walks a block of 64 tokens, V channels a lane, with the last three inputs in registers and the next
+// rows on their way. Only a sequence's first block reads its cache, and the same thread then writes the final
+// cache from the sequence's last inputs, so that a cache may be updated in place without a wait between threads.
+//
+// Bound by memory: packed 32768 x 7680 bf16 (1007 MB) in 210-214 us, 4.7-4.8 TB/s; a copy of as much takes
+// 187-207 us. What it took: four channels a lane (one: 380 us), eight rows ahead, stores past the caches
+// (219 -> 212 us); loads past the caches cost 224 us.
 //
 // Backward, with s_t = dy_t act'(p_t):  dxx_t = sum_k w[k] s_{t+3-k} + what dcache_out has for t,
-// dw[k] = sum_t s_t xx_{t-3+k},  db = sum_t s_t.  A block finds s of the three tokens behind it again.
+// dw[k] = sum_t s_t xx_{t-3+k},  db = sum_t s_t.  A block finds s of the three tokens behind it again, and four
+// blocks join their sums before they leave a part (with the forward pass 8 x 2048 x 7680 266 us).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -397,6 +402,17 @@ bool vectors_ok(const ConvArgs& a, int v, size_t es, bool backward) {
                    : aligned_to(a.y, v * es));
 }
 
+// Channels a lane: as many as alignment allows, fill a wave's lanes and leave waves enough for the card, since a
+// wave of four walks its tokens for longer than one of one (bf16: 32768 tokens x 256 14 -> 11 us, backward 42 ->
+// 21 us; 131072 x 64 19 -> 11 us, 48 -> 23 us; where there are many, 32768 x 2560, four 54 us, two 73 us).
+constexpr int64_t kManyWaves = 2048;
+int channels_a_lane(const ConvArgs& a, size_t es, bool backward) {
+  int v = vectors_ok(a, 4, es, backward) ? 4 : es == 2 && vectors_ok(a, 2, es, backward) ? 2 : 1;
+  while (v > 1 && (a.channels <= 32 * v || int64_t(a.p.rows) * ((a.channels + 64 * v - 1) / (64 * v)) < kManyWaves))
+    v = es == 4 ? 1 : v / 2;
+  return v;
+}
+
 template <typename Act, int V>
 void launch_conv(const ConvArgs& a, hipStream_t st) {
   const dim3 grid = block_grid(a.channels, 64 * V, a.p.rows);
@@ -454,12 +470,10 @@ axon_status axon_causal_conv(const axon_conv_shape* shape, const void* x, const 
   a.cache_in = cache_in, a.in_slots = in_slots, a.in_count = s.cache_slots;
   a.cache_out = cache_out, a.out_slots = out_slots, a.out_count = s.out_slots, a.y = y;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (!bf)
-    vectors_ok(a, 4, es, false) ? launch_conv<float, 4>(a, st) : launch_conv<float, 1>(a, st);
-  else if (vectors_ok(a, 4, es, false))
-    launch_conv<bf16_bits, 4>(a, st);
-  else
-    vectors_ok(a, 2, es, false) ? launch_conv<bf16_bits, 2>(a, st) : launch_conv<bf16_bits, 1>(a, st);
+  const int v = channels_a_lane(a, es, false);
+  if (v == 4) bf ? launch_conv<bf16_bits, 4>(a, st) : launch_conv<float, 4>(a, st);
+  else if (v == 2) launch_conv<bf16_bits, 2>(a, st);
+  else bf ? launch_conv<bf16_bits, 1>(a, st) : launch_conv<float, 1>(a, st);
   return hipGetLastError() == hipSuccess ? AXON_OK : AXON_ERR_HIP;
 }
 
@@ -511,12 +525,10 @@ axon_status axon_causal_conv_backward(const axon_conv_shape* shape, const void* 
   a.dcache_out = dcache_out, a.dx = dx, a.dw = dconv_w, a.db = dconv_b, a.dcache_in = dcache_in;
   a.partial = static_cast<float*>(workspace);
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (!bf)
-    vectors_ok(a, 4, es, true) ? launch_back<float, 4>(a, st) : launch_back<float, 1>(a, st);
-  else if (vectors_ok(a, 4, es, true))
-    launch_back<bf16_bits, 4>(a, st);
-  else
-    vectors_ok(a, 2, es, true) ? launch_back<bf16_bits, 2>(a, st) : launch_back<bf16_bits, 1>(a, st);
+  const int v = channels_a_lane(a, es, true);
+  if (v == 4) bf ? launch_back<bf16_bits, 4>(a, st) : launch_back<float, 4>(a, st);
+  else if (v == 2) launch_back<bf16_bits, 2>(a, st);
+  else bf ? launch_back<bf16_bits, 1>(a, st) : launch_back<float, 1>(a, st);
   hipLaunchKernelGGL(conv_sum_kernel, dim3((a.channels + 63) / 64, kSums), dim3(64 * kSumWaves), 0, st, a,
                      static_cast<int>(back_parts(a.p.rows)));
   return hipGetLastError() == hipSuccess ? AXON_OK : AXON_ERR_HIP;
