@@ -326,3 +326,52 @@ def test_stream_of_the_wrong_kind():
     z = make((1, 70), 24, seed=1)
     with pytest.raises(Exception):
         axon.linear_scan(**z, stream=7.5)
+
+
+# ---- Wide convolutions --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E", [65540, 65538, 65537])
+def test_conv_of_many_waves(E, dtype):
+    """Enough waves that a lane takes four, two or one channels, as the rows' alignment allows."""
+    import test_gpu_conv as conv
+
+    say(f"[calls] convolution {E} {dtype}")
+    axon = _axon()
+    lengths, spare = [5, 0, 64, 1, 70, 2, 3, 65], 7
+    total, N = sum(lengths) + spare, len(lengths)
+    z, dy = conv.make((total,), E, dtype, seed=1), conv.grad((total,), E, dtype)
+    z["x"][total - spare:] = float("nan")
+    dy[total - spare:] = float("nan")
+    tables = axon.sequence_tables(torch.tensor(lengths, dtype=torch.int32).cuda(), total)
+    c0, dc = conv.caches(N, E), conv.caches(N, E, 1)
+    y, c1 = axon.causal_conv(**z, activation="silu", cache_in=c0, tables=tables)
+    grads = axon.causal_conv_backward(dy, **z, activation="silu", cache_in=c0, dcache_out=dc, tables=tables)
+    torch.cuda.synchronize()
+    conv.compare(z, parts_of(lengths), c0, dc, dy, y, c1, grads, "silu")
+    assert not y[total - spare:].any() and not grads.dx[total - spare:].any()
+
+
+# ---- Wide steps ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("E,apart", [(16388, 0), (16388, 4), (16388, 2), (16385, 0)])
+def test_step_of_a_large_batch(E, apart, act):
+    """Rows enough that a thread takes four channels, where their alignment allows it."""
+    axon = _axon()
+    n, slots = 65, 70
+    z = make((n,), E + apart, act, seed=E)
+    z = {k: v[..., :E] if v.dim() == 2 else v[:E].contiguous() for k, v in z.items()}
+    pool = states(slots, E)
+    at = torch.randperm(slots, generator=torch.Generator().manual_seed(1))[:n].int()
+    at[7], at[20] = -1, slots
+    before, y = pool.clone(), torch.full((n, E), 7.0, dtype=T[act], device="cuda")
+    axon.linear_step(**z, state=pool, slots=at.cuda(), y=y)
+    torch.cuda.synchronize()
+    rows = [j for j in range(n) if 0 <= int(at[j]) < slots]
+    for j in rows[::8]:
+        r = sequence(z, before[int(at[j])], slice(j, j + 1), "sigmoid", "sqrt")
+        ref.within(y[j:j + 1], r.y, r.bound, f"y {j}")
+        ref.within(pool[int(at[j])], r.state, r.state_bound, f"state {j}")
+    idle = [j for j in range(slots) if j not in [int(at[i]) for i in rows]]
+    assert torch.equal(pool[idle], before[idle]) and bool((y[[7, 20]] == 7).all())
