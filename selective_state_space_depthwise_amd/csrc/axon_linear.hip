@@ -737,14 +737,14 @@ constexpr int kTokens = 16, kWaves = 12;
 constexpr int kBackTokens = 16, kBackWaves = 4;      // bf16
 constexpr int kBackTokens32 = 8, kBackWaves32 = 8;   // fp32
 
-// Rows x channels from which a step takes four channels a thread: 512 rows x 2560 bf16 16.4 -> 12.0 us from
-// memory, 256 rows 4.0 and 4.1 us in the caches, one row 2.1 and 2.9 us.
+// Rows x channels from which a step takes four channels a thread: 512 rows x 7680 bf16 16.4 -> 12.0 us from
+// memory; in the caches 256 rows x 2560 4.0 and 4.1 us, one row 2.1 and 2.9 us.
 constexpr int64_t kStepWide = 1 << 20;
 
 // Groups of channels up to which all waves of a tile look at the tiles in front, and tiles in a row from which
 // they do. Forward, bf16: 131072 tokens x 64 204 -> 61 us, 16384 x 512 46 -> 39 us, x 1024 52 -> 56 us, 21 tiles
 // in a row x 512 38 -> 39.5 us. Backward: 131072 x 64 572 -> 229 us, 16384 x 1024 108 -> 86 us, x 2560 158 ->
-// 167 us.
+// 167 us, 16 tiles in a row x 1024 54 -> 58 us.
 constexpr int kFewGroups = 8, kFewGroupsBack = 16, kLongChain = 32;
 
 // Tiles, and what of the workspace they use.
@@ -763,8 +763,9 @@ Plan plan_linear(const axon_linear_shape& s, bool packed, bool backward) {
   const int64_t blocks = (backward ? kBackTokens * kBackWaves : kTokens * kWaves) / kBlock;
   p.tiles = (rows + blocks - 1) / blocks;
   p.groups = (s.channels + 63) / 64;
-  p.together = p.groups <= (backward ? kFewGroupsBack : kFewGroups) &&
-               p.tiles / (packed ? 1 : s.sequences) >= kLongChain;
+  // few packed sequences may be long ones; where it would cost most they are taken as alike
+  const int64_t in_a_row = packed && p.groups <= kFewGroups ? p.tiles : p.tiles / s.sequences;
+  p.together = p.groups <= (backward ? kFewGroupsBack : kFewGroups) && in_a_row >= kLongChain;
   const size_t cells = size_t(p.tiles) * size_t(p.groups) * 64;
   if (p.tiles > 1) {
     p.sums = 0;
