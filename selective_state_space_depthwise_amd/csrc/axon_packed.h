@@ -16,7 +16,7 @@ constexpr int kBlock = 64;  // tokens of a block
 // A buffer of `tokens` rows: packed sequences with the tables of axon_sequence_tables (block 64), or,
 // where starts is null, a uniform batch of `seqlen` tokens each.
 struct Packed {
-  const int32_t *starts, *block_starts, *block_seq, *block_first;
+  const int32_t *starts, *block_seq, *block_first;
   int sequences, tokens, rows;   // rows: of the block tables, or of the batch's blocks
   int seqlen, blocks_per_seq;    // of a uniform batch
 };
@@ -35,7 +35,6 @@ inline Packed make_packed(int64_t sequences, int64_t tokens, const int32_t* tabl
   p.blocks_per_seq = (p.seqlen + kBlock - 1) / kBlock;
   if (tables) {
     p.starts = tables;
-    p.block_starts = tables + (sequences + 1);
     p.block_seq = tables + 2 * (sequences + 1);
     p.block_first = p.block_seq + p.rows;
   }
