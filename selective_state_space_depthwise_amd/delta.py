@@ -55,22 +55,24 @@ def _row_stride(t, name, tail):
     contiguous, else the one stride that all leading axes agree on."""
     if t.is_contiguous():
         return 0
+    shape, strides = t.shape, t.stride()
+    own = len(shape) - len(tail)
     want = 1
-    for axis in range(1, len(tail) + 1):
-        if t.shape[-axis] > 1 and t.stride(-axis) != want:
+    for axis in range(len(shape) - 1, own - 1, -1):
+        if shape[axis] > 1 and strides[axis] != want:
             raise ValueError(f"{name}: a row must lie contiguous in memory")
-        want *= t.shape[-axis]
+        want *= shape[axis]
     stride = 0
-    for axis in range(t.dim() - len(tail) - 1, -1, -1):
-        if t.shape[axis] == 1:
+    for axis in range(own - 1, -1, -1):
+        if shape[axis] == 1:
             continue
-        if t.stride(axis) < 1:
+        if strides[axis] < 1:
             raise ValueError(f"{name}: rows overlap (an expanded tensor)")
         if stride == 0:
-            stride = step = t.stride(axis)
-        elif t.stride(axis) != step:
+            stride = step = strides[axis]
+        elif strides[axis] != step:
             raise ValueError(f"{name}: the rows must be evenly spaced")
-        step *= t.shape[axis]
+        step *= shape[axis]
     if stride and stride < want:
         raise ValueError(f"{name}: rows overlap (stride {stride})")
     return stride
@@ -94,12 +96,13 @@ def _rows(t, name, lead, tail, dtype, device):
 class SequenceTables:
     """Tables of packed sequences (axon_sequence_tables): ``starts`` and ``block_starts``
     (sequences + 1), ``block_seq`` and ``block_first`` (total_tokens // block + sequences), int32
-    parts of the one tensor ``buffer``."""
+    parts of the one tensor ``buffer``. ``owner``: handle of the stream whose memory that is, None if
+    not known."""
 
-    __slots__ = ("buffer", "sequences", "total_tokens", "block", "_parts")
+    __slots__ = ("buffer", "sequences", "total_tokens", "block", "owner", "_parts")
 
-    def __init__(self, buffer, sequences, total_tokens, block):
-        self.buffer = buffer
+    def __init__(self, buffer, sequences, total_tokens, block, owner=None):
+        self.buffer, self.owner = buffer, owner
         self.sequences, self.total_tokens, self.block = sequences, total_tokens, block
         self._parts = None
 
@@ -137,7 +140,7 @@ def sequence_tables(lengths, total_tokens, *, block=DELTA_CHUNK, stream=None) ->
                                          buffer.data_ptr(), _handle(device, stream))
     if st != _abi.AXON_OK:
         raise AxonError(st, "axon_sequence_tables")
-    return SequenceTables(buffer, n, total_tokens, block)
+    return SequenceTables(buffer, n, total_tokens, block, _handle(device, None))
 
 
 def _delta_inputs(q, k, v, dt_raw, beta_raw, A_log, dt_bias, lead, device):

@@ -40,7 +40,8 @@ class _Launch:
         return self._context.__exit__(*what)
 
     def keep(self, made, tables=None):
-        if tables is not None:  # built on any stream
+        # tables may have been built from another stream's memory
+        if tables is not None and (tables.owner is None or tables.owner != _handle(self._device, None)):
             tables.buffer.record_stream(torch.cuda.current_stream(self._device))
         if self._caller is not None and self._caller != self._stream:
             for t in made:
@@ -94,24 +95,30 @@ def _optional(t, name, shape, dtype, device):
         _dense(t, name, shape, dtype, device)
 
 
-def _workspace(workspace, need, device, mine):
+def _new(like, shape, dtype):
+    """Memory beside `like`, dense (the quickest of torch's ways to it: these calls are short)."""
+    return like.new_empty(shape) if dtype == like.dtype else like.new_empty(shape, dtype=dtype)
+
+
+def _workspace(workspace, need, like, mine):
+    device = like.device
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _new(like, (need,), torch.uint8)
         mine.append(workspace)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _made(t, name, shape, dtype, device, mine):
-    """A given output, checked, or a new one."""
+def _made(t, name, like, mine):
+    """A given output like `like`, checked, or a new one."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty_like(like) if like.is_contiguous() else like.new_empty(like.shape)
         mine.append(t)
     else:
-        _dense(t, name, shape, dtype, device)
+        _dense(t, name, like.shape, like.dtype, like.device)
     return t
 
 
@@ -142,7 +149,7 @@ def linear_checkpoints(x, *, tables=None):
     lead = _lead(x, None, tables)
     n, _ = _sequences(lead, None, tables, device, None)
     rows = _lib().axon_linear_checkpoint_rows(n, math.prod(lead), 0 if tables is None else 1)
-    return torch.empty((rows, x.shape[-1]), dtype=torch.float32, device=device)
+    return _new(x, (rows, x.shape[-1]), torch.float32)
 
 
 def linear_scan(x, dt_raw, A_log, dt_bias=None, in_raw=None, in_bias=None, *, gate="sigmoid",
@@ -174,17 +181,17 @@ def linear_scan(x, dt_raw, A_log, dt_bias=None, in_raw=None, in_bias=None, *, ga
     with _Launch(device, stream) as on:
         mine = []
         shape.clear_behind = 1 if y is None else 0
-        y = _made(y, "y", x.shape, x.dtype, device, mine)
+        y = _made(y, "y", x, mine)
         if state_out is None:
             if out_slots is not None:
                 raise ValueError("out_slots address a pool: give state_out")
-            state_out = torch.empty((n, E), dtype=torch.float32, device=device)
+            state_out = _new(x, (n, E), torch.float32)
             mine.append(state_out)
         shape.out_slots = _pool(state_out, "state_out", (E,), device)
         if checkpoints is not None:
             rows = _lib().axon_linear_checkpoint_rows(n, shape.tokens, 0 if tables is None else 1)
             _dense(checkpoints, "checkpoints", (rows, E), torch.float32, device)
-        ws, size = _workspace(workspace, _lib().axon_linear_scan_workspace_bytes(shape), device, mine)
+        ws, size = _workspace(workspace, _lib().axon_linear_scan_workspace_bytes(shape), x, mine)
         on.keep(mine, tables)
         st = _lib().axon_linear_scan(
             shape, params, x.data_ptr(), dt_raw.data_ptr(), _ptr(in_raw),
@@ -229,19 +236,17 @@ def linear_scan_backward(dy, x, dt_raw, A_log, dt_bias=None, in_raw=None, in_bia
     _dense(checkpoints, "checkpoints", (rows, E), torch.float32, device)
     with _Launch(device, stream) as on:
         mine = []
-        acts = [None if t is None else _made(None, "", x.shape, x.dtype, device, mine)
-                for t in (x, dt_raw, in_raw)]
-        sums = torch.empty((2 if in_raw is None else 3, E), dtype=torch.float32, device=device)
-        dstate_in = torch.empty((n, E), dtype=torch.float32, device=device)
+        acts = [None if t is None else _made(None, "", x, mine) for t in (x, dt_raw, in_raw)]
+        sums = _new(x, (2 if in_raw is None else 3, E), torch.float32)
+        dstate_in = _new(x, (n, E), torch.float32)
         mine += [sums, dstate_in]
-        ws, size = _workspace(workspace, _lib().axon_linear_scan_backward_workspace_bytes(shape),
-                              device, mine)
+        ws, size = _workspace(workspace, _lib().axon_linear_scan_backward_workspace_bytes(shape), x, mine)
         on.keep(mine, tables)
-        parts = list(sums) + [None] * (in_raw is None)
+        parts = [*sums.unbind(0), None]
         st = _lib().axon_linear_scan_backward(
             shape, params, dy.data_ptr(), x.data_ptr(), dt_raw.data_ptr(), _ptr(in_raw),
             None if tables is None else tables.buffer.data_ptr(), checkpoints.data_ptr(),
-            _ptr(dstate_out), *map(_ptr, acts), *map(_ptr, parts), dstate_in.data_ptr(), ws, size,
+            _ptr(dstate_out), *map(_ptr, acts), *map(_ptr, parts[:3]), dstate_in.data_ptr(), ws, size,
             _handle(device, stream))
     if st != _abi.AXON_OK:
         raise AxonError(st, "axon_linear_scan_backward")
@@ -276,8 +281,7 @@ def _step_output(y, x, slots, on):
         _dense(y, "y", x.shape, x.dtype, x.device)
         return y
     # rows may be idle where there are slots
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if slots is None else torch.zeros(
-        x.shape, dtype=x.dtype, device=x.device)
+    y = _new(x, x.shape, x.dtype) if slots is None else x.new_zeros(x.shape)
     on.keep([y])
     return y
 
@@ -316,11 +320,11 @@ def causal_conv(x, conv_w, conv_b=None, *, activation="none", lengths=None, tabl
     with _Launch(device, stream) as on:
         mine = []
         shape.clear_behind = 1 if y is None else 0
-        y = _made(y, "y", x.shape, x.dtype, device, mine)
+        y = _made(y, "y", x, mine)
         if cache_out is None:
             if out_slots is not None:
                 raise ValueError("out_slots address a pool: give cache_out")
-            cache_out = torch.empty((n, *tail), dtype=torch.float32, device=device)
+            cache_out = _new(x, (n, *tail), torch.float32)
             mine.append(cache_out)
         shape.out_slots = _pool(cache_out, "cache_out", tail, device)
         on.keep(mine, tables)
@@ -361,12 +365,10 @@ def causal_conv_backward(dy, x, conv_w, conv_b=None, *, activation="none", lengt
     _optional(dcache_out, "dcache_out", (n, *tail), torch.float32, device)
     with _Launch(device, stream) as on:
         mine = []
-        dx = _made(None, "", x.shape, x.dtype, device, mine)
-        dw = _made(None, "", (E, D_CONV), torch.float32, device, mine)
-        db = _made(None, "", (E,), torch.float32, device, mine)
-        dcache = _made(None, "", (n, *tail), torch.float32, device, mine)
-        ws, size = _workspace(workspace, _lib().axon_causal_conv_backward_workspace_bytes(shape),
-                              device, mine)
+        dx = _made(None, "", x, mine)
+        dw, db, dcache = (_new(x, t, torch.float32) for t in ((E, D_CONV), (E,), (n, *tail)))
+        mine += [dw, db, dcache]
+        ws, size = _workspace(workspace, _lib().axon_causal_conv_backward_workspace_bytes(shape), x, mine)
         on.keep(mine, tables)
         st = _lib().axon_causal_conv_backward(
             shape, dy.data_ptr(), x.data_ptr(), conv_w.data_ptr(), _ptr(conv_b),

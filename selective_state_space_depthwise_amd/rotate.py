@@ -63,9 +63,9 @@ def norm_rotate(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-
         raise ValueError("k_out belongs to k")
     with _Launch(device, stream) as on:
         mine = []
-        q_out = _made(q_out, "q_out", q.shape, q.dtype, device, mine)
+        q_out = _made(q_out, "q_out", q, mine)
         if k is not None:
-            k_out = _made(k_out, "k_out", k.shape, k.dtype, device, mine)
+            k_out = _made(k_out, "k_out", k, mine)
         on.keep(mine)
         st = _lib().axon_norm_rotate(desc, q.data_ptr(), _ptr(k), positions.data_ptr(),
                                      freqs.data_ptr(), _ptr(q_weight), _ptr(k_weight),
@@ -95,15 +95,12 @@ def norm_rotate_backward(dq_out, dk_out, q, k, positions, freqs, *, q_weight=Non
         raise ValueError("dk_out belongs to k")
     if k is not None:
         desc.dk_stride = _rows(dk_out, "dk_out", lead, tuple(k.shape[-2:]), q.dtype, device)
-    D = q.shape[-1]
     with _Launch(device, stream) as on:
         mine = []
-        dq = _made(None, "", q.shape, q.dtype, device, mine)
-        dk = None if k is None else _made(None, "", k.shape, q.dtype, device, mine)
-        dw = [None if w is None else _made(None, "", (D,), torch.float32, device, mine)
-              for w in (q_weight, k_weight)]
-        ws, size = _workspace(workspace, _lib().axon_norm_rotate_backward_workspace_bytes(desc),
-                              device, mine)
+        dq = _made(None, "", q, mine)
+        dk = None if k is None else _made(None, "", k, mine)
+        dw = [None if w is None else _made(None, "", w, mine) for w in (q_weight, k_weight)]
+        ws, size = _workspace(workspace, _lib().axon_norm_rotate_backward_workspace_bytes(desc), q, mine)
         on.keep(mine)
         st = _lib().axon_norm_rotate_backward(
             desc, dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k), positions.data_ptr(),
