@@ -71,7 +71,7 @@ struct Gate {
   float on, off;
   __device__ __forceinline__ Gate(float raw, float bias) {
     const float x = __builtin_amdgcn_exp2f(fmaf(raw, -kLog2e, scaled_bias(bias)));
-    const float e = x > 8.5e37f ? 8.5e37f : x;
+    const float e = __builtin_elementwise_minimum(x, 8.5e37f);  // keeps NaN
     on = __builtin_amdgcn_rcpf(1.0f + e);
     off = e * on;
   }
@@ -588,15 +588,15 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
         sA += G;
         sdt += odt;
         sin += oin;
-        if (in_range) {
-          store_row<kPast>(kType, ddt, off, j * step, odt);
-          store_row<kPast>(kType, dx, off, j * step, gt * mo[j]);
-          if (g.in_raw) store_row<kPast>(kType, din, off, j * step, oin);
-        }
+        store_row<kPast>(kType, ddt, off, j * step, odt);
+        store_row<kPast>(kType, dx, off, j * step, gt * mo[j]);
+        if (g.in_raw) store_row<kPast>(kType, din, off, j * step, oin);
       }
     };
-    if (g.past) grads(Past{});
-    else grads(Kept{});
+    if (in_range) {
+      if (g.past) grads(Past{});
+      else grads(Kept{});
+    }
     if (s.begins && g.dstate_in && in_range) g.dstate_in[int64_t(s.seq) * g.channels + e] = k;
   }
   totals[wave][0][lane] = sA;
