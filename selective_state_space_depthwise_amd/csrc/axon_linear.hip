@@ -16,11 +16,11 @@
 //
 // Bound by memory and, as much, by the gates: about 60 vector instructions a token forward and 90 backward, of which
 // 6 take four times as long, or 58 and 107 us of all SIMDs for 16384 x 2560; a wave does not load while it computes.
-// bf16: 16384 x 2560 (336 MB) 97-100 us; packed 32768 x 2560 185 us; training of 8 x 2048 x 2560 (336 + 587 MB)
-// 265 us. From the first kernel, one channel of a sequence a lane, of 16384 tokens 21.7 ms. What it took: tiles that
+// bf16: 16384 x 2560 (336 MB) 97-100 us; packed 32768 x 2560 183 us; training of 8 x 2048 x 2560 (336 + 587 MB)
+// 262 us. From the first kernel, one channel of a sequence a lane, of 16384 tokens 21.7 ms. What it took: tiles that
 // hand on; 12 waves of 16 tokens; gate and input scale as template arguments; plain decays inside a wave; loads of
 // rows at a scalar offset; stores past the caches. Tried and dropped: two channels a lane, persistent workgroups
-// that ask for the next tile's rows early (registers 122-193 us, LDS 133 us), eight tokens a wave (143 us).
+// (117 us; that ask for the next tile's rows early 122-193 us), eight tokens a wave (143 us).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
