@@ -375,3 +375,81 @@ def test_step_of_a_large_batch(E, apart, act):
         ref.within(pool[int(at[j])], r.state, r.state_bound, f"state {j}")
     idle = [j for j in range(slots) if j not in [int(at[i]) for i in rows]]
     assert torch.equal(pool[idle], before[idle]) and bool((y[[7, 20]] == 7).all())
+
+
+# ---- The most sequences, other ways to a stream, gradients recorded --------------------------------
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_the_most_sequences(packed):
+    """65535 sequences of one token: a scan is a step."""
+    axon = _axon()
+    N, E = 65535, 6
+    z = make((N,), E, seed=1)
+    s0 = states(N, E)
+    lead = z if packed else {k: v[:, None] if v.dim() == 2 else v for k, v in z.items()}
+    x = lead["x"]
+    n = torch.ones(N, dtype=torch.int32, device="cuda") if packed else None
+    tables = axon.sequence_tables(n, N) if packed else None
+    p = axon.linear_checkpoints(x, tables=tables)
+    y, s1 = axon.linear_scan(**lead, tables=tables, state_in=s0, checkpoints=p)
+    d = axon.linear_scan_backward(x, **lead, tables=tables, checkpoints=p)
+    c, c1 = axon.causal_conv(x, torch.ones(E, 4, device="cuda"), tables=tables)
+    pool = s0.clone()
+    y2 = axon.linear_step(**z, state=pool)
+    torch.cuda.synchronize()
+    assert torch.equal(y.reshape(N, E), s1) and torch.equal(c.reshape(N, E), z["x"])
+    assert torch.equal(c1[:, 2], z["x"]) and not c1[:, :2].any()
+    # one token by the step's and by the scan's form: the bounds of both
+    for j in (0, 1, 191, 192, 32768, 65533, 65534):
+        r = sequence(z, s0[j], slice(j, j + 1), "sigmoid", "sqrt")
+        ref.within(y.reshape(N, E)[j:j + 1], r.y, r.bound, f"scan {j}")
+        ref.within(y2[j:j + 1], r.y, r.bound, f"step {j}")
+        want = r.backward(z["x"][j:j + 1], torch.zeros(E))
+        ref.within(d.dx.reshape(N, E)[j:j + 1], *want["dx"], f"dx {j}")
+    assert torch.equal(pool, y2)
+
+
+def test_tables_of_another_stream():
+    """Tables of one stream in calls on another, and in a captured graph, dropped while they run."""
+    axon = _axon()
+    z = make((900,), 64, "bf16", seed=1)
+    n = torch.tensor([400, 500], dtype=torch.int32).cuda()
+    want = axon.linear_scan(**z, lengths=n)
+    tables = axon.sequence_tables(n, 900)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = axon.linear_scan(**z, tables=tables)
+    for _ in range(3):
+        captured[0].fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(captured[0], want[0]) and torch.equal(captured[1], want[1])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        got = axon.linear_scan(**z, tables=tables)
+    count = tables.buffer.numel()
+    del graph, tables
+    junk = [torch.full((count,), 7, dtype=torch.int32, device="cuda") for _ in range(64)]
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    del junk
+
+
+def test_tensors_that_want_gradients():
+    """The calls record no graph, whatever their inputs want, and give the same in inference mode."""
+    axon = _axon()
+    z = make((1, 300), 40, seed=1)
+    want = axon.linear_scan(**z)
+    grads = {k: v.clone().requires_grad_() for k, v in z.items()}
+    got = axon.linear_scan(**grads)
+    p = axon.linear_checkpoints(grads["x"])
+    axon.linear_scan(**grads, checkpoints=p)
+    back = axon.linear_scan_backward(got[0], **grads, checkpoints=p)
+    with torch.inference_mode():
+        other = axon.linear_scan(**z)
+    torch.cuda.synchronize()
+    for t in (*got, *back):
+        assert not t.requires_grad and t.grad_fn is None
+    for o in (got, other):
+        assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
