@@ -25,6 +25,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "axon_device.h"
 #include "axon_packed.h"
@@ -143,6 +144,20 @@ __device__ __forceinline__ Share share_of(const Packed& p, int tile, int wave) {
   return s;
 }
 
+// A channel's parameters, asked for before the rows so that nothing waits for them alone.
+template <bool GATED>
+struct Channel {
+  float A_log, dt_bias, in_bias = 0.0f;
+  __device__ __forceinline__ Channel(const LinearArgs& g, int e) {
+    A_log = g.A_log[e];
+    dt_bias = (g.dt_bias ? g.dt_bias : g.A_log)[e];
+    if constexpr (GATED) in_bias = (g.in_bias ? g.in_bias : g.A_log)[e];
+    if (!g.dt_bias) dt_bias = 0.0f;
+    if (!g.in_bias) in_bias = 0.0f;
+  }
+  __device__ __forceinline__ float rate() const { return -expf(A_log) * kLog2e; }
+};
+
 // P rows of a wave as loaded; rows behind the last repeat it.
 template <typename Act, int P>
 struct Rows {
@@ -169,8 +184,8 @@ template <bool PAST>
 __device__ __forceinline__ void store_row(const bf16_bits*, rsrc_t r, uint32_t off, uint32_t row, float v) {
   __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v), r, off, row, PAST ? 2 : 0);
 }
-struct Past { static constexpr bool value = true; };
-struct Kept { static constexpr bool value = false; };
+using Past = std::true_type;
+using Kept = std::false_type;
 
 // ---- What tiles tell each other -----------------------------------------------------------------
 // A tile first publishes its own part (its decay, as for advance, and h from zero), then, once it knows what
@@ -366,7 +381,7 @@ __device__ __forceinline__ uint32_t take_ticket(const LinearArgs& g, uint32_t* s
 
 // ---- The scan -----------------------------------------------------------------------------------
 // Waves to a workgroup and registers are chosen for 24 waves a CU.
-template <typename Act, int P, int WAVES, int GATE, int SCALE>
+template <typename Act, int P, int WAVES, int GATE, int SCALE, bool GATED>
 __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g) {
   __shared__ uint32_t ticket;
   __shared__ Parts<WAVES> sh;
@@ -377,6 +392,7 @@ __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const bool in_range = grp * 64 + lane < g.channels;
   const int e = min(grp * 64 + lane, g.channels - 1);
+  const Channel<GATED> channel(g, e);
   const Share s = share_of<P, WAVES>(g.p, tile, wave);
   float a[P], b[P];
   float h0 = 0.0f;  // what enters the wave, where it begins a sequence
@@ -385,14 +401,12 @@ __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g
     Rows<Act, P> x, raw, in;
     raw.load(g.dt_raw, g.dt_stride, s, e);
     x.load(g.x, g.x_stride, s, e);
-    if (g.in_raw) in.load(g.in_raw, g.in_stride, s, e);
+    if constexpr (GATED) in.load(g.in_raw, g.in_stride, s, e);
     if (s.begins && g.state_in) {
       const int64_t slot = g.in_slots ? table_at(g.in_slots, s.seq) : s.seq;
       if (slot >= 0 && slot < g.in_count) h0 = g.state_in[slot * g.channels + e];
     }
-    const float rate = -expf(g.A_log[e]) * kLog2e;
-    const float bias = g.dt_bias ? g.dt_bias[e] : 0.0f;
-    const float ib = scaled_bias(g.in_raw && g.in_bias ? g.in_bias[e] : 0.0f);
+    const float rate = channel.rate(), bias = channel.dt_bias, ib = scaled_bias(channel.in_bias);
     // a: log2 a first
 #pragma unroll
     for (int j = 0; j < P; ++j) a[j] = log2_decay<GATE>(rate, raw[j], bias);
@@ -408,7 +422,7 @@ __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g
       a[j] = __builtin_amdgcn_exp2f(l2);
       b[j] = x[j] * input_factor<SCALE>(l2, a[j]);
     }
-    if (g.in_raw) {
+    if constexpr (GATED) {
 #pragma unroll
       for (int j = 0; j < P; ++j) b[j] *= sigmoid_f32(in[j], ib);
     }
@@ -466,7 +480,7 @@ __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g
 // ---- Its backward pass --------------------------------------------------------------------------
 // The same from the last tile to the first. A wave finds its block's states again from the block's
 // checkpoint and the parts of the waves in front of it.
-template <typename Act, int P, int WAVES, int GATE, int SCALE>
+template <typename Act, int P, int WAVES, int GATE, int SCALE, bool GATED>
 __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_back_kernel(LinearArgs g) {
   static_assert(WAVES * P % kBlock == 0, "a tile holds whole blocks");
   constexpr int kBlockWaves = kBlock / P;
@@ -481,6 +495,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const bool in_range = grp * 64 + lane < g.channels;
   const int e = min(grp * 64 + lane, g.channels - 1);
+  const Channel<GATED> channel(g, e);
   const Share s = share_of<P, WAVES>(g.p, tile, wave);
   // Per token: a, what the gate's slope makes of G, m times the input's gate, m u (1 - gate), dy. G is
   // g (aL h - w): first aL, w and the inputs m u, then, once the states are known, aL h - w in their place.
@@ -490,15 +505,13 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
     Rows<Act, P> x, raw, in, d;
     raw.load(g.dt_raw, g.dt_stride, s, e);
     x.load(g.x, g.x_stride, s, e);
-    if (g.in_raw) in.load(g.in_raw, g.in_stride, s, e);
+    if constexpr (GATED) in.load(g.in_raw, g.in_stride, s, e);
     d.load(g.dy, g.dy_stride, s, e);
     if (s.opens) point = g.points[int64_t(s.row) * g.channels + e];
     if (s.ends && g.dstate_out) k0 = g.dstate_out[int64_t(s.seq) * g.channels + e];
-    const float rate = -expf(g.A_log[e]) * kLog2e;
-    const float bias = g.dt_bias ? g.dt_bias[e] : 0.0f;
-    const float ib = g.in_raw && g.in_bias ? g.in_bias[e] : 0.0f;
+    const float rate = channel.rate(), bias = channel.dt_bias, ib = channel.in_bias;
     // mo: the input's gate, mz: u (1 - gate), hb: u at first
-    if (g.in_raw) {
+    if constexpr (GATED) {
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         const Gate q(in[j], ib);
@@ -574,7 +587,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
     const int64_t first = int64_t(s.first) * g.channels;
     const rsrc_t dx = make_rsrc(static_cast<Act*>(g.dx) + first);
     const rsrc_t ddt = make_rsrc(static_cast<Act*>(g.ddt_raw) + first);
-    const rsrc_t din = make_rsrc(static_cast<Act*>(g.din_raw) + (g.in_raw ? first : 0));
+    const rsrc_t din = make_rsrc(static_cast<Act*>(g.din_raw) + (GATED ? first : 0));
     const uint32_t step = static_cast<uint32_t>(g.channels) * sizeof(Act), off = e * sizeof(Act);
     auto grads = [&](auto past) {
       constexpr Act* kType = nullptr;
@@ -590,7 +603,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
         sin += oin;
         store_row<kPast>(kType, ddt, off, j * step, odt);
         store_row<kPast>(kType, dx, off, j * step, gt * mo[j]);
-        if (g.in_raw) store_row<kPast>(kType, din, off, j * step, oin);
+        if constexpr (GATED) store_row<kPast>(kType, din, off, j * step, oin);
       }
     };
     if (in_range) {
@@ -621,7 +634,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
     const int64_t at = r * g.channels + e;
     store_act(static_cast<Act*>(g.dx), at, 0.0f);
     store_act(static_cast<Act*>(g.ddt_raw), at, 0.0f);
-    if (g.in_raw) store_act(static_cast<Act*>(g.din_raw), at, 0.0f);
+    if constexpr (GATED) store_act(static_cast<Act*>(g.din_raw), at, 0.0f);
   }
 }
 
@@ -820,24 +833,26 @@ dim3 tile_grid(const Plan& p) {
   return dim3(static_cast<unsigned>(x), static_cast<unsigned>((n + x - 1) / x));
 }
 
-template <bool BACK, typename Act, int GATE>
-void launch_scale(const LinearArgs& a, dim3 grid, hipStream_t st) {
+template <bool BACK, typename Act, int GATE, int SCALE>
+void launch_gated(const LinearArgs& a, dim3 grid, hipStream_t st) {
   constexpr bool kWide = sizeof(Act) == 4;
   constexpr int P = !BACK ? kTokens : kWide ? kBackTokens32 : kBackTokens;
   constexpr int W = !BACK ? kWaves : kWide ? kBackWaves32 : kBackWaves;
-#define AXON_LAUNCH(SCALE)                                                                              \
-  if constexpr (BACK)                                                                                   \
-    hipLaunchKernelGGL((linear_tile_back_kernel<Act, P, W, GATE, SCALE>), grid, dim3(64 * W), 0, st, a); \
-  else                                                                                                  \
-    hipLaunchKernelGGL((linear_tile_kernel<Act, P, W, GATE, SCALE>), grid, dim3(64 * W), 0, st, a)
-  if (a.input_scale == AXON_INPUT_SQRT) {
-    AXON_LAUNCH(AXON_INPUT_SQRT);
-  } else if (a.input_scale == AXON_INPUT_COMPLEMENT) {
-    AXON_LAUNCH(AXON_INPUT_COMPLEMENT);
-  } else {
-    AXON_LAUNCH(AXON_INPUT_PLAIN);
-  }
-#undef AXON_LAUNCH
+  auto launch = [&](auto gated) {
+    constexpr bool kGated = decltype(gated)::value;
+    if constexpr (BACK)
+      hipLaunchKernelGGL((linear_tile_back_kernel<Act, P, W, GATE, SCALE, kGated>), grid, dim3(64 * W), 0, st, a);
+    else
+      hipLaunchKernelGGL((linear_tile_kernel<Act, P, W, GATE, SCALE, kGated>), grid, dim3(64 * W), 0, st, a);
+  };
+  a.in_raw ? launch(std::true_type()) : launch(std::false_type());
+}
+
+template <bool BACK, typename Act, int GATE>
+void launch_scale(const LinearArgs& a, dim3 grid, hipStream_t st) {
+  if (a.input_scale == AXON_INPUT_SQRT) launch_gated<BACK, Act, GATE, AXON_INPUT_SQRT>(a, grid, st);
+  else if (a.input_scale == AXON_INPUT_COMPLEMENT) launch_gated<BACK, Act, GATE, AXON_INPUT_COMPLEMENT>(a, grid, st);
+  else launch_gated<BACK, Act, GATE, AXON_INPUT_PLAIN>(a, grid, st);
 }
 
 template <bool BACK>
