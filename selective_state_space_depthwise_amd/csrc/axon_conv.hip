@@ -78,7 +78,8 @@ struct Taps {
     for (int i = 0; i < V; ++i) {
 #pragma unroll
       for (int k = 0; k < kConv; ++k) w[k][i] = g.w[int64_t(e + i) * kConv + k];
-      b[i] = g.b ? g.b[e + i] : 0.0f;
+      b[i] = (g.b ? g.b : g.w)[e + i];
+      if (!g.b) b[i] = 0.0f;
     }
   }
   __device__ __forceinline__ float at(int i, float x0, float x1, float x2, float x3) const {
