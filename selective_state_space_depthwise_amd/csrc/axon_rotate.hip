@@ -207,30 +207,30 @@ __global__ __launch_bounds__(64 * kWaves, BACK ? kBackFit<Act> : 1) void rotate_
     const uint32_t row = ROWS ? min(which * together + ahead, rows - 1) : which;
     P c[UNITS];  // cosines and sines of the row
     for (int first = split; first < groups; first += g.splits * G) {
-      // The values of G groups are asked for before the first is used (and before the row's angles).
+      // The values of G groups are asked for before the first is used (and before the row's angles); places
+      // that hold none read others' again, since loads behind branches wait for each other.
+      const int position = g.positions[row];
       Raw<Act, V> rx[G][UNITS][2], rd[BACK ? G : 1][UNITS][2];
 #pragma unroll
       for (int k = 0; k < G; ++k) {
-        const int grp = first + k * g.splits;
+        const int grp = min(first + k * g.splits, groups - 1);
         const Tensor<Act> t(g, grp < q_groups);
-        const int head = (grp < q_groups ? grp : grp - q_groups) * per;
-        const Act* x = t.x + row * t.x_stride + int64_t(head) * g.dim;
-        const Act* dy = t.dy + row * t.dy_stride + int64_t(head) * g.dim;
+        const int head = min((grp < q_groups ? grp : grp - q_groups) * per + sub, t.heads - 1);
+        const Act* x = t.x + row * t.x_stride;
+        const Act* dy = t.dy + row * t.dy_stride;
 #pragma unroll
         for (int n = 0; n < UNITS; ++n) {
           const Unit<V> u(g, l + n * g.lanes);
-          if (held && grp < groups && head + sub < t.heads && u.live) {
-            rx[k][n][0].load(x + (sub * g.dim + u.lo));
-            rx[k][n][1].load(x + (sub * g.dim + u.hi));
-            if constexpr (BACK) {
-              rd[k][n][0].load(dy + (sub * g.dim + u.lo));
-              rd[k][n][1].load(dy + (sub * g.dim + u.hi));
-            }
+          const int lo = head * g.dim + (u.live ? u.lo : 0), hi = head * g.dim + (u.live ? u.hi : 0);
+          rx[k][n][0].load(x + lo);
+          rx[k][n][1].load(x + hi);
+          if constexpr (BACK) {
+            rd[k][n][0].load(dy + lo);
+            rd[k][n][1].load(dy + hi);
           }
         }
       }
       if (first == split) {
-        const int position = g.positions[row];
 #pragma unroll
         for (int n = 0; n < UNITS; ++n) {
           const bool turned = Unit<V>(g, l + n * g.lanes).turned;
