@@ -4,13 +4,13 @@
 // rows on their way. Only a sequence's first block reads its cache, and the same thread then writes the final
 // cache from the sequence's last inputs, so that a cache may be updated in place without a wait between threads.
 //
-// Bound by memory: packed 32768 x 7680 bf16 (1007 MB) in 210-214 us, 4.7-4.8 TB/s; a copy of as much takes
+// Bound by memory: packed 32768 x 7680 bf16 (1007 MB) in 207-210 us, 4.8-4.9 TB/s; a copy of as much takes
 // 187-207 us. What it took: four channels a lane (one: 380 us), eight rows ahead, stores past the caches
 // (219 -> 212 us); loads past the caches cost 224 us.
 //
 // Backward, with s_t = dy_t act'(p_t):  dxx_t = sum_k w[k] s_{t+3-k} + what dcache_out has for t,
 // dw[k] = sum_t s_t xx_{t-3+k},  db = sum_t s_t.  A block finds s of the three tokens behind it again, and four
-// blocks join their sums before they leave a part (with the forward pass 8 x 2048 x 7680 266 us).
+// blocks join their sums before they leave a part (with the forward pass 8 x 2048 x 7680 262 us).
 #include <hip/hip_runtime.h>
 
 #include <cmath>

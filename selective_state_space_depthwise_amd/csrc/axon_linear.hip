@@ -14,13 +14,13 @@
 // waves are joined in LDS, and tiles hand on what leaves them in the order in which workgroups start (below). Only
 // then are the states found and stored, so that every value is read and written once.
 //
-// Bound by memory and, as much, by the gates: about 60 vector instructions a token forward and 90 backward, of which
-// 6 take four times as long, or 58 and 107 us of all SIMDs for 16384 x 2560; a wave does not load while it computes.
-// bf16: 16384 x 2560 (336 MB) 97-100 us; packed 32768 x 2560 183 us; training of 8 x 2048 x 2560 (336 + 587 MB)
-// 262 us. From the first kernel, one channel of a sequence a lane, of 16384 tokens 21.7 ms. What it took: tiles that
-// hand on; 12 waves of 16 tokens; gate and input scale as template arguments; plain decays inside a wave; loads of
-// rows at a scalar offset; stores past the caches. Tried and dropped: two channels a lane, persistent workgroups
-// (117 us; that ask for the next tile's rows early 122-193 us), eight tokens a wave (143 us).
+// Bound by memory, in this pattern: rows of 128 bytes, three streams in and one out, then four in and three out,
+// reach 4.8 TB/s by themselves, and a wave does not load while it computes. bf16: 16384 x 2560 (336 MB) 82-92 us;
+// packed 32768 x 2560 155-164 us; training of 8 x 2048 x 2560 (336 + 587 MB) 240 us. From the first kernel, one channel
+// of a sequence a lane, of 16384 tokens 21.7 ms. What it took: tiles that hand on; 12 waves of 16 tokens; gates,
+// input scale and what is gated as template arguments, since loads behind branches are waited for at once (101 ->
+// 90 us); plain decays inside a wave; rows at a scalar offset; stores past the caches. Tried and dropped: two channels
+// a lane, persistent workgroups (117 us; that ask for the next tile's rows early 122-193 us), eight tokens a wave.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -756,9 +756,9 @@ size_t tables_bytes(const Packed& p) {
 }
 
 // Tokens a wave and waves a tile. Forward: 12 waves of 16 tokens, two workgroups a CU (16384 tokens x
-// 2560 bf16 102 us; 8 waves 107 us, 4 waves 148 us, 8 waves of 8 tokens 143 us). Backward bf16: 4 waves of
-// 16 tokens, three workgroups a CU (8 x 2048 tokens x 2560, with the forward pass, 275 us; 8 waves of 8
-// tokens 304 us); fp32: 8 waves of 8 (3 x 1999 tokens x 1001 79 us against 86 us).
+// 2560 bf16 92 us; 8 waves 94 us, 4 waves 147 us). Backward bf16: 4 waves of
+// 16 tokens, three workgroups a CU (8 x 2048 tokens x 2560, with the forward pass, 241 us; 8 waves of 8
+// tokens 264 us); fp32: 8 waves of 8 (3 x 1999 tokens x 1001 79 us against 86 us).
 constexpr int kTokens = 16, kWaves = 12;
 constexpr int kBackTokens = 16, kBackWaves = 4;      // bf16
 constexpr int kBackTokens32 = 8, kBackWaves32 = 8;   // fp32

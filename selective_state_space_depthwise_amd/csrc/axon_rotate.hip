@@ -9,10 +9,10 @@
 // the other, so that its angles are found once a row; where heads are few, the heads of several rows (ROWS).
 // Angles: p freqs / (2 pi) turns in 64 bits, of which only the fraction goes to 32 bits.
 //
-// Bound by memory: 16384 rows of 40 heads of 128 bf16 (336 MB) in 69-73 us, 4.6-4.9 TB/s where a copy of that
+// Bound by memory: 16384 rows of 40 heads of 128 bf16 (336 MB) in 65-68 us, 5.0 TB/s where a copy of that
 // type reaches 5.4. What it took from 81 us: groups of one tensor (pointers and weights the same in all
 // lanes), sums whose exchanges are part of the addition, the values of five groups asked for before the
-// first is used, stores past the caches.
+// first is used and without branches, stores past the caches.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -365,8 +365,8 @@ __global__ __launch_bounds__(64 * kSumWaves) void rotate_sum_kernel(const float*
 }
 
 // Workgroups that run at once and take item after item, so that weights and frequencies are read seldom. Forward
-// five a CU, with their registers, else four (16384 rows of 40 heads of 128 bf16 73 us; eight 83 us, four 80 us;
-// fp32, 32768 rows of 16 heads of 64: four 45 us, five 49 us).
+// five a CU, of fp32 or of several rows four (16384 rows of 40 heads of 128 bf16 67 us, six 69 us; fp32, 32768 rows
+// of 16 heads of 64: four 45 us, five 49 us).
 int64_t forward_workgroups(bool bf16, bool rows) { return kCus * (bf16 && !rows ? 5 : 4); }
 int back_workgroups(int64_t rows, bool bf16) {
   const int64_t most = kCus * (bf16 ? kBackFit<bf16_bits> : kBackFit<float>);
