@@ -768,9 +768,8 @@ constexpr int kBackTokens32 = 8, kBackWaves32 = 8;   // fp32
 constexpr int64_t kStepWide = 1 << 20;
 
 // Groups of channels up to which all waves of a tile look at the tiles in front, and tiles in a row from which
-// they do. Forward, bf16: 131072 tokens x 64 204 -> 61 us, 16384 x 512 46 -> 39 us, x 1024 52 -> 56 us, 21 tiles
-// in a row x 512 38 -> 39.5 us. Backward: 131072 x 64 572 -> 229 us, 16384 x 1024 108 -> 86 us, x 2560 158 ->
-// 167 us, 16 tiles in a row x 1024 54 -> 58 us.
+// they do. Forward, bf16: 131072 tokens x 64 200 -> 60 us, 16384 x 512 44 -> 37 us, x 1024 48 -> 50 us. Backward:
+// 131072 x 64 581 -> 229 us, 16384 x 1024 109 -> 81 us, x 2560 151 -> 166 us, 16 tiles in a row x 1024 54 -> 58 us.
 constexpr int kFewGroups = 8, kFewGroupsBack = 16, kLongChain = 32;
 
 // Tiles, and what of the workspace they use.
