@@ -478,8 +478,8 @@ axon_status axon_group_norm(const axon_group_norm_desc* desc, const void* x, con
  * and dy may lie x_stride, dt_stride, in_stride, dy_stride elements apart (0 = dense, else at least
  * `channels`); y and the gradients are dense. A_log, dt_bias, in_bias (channels) fp32; the biases
  * may be NULL (zeros). Pools of states (slots, channels) fp32. Sequences (a uniform batch, or packed
- * with tables of block 64) and slots as for axon_gated_delta_scan. Activations need the alignment of an element only, fp32
- * and integer arrays 4-byte.
+ * with tables of block 64) and slots as for axon_gated_delta_scan. Activations need the alignment of an
+ * element only, fp32 and integer arrays 4-byte.
  * Limits: sequences in [1, 65535]; channels in [1, 2^22]; tokens < 2^29; strides up to 2^22; tokens *
  * stride and slots * channels <= 2^40; (tokens / 64 + sequences) * channels < 2^37.
  *
