@@ -471,8 +471,11 @@ axon_status axon_group_norm(const axon_group_norm_desc* desc, const void* x, con
  *   y     = h
  *
  * (With softplus, A_log = 0 and the complement, a = 1 - z and m = z for the gate z = sigmoid(dt_raw
- * + dt_bias).) Gates, decays and states are fp32, y is rounded once; h is advanced by expm1(log a)
- * where a >= 1/2, so that slow decays lose nothing to the rounding of a.
+ * + dt_bias).) Gates, decays and states are fp32, y is rounded once. Where a >= 1/2, states are handed
+ * on as h + expm1(log a) h, so that slow decays lose nothing to the rounding of a, in a long scan as in many
+ * short ones: from the state that a sequence begins with, every 16 tokens at most, to the one that it hands
+ * back, which its last y shows, and so their gradients. The y between multiply by a (off by 32 2^-24 of h
+ * at most, which does not add up).
  *
  * Layouts: x, dt_raw, in_raw, y (tokens, channels), activation dtype; the rows of x, dt_raw, in_raw
  * and dy may lie x_stride, dt_stride, in_stride, dy_stride elements apart (0 = dense, else at least

@@ -92,10 +92,13 @@ __device__ __forceinline__ float expm1_of(float l2, float a) {
 }
 
 // A state over several tokens, from the sum of their log2 a and their own part: a h + part. Rounding a
-// close to 1 would be the same error for every block of a slow channel, 2^-25 against 1 - a, so that for
-// a >= 1/2 it is h + expm1(log a) h; below, that would lose the part beside a larger h. (Within a
-// block of 16 tokens the roundings of a are 16 2^-25 of h at most, and end with the block.) `carry` holds
-// a, or expm1(log a) with the sign bit set.
+// close to 1 would be the same error for every block of a slow channel, 2^-24 against 1 - a, so that for
+// a >= 1/2 it is h + expm1(log a) h; below, that would lose the part beside a larger h. Whatever outlives
+// a wave's tokens goes this way: what waves and tiles hand on, from the state that a sequence begins with to
+// the one that it hands back (and so for its gradients), else scans of a few tokens that continue one another
+// would lose the decay (300 of 16 tokens at log a = -1e-6 to -1e-7: nine roundings of the state a call, now
+// one). Only the outputs in between multiply by the plain a, up to 16 times from what entered the wave: off by
+// 32 2^-24 of h at most, which ends with the wave. `carry` holds a, or expm1(log a) with the sign bit set.
 __device__ __forceinline__ float carry_of(float l2) {
   const float a = __builtin_amdgcn_exp2f(l2);
   return l2 < -1.0f ? a : __uint_as_float(__float_as_uint(expm1_of(l2, a)) | 0x80000000u);
@@ -431,9 +434,9 @@ __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g
       for (int j = 0; j < P; ++j)
         if (j >= s.count) b[j] = 0.0f;
     }
-    h = h0;
 #pragma unroll
     for (int j = 0; j < P; ++j) h = fmaf(a[j], h, b[j]);
+    if (s.begins) h = advance(carry_of(L), h0, h);
   }
   sh.put(wave, lane, L, h, s.begins);
   __syncthreads();
@@ -442,6 +445,8 @@ __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g
   __syncthreads();
   if (s.count > 0) {
     h = s.begins ? h0 : front.enter(sh.enter[lane]);
+    const float enters = h;
+    const int plain = s.count - (s.ends ? 1 : 0);  // tokens whose output is the plain product
     if (in_range) {
       if (s.opens && g.checkpoints) g.checkpoints[int64_t(s.row) * g.channels + e] = h;
       const rsrc_t y = make_rsrc(static_cast<Act*>(g.y) + int64_t(s.first) * g.channels);
@@ -450,14 +455,17 @@ __global__ __launch_bounds__(64 * WAVES, 6) void linear_tile_kernel(LinearArgs g
 #pragma unroll
         for (int j = 0; j < P; ++j) {
           h = fmaf(a[j], h, b[j]);
-          if (j < s.count) store_row<decltype(past)::value>(static_cast<Act*>(nullptr), y, off, j * step, h);
+          if (j < plain) store_row<decltype(past)::value>(static_cast<Act*>(nullptr), y, off, j * step, h);
         }
       };
       if (g.past) states(Past{});
       else states(Kept{});
-      if (s.ends && g.state_out) {
+      if (s.ends) {
+        // the final state is the last output too
+        const float own = sh.part[wave][lane], last = s.begins ? own : advance(sh.decay[wave][lane], enters, own);
+        store_row<false>(static_cast<Act*>(nullptr), y, off, (s.count - 1) * step, last);
         const int64_t slot = g.out_slots ? table_at(g.out_slots, s.seq) : s.seq;
-        if (slot >= 0 && slot < g.out_count) g.state_out[slot * g.channels + e] = h;
+        if (g.state_out && slot >= 0 && slot < g.out_count) g.state_out[slot * g.channels + e] = last;
       }
     }
   }
@@ -560,10 +568,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
       dy[j] = held ? d[j] : 0.0f;
       h = fmaf(av[j], h, hb[j]);
     }
-    k = k0;
 #pragma unroll
     for (int j = P - 1; j >= 0; --j) k = av[j] * (k + dy[j]);
   }
+  if (s.ends) k = advance(carry_of(L), k0, k);
   sh.put(wave, lane, L, k, s.ends);
   states[wave][lane] = h;
   __syncthreads();
@@ -584,6 +592,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
   float sA = 0.0f, sdt = 0.0f, sin = 0.0f;
   if (s.count > 0) {
     k = s.ends ? k0 : behind.enter(sh.enter[lane]);
+    const float enters = k;
     const int64_t first = int64_t(s.first) * g.channels;
     const rsrc_t dx = make_rsrc(static_cast<Act*>(g.dx) + first);
     const rsrc_t ddt = make_rsrc(static_cast<Act*>(g.ddt_raw) + first);
@@ -610,7 +619,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 3 : 5) void linear_tile_ba
       if (g.past) grads(Past{});
       else grads(Kept{});
     }
-    if (s.begins && g.dstate_in && in_range) g.dstate_in[int64_t(s.seq) * g.channels + e] = k;
+    if (s.begins && g.dstate_in && in_range)
+      g.dstate_in[int64_t(s.seq) * g.channels + e] =
+          s.ends ? sh.part[wave][lane] : advance(sh.decay[wave][lane], enters, sh.part[wave][lane]);
   }
   totals[wave][0][lane] = sA;
   totals[wave][1][lane] = sdt;
