@@ -630,7 +630,8 @@ axon_status axon_causal_conv_step(const axon_conv_shape* shape, const void* x, c
  * (and k_out k) where that is dense, else outputs overlap nothing.
  * Limits: D even, in [2, 256]; R even, in [2, D]; q_heads in [1, 65535], k_heads in [0, 65535]; rows
  * < 2^31; strides up to 2^31; rows * stride <= 2^40. Activations need the alignment of an element
- * only, fp32 and int32 arrays 4-byte, freqs 8-byte. Squares of a head must not sum beyond fp32. */
+ * only, fp32 and int32 arrays 4-byte, freqs 8-byte. Squares of a head must not sum beyond fp32 nor, where eps
+ * is 0, have a mean below its least normal number, 2^-126. */
 typedef struct {
   int64_t rows;
   int64_t q_heads;

@@ -10,7 +10,9 @@
 //
 // Backward, with s_t = dy_t act'(p_t):  dxx_t = sum_k w[k] s_{t+3-k} + what dcache_out has for t,
 // dw[k] = sum_t s_t xx_{t-3+k},  db = sum_t s_t.  A block finds s of the three tokens behind it again, and four
-// blocks join their sums before they leave a part (with the forward pass 8 x 2048 x 7680 262 us).
+// blocks join their sums before they leave a part: fp32 over 256 tokens, 64 bits over the parts (with the forward pass
+// 8 x 2048 x 7680 262 us; 134 registers, three waves a SIMD). fp32, 16384 x 2560: 68 us forward (336 MB), 113 us backward.
+// A step is bound by memory from a large batch on (512 rows x 7680 bf16 22 us, 110 MB; fp32 24 us, 126 MB).
 #include <hip/hip_runtime.h>
 
 #include <cmath>

@@ -14,9 +14,11 @@
 // waves are joined in LDS, and tiles hand on what leaves them in the order in which workgroups start (below). Only
 // then are the states found and stored, so that every value is read and written once.
 //
-// Bound by memory, in this pattern: rows of 128 bytes, three streams in and one out, then four in and three out,
-// reach 4.8 TB/s by themselves, and a wave does not load while it computes. bf16: 16384 x 2560 (336 MB) 82-92 us;
-// packed 32768 x 2560 155-164 us; training of 8 x 2048 x 2560 (336 + 587 MB) 240 us. From the first kernel, one channel
+// Bound by memory and by latency: rows of 128 bytes, four streams in and three out, reach 4.6 to 4.8 TB/s by themselves
+// in this order of workgroups (5.5 where each die takes the same neighbouring groups of every tile, which made the
+// kernels no faster), and a wave does not load while it computes. 16384 x 2560 bf16 (336 MB) 84-92 us, fp32 127 us;
+// packed 32768 x 2560 159-168 us; training of 8 x 2048 x 2560 (336 + 587 MB) 242 us; backward of 16384 x 2560 fp32
+// (1.17 GB) 207-230 us. From the first kernel, one channel
 // of a sequence a lane, of 16384 tokens 21.7 ms. What it took: tiles that hand on; 12 waves of 16 tokens; gates,
 // input scale and what is gated as template arguments, since loads behind branches are waited for at once (101 ->
 // 90 us); plain decays inside a wave; rows at a scalar offset; stores past the caches. Tried and dropped: two channels
@@ -773,10 +775,10 @@ size_t tables_bytes(const Packed& p) {
   return p.starts ? 4 * (2 * (size_t(p.sequences) + 1) + 2 * size_t(p.rows)) : 0;
 }
 
-// Tokens a wave and waves a tile. Forward: 12 waves of 16 tokens, two workgroups a CU (16384 tokens x
-// 2560 bf16 92 us; 8 waves 94 us, 4 waves 147 us). Backward bf16: 4 waves of
-// 16 tokens, three workgroups a CU (8 x 2048 tokens x 2560, with the forward pass, 241 us; 8 waves of 8
-// tokens 264 us); fp32: 8 waves of 8 (3 x 1999 tokens x 1001 79 us against 86 us).
+// Tokens a wave and waves a tile. Forward: 12 waves of 16 tokens, two workgroups a CU (16384 tokens x 2560 bf16 92 us;
+// 8 waves 94 us, 4 waves 147 us). Backward bf16: 4 waves of 16 tokens, three workgroups a CU (8 x 2048 tokens x 2560,
+// with the forward pass, 242 us; 8 waves of 8 tokens 264 us; a softplus gate with a gated input spills 8 to 12 of 168
+// registers); fp32: 8 waves of 8 (3 x 1999 tokens x 1001 79 us against 86 us).
 constexpr int kTokens = 16, kWaves = 12;
 constexpr int kBackTokens = 16, kBackWaves = 4;      // bf16
 constexpr int kBackTokens32 = 8, kBackWaves32 = 8;   // fp32
@@ -788,6 +790,10 @@ constexpr int64_t kStepWide = 1 << 20;
 // Groups of channels up to which all waves of a tile look at the tiles in front, and tiles in a row from which
 // they do. Forward, bf16: 131072 tokens x 64 200 -> 60 us, 16384 x 512 44 -> 37 us, x 1024 48 -> 50 us. Backward:
 // 131072 x 64 581 -> 229 us, 16384 x 1024 109 -> 81 us, x 2560 151 -> 166 us, 16 tiles in a row x 1024 54 -> 58 us.
+// Between: 16384 x 768 forward 47 -> 42 us, x 1280 backward 111 -> 95 us, x 1536 127 -> 118 us; backward, tiles in a row
+// of 8 sequences x 1024, 24 67 -> 69 us, 32 82 -> 81 us, 64 150 -> 133 us. fp32: 131072 x 64 205 -> 63 us and 568 -> 196
+// us, 16384 x 512 forward 49 -> 41 us, x 768 52 -> 51 us, x 1024 56 -> 60 us, backward x 1024 107 -> 94 us, x 1280 111
+// and 111 us, x 1536 143 -> 146 us; 24 tiles in a row x 1024 85 -> 87 us, 32 91 -> 94 us, 64 202 -> 195 us.
 constexpr int kFewGroups = 8, kFewGroupsBack = 16, kLongChain = 32;
 
 // Tiles, and what of the workspace they use.

@@ -7,7 +7,8 @@
 // channels: V of the first and V of the second halves of V pairs, or 2 V channels in order (pairs side
 // by side, or not turned). A wave takes 64 / LANES heads at a time and one row's heads one group after
 // the other, so that its angles are found once a row; where heads are few, the heads of several rows (ROWS).
-// Angles: p freqs / (2 pi) turns in 64 bits, of which only the fraction goes to 32 bits.
+// Angles: p freqs / (2 pi) turns in 64 bits, of which only the fraction goes to 32 bits: off by 2^-26 turns at most, 9e-8
+// rad whatever the position, beside sine and cosine of 32 bits (a product in 64 bits a pair and row is what costs).
 //
 // Bound by memory: 16384 rows of 40 heads of 128 bf16 (336 MB) in 65-68 us, 5.0 TB/s where a copy of that
 // type reaches 5.4. What it took from 81 us: groups of one tensor (pointers and weights the same in all
@@ -28,12 +29,13 @@ namespace axon {
 namespace {
 
 constexpr int kWaves = 4;   // of a workgroup
-constexpr int kFlush = 32;  // rows
+constexpr int kFlush = 32;  // items: rows, or several rows where heads are few
 
 // Backward workgroups that a CU holds at once, as registers allow; as many are started, since a second
 // round of them finds the CUs half empty (16384 rows of 40 heads of 128 bf16 with four a CU 111 us, of which
 // one head group a wave is asked for at a time; three a CU and two groups 120 us, and 150 us with four started.
-// fp32, 8192 rows of 20 heads: 54 us and 48 us, for four spill).
+// fp32, 8192 rows of 20 heads: 54 us and 48 us, for four spill). Of the 128 registers that four leave, one row a wave
+// takes 125 or 127; several rows a wave spill two (pairs apart) or four (side by side).
 template <typename Act>
 constexpr int kBackFit = sizeof(Act) == 2 ? 4 : 3;
 constexpr int kCus = 256;
@@ -169,7 +171,8 @@ __global__ __launch_bounds__(64 * kWaves, BACK ? kBackFit<Act> : 1) void rotate_
       if constexpr (BACK) sq[n].first[i] = sq[n].second[i] = sk[n].first[i] = sk[n].second[i] = 0.0f;
     }
   }
-  // Weight gradients: fp32 over up to kFlush rows a lane, 64 bits beyond.
+  // Weight gradients: fp32 over up to kFlush items a lane, all head groups of their rows, 64 bits beyond; a
+  // workgroup's part is rounded once to fp32.
   __shared__ double part[BACK ? kWaves : 1][2][BACK ? 256 : 1];
   auto flush = [&] {
 #pragma unroll
